@@ -331,6 +331,171 @@ dspark_status dspark_assemble(const dspark_assemble_args* args, void* workspace,
                               void* stream);
 
 /*
+ * The target layer's attention over the assembled batch (no counterpart in the paper, which takes
+ * the target's logits as given): the admitted tokens dspark_assemble laid out run through the
+ * target's layers, and in each layer
+ *   dspark_qk_norm_rope   norms the heads of the queries and keys and rotates them by position,
+ *   dspark_cache_append   writes keys and values into a paged cache of 4-bit codes,
+ *   dspark_cache_attend   attends over that cache, optionally in a sliding window with first
+ *                         tokens that stay visible,
+ * and dspark_cache_read gives cached rows back as values.
+ *
+ * A flat token t belongs to request[t] at position[t] after the ctx_len[request[t]] tokens that the
+ * request's cache holds already, that is at the absolute position ctx_len + position. request[t] < 0
+ * marks padding (dspark_assemble's tail): it is written as zeros, or not at all into the cache.
+ *
+ * The cache. pages holds n_pages pages of page_size tokens (16, 32, 48, .., 256); token p of request
+ * r lives in page table[r][p / page_size], slot p % page_size. A page holds one block for each key /
+ * value head, dspark_cache_block_bytes(page_size, D) = page_size * D * 9 / 8 bytes:
+ *   K codes  [page_size][D / 2]            two channels a byte, the even one in the low half
+ *   V codes  [page_size][D / 2]
+ *   K scales [page_size][D / 32]           fp16
+ *   V scales [page_size / 16][D / 32][16]  fp16
+ * The code u (1 .. 15) of a channel stands for (u - 8) * s, s the scale of its 32 channels:
+ *   s = min(bf16(max|x| * fp32(1/7)), 9344) held in fp16,  u = clamp(x / s rounded to nearest, ties to even, -7, 7) + 8.
+ * A scale keeps 8 significant bits, so that code * scale (11 at most) is exact in fp16 and every
+ * kernel that reads the cache works on the values it stands for without a further rounding. Stored
+ * magnitudes end at 65408 and scales below 2^-24 become 0. NaN counts as 0, an infinity takes the
+ * largest code of its sign without counting for the scale, and DSPARK_ERR_NONFINITE_INPUT is recorded.
+ *
+ * A request id, position or page that is out of range is recorded (DSPARK_ERR_DEVICE_INPUT): the
+ * token's rows are skipped or read as zeros, a key in such a page is not attended.
+ */
+typedef struct {
+    void* pages;              /* [n_pages][Hkv][block], 16-byte aligned */
+    int64_t n_pages;          /* 1 .. 2^31 - 1 */
+    int32_t page_size;        /* a multiple of 16, 16 .. 256 */
+    int32_t Hkv;              /* key / value heads, 1 .. 1024 */
+    int32_t D;                /* head width, a multiple of 32, 32 .. 256 */
+    int32_t R;                /* requests, 1 .. DSPARK_MAX_SLOTS */
+    int32_t table_width;      /* pages a request can hold, >= 1; table_width * page_size < 2^31 */
+    int32_t reserved;         /* 0 */
+    const int32_t* table;     /* [R][table_width] page of each logical page (unused entries: anything) */
+    const int32_t* ctx_len;   /* [R] tokens of each request already in the cache */
+} dspark_cache;
+
+/* Bytes of one head's block of a page, 0 for sizes the cache does not take. */
+size_t dspark_cache_block_bytes(int32_t page_size, int32_t D);
+
+/*
+ * dspark_qk_norm_rope -- for every token and every head of q and k (width D, fp32 statistics):
+ *   y = x / sqrt(sum(x^2) / D + eps) * gain          (norm = 1; y = x for norm = 0)
+ *   with the angle phi_i = 2 pi * freq[i] * 2^-64 * position, for the pairs i < rot / 2
+ *   (y_a, y_b) -> (y_a cos phi_i - y_b sin phi_i, y_a sin phi_i + y_b cos phi_i),
+ *   (a, b) = (i, i + rot / 2), or (2i, 2i + 1) when interleaved; channels from rot on are not turned.
+ * freq[i] is the turn of pair i per position as a 64-bit fraction of a whole turn, so that far
+ * positions lose nothing: whole turns leave the product by integer arithmetic.
+ */
+typedef struct {
+    uint32_t struct_size;
+    int32_t T;                 /* flat tokens, >= 0 */
+    int32_t Hq, Hkv;           /* heads, 1 .. 1024 */
+    int32_t D;                 /* head width, even, 2 .. 1024 */
+    int32_t rot;               /* rotated channels, even, 0 .. D */
+    int32_t dtype;             /* element type of q, k and the outputs */
+    int32_t norm;              /* 1: norm by head, 0: rotate only */
+    int32_t interleaved;       /* pairs (2i, 2i + 1) instead of (i, i + rot / 2) */
+    int32_t R;                 /* requests (with request) */
+    float eps;                 /* >= 0 */
+    int32_t reserved;          /* 0 */
+    const void* q;             /* [T][Hq][D], the last axis contiguous */
+    const void* k;             /* [T][Hkv][D] */
+    int64_t q_token_stride, q_head_stride;   /* in elements, so that q and k may be parts of one projection's rows */
+    int64_t k_token_stride, k_head_stride;
+    const float* q_gain;       /* [D] or NULL = 1 */
+    const float* k_gain;       /* [D] or NULL = 1 */
+    const uint64_t* freq;      /* [rot / 2] */
+    const int32_t* position;   /* [T] */
+    const int32_t* request;    /* [T] or NULL: no padding, ctx_len not added */
+    const int32_t* ctx_len;    /* [R] or NULL: not added to position */
+    void* q_out;               /* out [T][Hq][D] contiguous */
+    void* k_out;               /* out [T][Hkv][D] contiguous */
+} dspark_qk_norm_rope_args;
+
+dspark_status dspark_qk_norm_rope_workspace_size(const dspark_qk_norm_rope_args* args, size_t* bytes);
+dspark_status dspark_qk_norm_rope(const dspark_qk_norm_rope_args* args, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* dspark_cache_append -- write the key and value rows of every token into the cache. Two tokens of
+ * one call must not share a (request, position). Pages are the caller's: a page that two requests
+ * share must not be written. */
+typedef struct {
+    uint32_t struct_size;
+    int32_t T;                 /* flat tokens, >= 0 */
+    int32_t dtype;             /* element type of k and v */
+    int32_t reserved;          /* 0 */
+    dspark_cache cache;
+    const void* k;             /* [T][Hkv][D], the last axis contiguous */
+    const void* v;
+    int64_t k_token_stride, k_head_stride;   /* in elements */
+    int64_t v_token_stride, v_head_stride;
+    const int32_t* request;    /* [T] */
+    const int32_t* position;   /* [T] */
+} dspark_cache_append_args;
+
+dspark_status dspark_cache_append_workspace_size(const dspark_cache_append_args* args, size_t* bytes);
+dspark_status dspark_cache_append(const dspark_cache_append_args* args, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* dspark_cache_read -- the cached key and value rows of every token, as the values their codes stand
+ * for, rounded once to the output type. */
+typedef struct {
+    uint32_t struct_size;
+    int32_t T;
+    int32_t dtype;             /* element type of k_out and v_out */
+    int32_t reserved;          /* 0 */
+    dspark_cache cache;
+    const int32_t* request;    /* [T] */
+    const int32_t* position;   /* [T] */
+    void* k_out;               /* out [T][Hkv][D] contiguous */
+    void* v_out;
+} dspark_cache_read_args;
+
+dspark_status dspark_cache_read_workspace_size(const dspark_cache_read_args* args, size_t* bytes);
+dspark_status dspark_cache_read(const dspark_cache_read_args* args, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * dspark_cache_attend -- attention of the flat batch over the cache. Request r has the flat rows
+ * offsets[r] .. offsets[r+1]-1 (dspark_assemble's offsets); its row j is the token at position
+ * p = ctx_len[r] + j, whose own key has been appended. Query head h reads key / value head
+ * h / (Hq / Hkv). Over the visible keys i, those with i <= p and, with a window, i > p - window or
+ * i < sinks:
+ *   z_i = scale * q . k_i,  out = sum_i exp(z_i) v_i / sum_i exp(z_i),  lse = log sum_i exp(z_i).
+ * A row with no visible key (every page of it out of range) and the rows outside
+ * offsets[0] .. offsets[R] give out = 0, lse = -inf. A row whose q holds a NaN or an infinity gives
+ * NaN and DSPARK_ERR_NONFINITE_INPUT; the other rows are not touched by it.
+ * Statistics and sums are fp32. On the tensor-core path (D = 64 or 128) a row of q enters the
+ * products as fp16 after a scaling by a power of two (exact for bf16 unless an element is 2^-25 of
+ * the row's largest; two fp16 terms for fp32) and the weights exp(z - max) as fp16 (two terms for
+ * fp32); elsewhere a CUDA-core kernel in fp32 runs.
+ * Decreasing offsets or more than max_q rows of one request are recorded (DSPARK_ERR_DEVICE_INPUT):
+ * that request's rows are not computed, or none past max_q.
+ */
+typedef struct {
+    uint32_t struct_size;
+    int32_t T;                 /* flat rows of q and out, >= 0 */
+    int32_t Hq;                /* query heads, a multiple of cache.Hkv */
+    int32_t dtype;             /* element type of q and out */
+    int32_t path;              /* DSPARK_PATH_AUTO, _CUDA_CORE or _TENSOR_CORE */
+    int32_t max_q;             /* most rows of one request (gamma_max + 1 in a verify pass), >= 1 */
+    int32_t window;            /* keys in the sliding window, 0 = no window */
+    int32_t sinks;             /* first tokens that stay visible beside the window, >= 0 */
+    float scale;               /* > 0 */
+    int32_t reserved;          /* 0 */
+    dspark_cache cache;
+    const void* q;             /* [T][Hq][D], the last axis contiguous */
+    int64_t q_token_stride, q_head_stride;   /* in elements */
+    const int32_t* offsets;    /* [R + 1] */
+    void* out;                 /* out [T][Hq][D] contiguous */
+    float* lse;                /* out [T][Hq] or NULL */
+} dspark_cache_attend_args;
+
+dspark_status dspark_cache_attend_workspace_size(const dspark_cache_attend_args* args, size_t* bytes);
+dspark_status dspark_cache_attend(const dspark_cache_attend_args* args, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
  * Launch accounting and timing (measurement support, not part of the method).
  *
  * dspark_launch_count: number of kernels this library has launched in this
@@ -356,7 +521,12 @@ enum {
     DSPARK_KERNEL_ASSEMBLE = 8,
     DSPARK_KERNEL_RNN_STEP = 9,      /* RNN head: the per-step state update */
     DSPARK_KERNEL_RNN_HIDDEN = 10,   /* RNN head: the h part of the projection, every position, once per call */
-    DSPARK_KERNEL_DRAFT_LOOP = 11    /* the resident path's one launch: every draft step and its commit */
+    DSPARK_KERNEL_DRAFT_LOOP = 11,   /* the resident path's one launch: every draft step and its commit */
+    DSPARK_KERNEL_QK_NORM_ROPE = 12,
+    DSPARK_KERNEL_CACHE_APPEND = 13,
+    DSPARK_KERNEL_CACHE_READ = 14,
+    DSPARK_KERNEL_CACHE_ATTEND = 15,
+    DSPARK_KERNEL_CACHE_MERGE = 16   /* joins the parts of rows whose keys were split over CTAs */
 };
 
 typedef struct {

@@ -10,10 +10,18 @@ Calls (same names as the C ABI):
   sample_block  Markov-head serial sampling, confidence head, survival products
   schedule      hardware-aware prefix scheduler (sync / async capacity / full scan)
   verify        rejection-sampling verification, residual or bonus token
+  assemble      the admitted prefixes as one flat token stream
+and, for the target layers that stream runs through (verify_pass.py puts them together):
+  qk_norm_rope  norms of the query and key heads and their rotation by position
+  cache_append  key and value rows into a paged cache of 4-bit codes
+  cache_read    cached rows back as values
+  cache_attend  attention over that cache, with an optional sliding window and first tokens
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import math
 import os
 
 import torch
@@ -82,16 +90,65 @@ class AssembleArgs(C.Structure):
     ]
 
 
+class Cache(C.Structure):
+    _fields_ = [("pages", _vp), ("n_pages", C.c_int64), ("page_size", C.c_int32), ("Hkv", C.c_int32),
+                ("D", C.c_int32), ("R", C.c_int32), ("table_width", C.c_int32), ("reserved", C.c_int32),
+                ("table", _vp), ("ctx_len", _vp)]
+
+
+class QkNormRopeArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("T", C.c_int32), ("Hq", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32),
+        ("rot", C.c_int32), ("dtype", C.c_int32), ("norm", C.c_int32), ("interleaved", C.c_int32),
+        ("R", C.c_int32), ("eps", C.c_float), ("reserved", C.c_int32), ("q", _vp), ("k", _vp),
+        ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64),
+        ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+        ("q_gain", _vp), ("k_gain", _vp), ("freq", _vp), ("position", _vp), ("request", _vp), ("ctx_len", _vp),
+        ("q_out", _vp), ("k_out", _vp),
+    ]
+
+
+class CacheAppendArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("T", C.c_int32), ("dtype", C.c_int32), ("reserved", C.c_int32),
+        ("cache", Cache), ("k", _vp), ("v", _vp),
+        ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+        ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64),
+        ("request", _vp), ("position", _vp),
+    ]
+
+
+class CacheReadArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("T", C.c_int32), ("dtype", C.c_int32), ("reserved", C.c_int32),
+        ("cache", Cache), ("request", _vp), ("position", _vp), ("k_out", _vp), ("v_out", _vp),
+    ]
+
+
+class CacheAttendArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("T", C.c_int32), ("Hq", C.c_int32), ("dtype", C.c_int32),
+        ("path", C.c_int32), ("max_q", C.c_int32), ("window", C.c_int32), ("sinks", C.c_int32),
+        ("scale", C.c_float), ("reserved", C.c_int32), ("cache", Cache), ("q", _vp),
+        ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64), ("offsets", _vp), ("out", _vp), ("lse", _vp),
+    ]
+
+
 EXPORTS = ("dspark_sample_workspace_size", "dspark_sample_block", "dspark_schedule_workspace_size",
            "dspark_schedule", "dspark_verify_workspace_size", "dspark_verify", "dspark_check",
            "dspark_status_string", "dspark_abi_version", "dspark_launch_count", "dspark_time_kernel",
            "dspark_last_error", "dspark_sample_path", "dspark_sample_block_static", "dspark_check_static",
            "dspark_set_wait_limit",
-           "dspark_assemble_workspace_size", "dspark_assemble")
+           "dspark_assemble_workspace_size", "dspark_assemble", "dspark_cache_block_bytes",
+           "dspark_qk_norm_rope_workspace_size", "dspark_qk_norm_rope",
+           "dspark_cache_append_workspace_size", "dspark_cache_append",
+           "dspark_cache_read_workspace_size", "dspark_cache_read",
+           "dspark_cache_attend_workspace_size", "dspark_cache_attend")
 
 KERNELS = {"draft_setup": 0, "draft_stats": 1, "draft_commit": 2, "schedule": 3, "verify_rows": 4,
            "verify_decide": 5, "residual_stats": 6, "residual_pick": 7, "assemble": 8, "rnn_step": 9,
-           "rnn_hidden": 10, "draft_loop": 11}
+           "rnn_hidden": 10, "draft_loop": 11, "qk_norm_rope": 12, "cache_append": 13, "cache_read": 14,
+           "cache_attend": 15, "cache_merge": 16}
 
 
 class EventPair(C.Structure):
@@ -125,10 +182,22 @@ def lib():
                            ("dspark_verify", [C.POINTER(VerifyArgs), _vp, C.c_size_t, _vp]),
                            ("dspark_assemble_workspace_size", [C.POINTER(AssembleArgs), C.POINTER(C.c_size_t)]),
                            ("dspark_assemble", [C.POINTER(AssembleArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_qk_norm_rope_workspace_size", [C.POINTER(QkNormRopeArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_qk_norm_rope", [C.POINTER(QkNormRopeArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_cache_append_workspace_size",
+                            [C.POINTER(CacheAppendArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_cache_append", [C.POINTER(CacheAppendArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_cache_read_workspace_size", [C.POINTER(CacheReadArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_cache_read", [C.POINTER(CacheReadArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_cache_attend_workspace_size",
+                            [C.POINTER(CacheAttendArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_cache_attend", [C.POINTER(CacheAttendArgs), _vp, C.c_size_t, _vp]),
                            ("dspark_check", [_vp, _vp])):
             f = getattr(L, name)
             f.argtypes = argt
             f.restype = C.c_int32
+        L.dspark_cache_block_bytes.argtypes = [C.c_int32, C.c_int32]
+        L.dspark_cache_block_bytes.restype = C.c_size_t
         L.dspark_status_string.argtypes = [C.c_int32]
         L.dspark_status_string.restype = C.c_char_p
         L.dspark_abi_version.argtypes = []
@@ -459,6 +528,227 @@ def verify(target, U, E, W, anchor, tokens, draft_lse, draft_logit, keep, temper
                          gamma=gamma, bias_first=bias_first, path=path, out=out, a_rows=a_rows)
     ws = _workspace("dspark_verify_workspace_size", a, workspace, U.device)
     _call("dspark_verify", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    out["workspace"] = ws
+    return out
+
+
+# ----------------------------------------------------------------- the target layer's attention
+
+CACHE_GROUP = 32     # channels that share a scale
+
+
+def _strided(t, name, dtype=None, width=None):
+    """Rows [T][heads][D] whose last axis is contiguous; returns (token stride, head stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must have shape [tokens][heads][width], got %s" % (name, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if width is not None and t.shape[2] != width:
+        raise ValueError("%s must have heads of width %d, got %d" % (name, width, t.shape[2]))
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError("the last axis of %s must be contiguous" % name)
+    return st[0], st[1]
+
+
+def _on(stream):
+    """Allocate what a call on `stream` uses on that stream, so that the allocator orders its reuse."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _status_workspace(workspace, device, stream):
+    """The workspace of a call that keeps no more there than its status word."""
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.zeros(256, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def rope_frequencies(rot, base=10000.0, *, device="cuda"):
+    """The turn per position of each of the rot / 2 pairs, base^(-2i / rot) / 2 pi, as 64-bit fractions of a
+    whole turn (int64 tensor): what qk_norm_rope takes. Scaled frequencies (position interpolation and
+    the like) are made the same way: int(turns * 2**64)."""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even, got %d" % rot)
+    turns = [base ** (-2.0 * i / rot) / (2.0 * math.pi) for i in range(rot // 2)]
+    f = [int(t * 2.0 ** 64) % (1 << 64) for t in turns]
+    return torch.tensor([x - (1 << 64) if x >> 63 else x for x in f], dtype=torch.int64, device=device)
+
+
+def qk_norm_rope_args(q, k, freq, position, *, request=None, ctx_len=None, q_gain=None, k_gain=None, eps=1e-6,
+                      norm=True, interleaved=False, out=None):
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dt = q.dtype
+    a = QkNormRopeArgs()
+    a.q_token_stride, a.q_head_stride = _strided(q, "q")
+    a.k_token_stride, a.k_head_stride = _strided(k, "k", dt, D)
+    if k.shape[0] != T:
+        raise ValueError("q has %d tokens, k %d" % (T, k.shape[0]))
+    rot = 0
+    if freq is not None:
+        _dev(freq, "freq", torch.int64)
+        rot = 2 * freq.numel()
+    _dev(position, "position", torch.int32, (T,))
+    _dev(request, "request", torch.int32, (T,))
+    _dev(ctx_len, "ctx_len", torch.int32)
+    _dev(q_gain, "q_gain", torch.float32, (D,))
+    _dev(k_gain, "k_gain", torch.float32, (D,))
+    if request is not None and ctx_len is None:
+        raise ValueError("request needs ctx_len, whose length is the number of requests")
+    if out is None:
+        out = {"q": torch.empty((T, Hq, D), dtype=dt, device=q.device),
+               "k": torch.empty((T, Hkv, D), dtype=dt, device=q.device)}
+    else:
+        _dev(out["q"], "out q", dt, (T, Hq, D))
+        _dev(out["k"], "out k", dt, (T, Hkv, D))
+    a.struct_size = C.sizeof(QkNormRopeArgs)
+    a.T, a.Hq, a.Hkv, a.D, a.rot, a.dtype = T, Hq, Hkv, D, rot, _dtype_code(q)
+    a.norm, a.interleaved, a.eps = int(bool(norm)), int(bool(interleaved)), float(eps)
+    a.R = 0 if ctx_len is None else ctx_len.numel()
+    a.q, a.k, a.q_gain, a.k_gain, a.freq = _ptr(q), _ptr(k), _ptr(q_gain), _ptr(k_gain), _ptr(freq)
+    a.position, a.request, a.ctx_len = _ptr(position), _ptr(request), _ptr(ctx_len)
+    a.q_out, a.k_out = _ptr(out["q"]), _ptr(out["k"])
+    return a, out
+
+
+def qk_norm_rope(q, k, freq, position, *, request=None, ctx_len=None, q_gain=None, k_gain=None, eps=1e-6,
+                 norm=True, interleaved=False, out=None, workspace=None, stream=None):
+    """dspark_qk_norm_rope: q [T][Hq][D] and k [T][Hkv][D] (views into one projection's rows will do) normed by
+    head and rotated; returns {"q", "k"}. freq: rope_frequencies(rot), None for no rotation. position: int32
+    [T]; with request [T] and ctx_len [R] the tokens of a request follow its ctx_len tokens, and rows with
+    request < 0 are written as zeros."""
+    with _on(stream):
+        a, out = qk_norm_rope_args(q, k, freq, position, request=request, ctx_len=ctx_len, q_gain=q_gain,
+                                   k_gain=k_gain, eps=eps, norm=norm, interleaved=interleaved, out=out)
+    ws = _status_workspace(workspace, q.device, stream)
+    _call("dspark_qk_norm_rope", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    out["workspace"] = ws
+    return out
+
+
+def cache_block_bytes(page_size, D) -> int:
+    """Bytes of one head's block of a page (DsparkError for sizes the cache does not take)."""
+    n = int(lib().dspark_cache_block_bytes(int(page_size), int(D)))
+    if n == 0:
+        raise DsparkError("dspark_cache_block_bytes", 2, "page_size %d, D %d" % (page_size, D))
+    return n
+
+
+def cache_pool(n_pages, Hkv, page_size, D, *, device="cuda"):
+    """The pages of a cache: uint8 [n_pages][Hkv][block]."""
+    return torch.zeros((n_pages, Hkv, cache_block_bytes(page_size, D)), dtype=torch.uint8, device=device)
+
+
+def cache_view(pool, table, ctx_len, D):
+    """The C struct of a cache: pool (cache_pool), table [R][width] int32, ctx_len [R] int32."""
+    _dev(pool, "pool", torch.uint8)
+    _dev(table, "table", torch.int32)
+    if pool.dim() != 3 or table.dim() != 2:
+        raise ValueError("pool must be [pages][heads][block] and table [requests][pages]")
+    R, width = table.shape
+    _dev(ctx_len, "ctx_len", torch.int32, (R,))
+    n_pages, Hkv, block = pool.shape
+    page_size = block * 8 // (9 * D) if D > 0 else 0
+    if page_size * D * 9 != block * 8:
+        raise ValueError("pool blocks of %d bytes hold no whole tokens of width %d" % (block, D))
+    c = Cache()
+    c.pages, c.n_pages, c.page_size, c.Hkv, c.D = _ptr(pool), n_pages, page_size, Hkv, D
+    c.R, c.table_width, c.table, c.ctx_len = R, width, _ptr(table), _ptr(ctx_len)
+    return c
+
+
+def cache_append_args(k, v, pool, table, request, position, ctx_len):
+    a = CacheAppendArgs()
+    T, Hkv, D = k.shape
+    a.k_token_stride, a.k_head_stride = _strided(k, "k")
+    a.v_token_stride, a.v_head_stride = _strided(v, "v", k.dtype, D)
+    a.cache = cache_view(pool, table, ctx_len, D)
+    if tuple(v.shape) != (T, Hkv, D) or pool.shape[1] != Hkv:
+        raise ValueError("k %s, v %s and the pool's %d heads do not match" % (tuple(k.shape), tuple(v.shape),
+                                                                           pool.shape[1]))
+    _dev(request, "request", torch.int32, (T,))
+    _dev(position, "position", torch.int32, (T,))
+    a.struct_size = C.sizeof(CacheAppendArgs)
+    a.T, a.dtype = T, _dtype_code(k)
+    a.k, a.v, a.request, a.position = _ptr(k), _ptr(v), _ptr(request), _ptr(position)
+    return a
+
+
+def cache_append(k, v, pool, table, request, position, ctx_len, *, workspace=None, stream=None):
+    """dspark_cache_append: the rows k, v [T][Hkv][D] of the tokens (request, position) into the pages of the
+    cache, at position ctx_len[request] + position. Returns {"workspace"}."""
+    a = cache_append_args(k, v, pool, table, request, position, ctx_len)
+    ws = _status_workspace(workspace, k.device, stream)
+    _call("dspark_cache_append", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    return {"workspace": ws}
+
+
+def cache_read_args(pool, table, request, position, ctx_len, *, D, dtype=torch.bfloat16, out=None):
+    a = CacheReadArgs()
+    a.cache = cache_view(pool, table, ctx_len, D)
+    T, Hkv = request.numel(), pool.shape[1]
+    _dev(request, "request", torch.int32, (T,))
+    _dev(position, "position", torch.int32, (T,))
+    if out is None:
+        out = {n: torch.empty((T, Hkv, D), dtype=dtype, device=pool.device) for n in ("k", "v")}
+    else:
+        for n in ("k", "v"):
+            _dev(out[n], "out " + n, dtype, (T, Hkv, D))
+    a.struct_size = C.sizeof(CacheReadArgs)
+    a.T, a.dtype = T, _dtype_code(out["k"])
+    a.request, a.position, a.k_out, a.v_out = _ptr(request), _ptr(position), _ptr(out["k"]), _ptr(out["v"])
+    return a, out
+
+
+def cache_read(pool, table, request, position, ctx_len, *, D, dtype=torch.bfloat16, out=None, workspace=None,
+               stream=None):
+    """dspark_cache_read: the cached rows of the tokens (request, position) as values; returns {"k", "v"}
+    [T][Hkv][D], zeros where request < 0."""
+    with _on(stream):
+        a, out = cache_read_args(pool, table, request, position, ctx_len, D=D, dtype=dtype, out=out)
+    ws = _status_workspace(workspace, pool.device, stream)
+    _call("dspark_cache_read", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    out["workspace"] = ws
+    return out
+
+
+def cache_attend_args(q, pool, table, offsets, ctx_len, *, scale=None, window=0, sinks=0, max_q=None,
+                      path=PATH_AUTO, lse=True, out=None):
+    a = CacheAttendArgs()
+    T, Hq, D = q.shape
+    a.q_token_stride, a.q_head_stride = _strided(q, "q")
+    a.cache = cache_view(pool, table, ctx_len, D)
+    _dev(offsets, "offsets", torch.int32, (table.shape[0] + 1,))
+    if out is None:
+        out = {"out": torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)}
+        if lse:
+            out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _dev(out["out"], "out", q.dtype, (T, Hq, D))
+        _dev(out.get("lse"), "lse", torch.float32, (T, Hq))
+    a.struct_size = C.sizeof(CacheAttendArgs)
+    a.T, a.Hq, a.dtype, a.path = T, Hq, _dtype_code(q), int(path)
+    a.max_q = max(1, T) if max_q is None else int(max_q)
+    a.window, a.sinks = int(window), int(sinks)
+    a.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    a.q, a.offsets, a.out, a.lse = _ptr(q), _ptr(offsets), _ptr(out["out"]), _ptr(out.get("lse"))
+    return a, out
+
+
+def cache_attend(q, pool, table, offsets, ctx_len, *, scale=None, window=0, sinks=0, max_q=None, path=PATH_AUTO,
+                 lse=True, out=None, workspace=None, stream=None):
+    """dspark_cache_attend: q [T][Hq][D], the flat rows of all requests (offsets [R + 1]), over the cache that
+    already holds their own keys; returns {"out"} [T][Hq][D] and, unless lse=False, {"lse"} [T][Hq]. scale
+    defaults to 1 / sqrt(D), max_q (most rows of one request) to T; say it where it is known, the kernels
+    are chosen by it."""
+    with _on(stream):
+        a, out = cache_attend_args(q, pool, table, offsets, ctx_len, scale=scale, window=window, sinks=sinks,
+                                   max_q=max_q, path=path, lse=lse, out=out)
+        ws = _workspace("dspark_cache_attend_workspace_size", a, workspace, q.device)
+    _call("dspark_cache_attend", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
     out["workspace"] = ws
     return out
 

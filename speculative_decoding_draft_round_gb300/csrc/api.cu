@@ -1,11 +1,13 @@
 // api.cu -- the C ABI of libdspark (include/dspark.h): argument validation,
 // workspace layout and the launch sequence of each call. Every step of the
 // round runs in this library's kernels; nothing here computes on the host.
+#include <float.h>
 #include <stdio.h>
 #include <string.h>
 
 #include <atomic>
 
+#include "cache.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -33,8 +35,9 @@ const char* kernel_name(int kernel)
 {
     static const char* names[] = {"draft_setup", "draft_stats", "draft_commit", "schedule",
                                   "verify_rows", "verify_decide", "residual_stats", "residual_pick",
-                                  "assemble", "rnn_step", "rnn_hidden", "draft_loop"};
-    return kernel >= 0 && kernel <= DSPARK_KERNEL_DRAFT_LOOP ? names[kernel] : "?";
+                                  "assemble", "rnn_step", "rnn_hidden", "draft_loop",
+                                  "qk_norm_rope", "cache_append", "cache_read", "cache_attend", "cache_merge"};
+    return kernel >= 0 && kernel <= DSPARK_KERNEL_CACHE_MERGE ? names[kernel] : "?";
 }
 
 thread_local char g_last_error[256] = "no error";
@@ -218,6 +221,106 @@ dspark_status check_schedule(const dspark_schedule_args* a)
     if (!a->surv || !a->sps || !a->keep || !a->stats) return DSPARK_ERR_INVALID_ARGUMENT;
     if (a->mode == DSPARK_SCHED_ASYNC_CAPACITY && !a->surv_capacity) return DSPARK_ERR_INVALID_ARGUMENT;
     return DSPARK_OK;
+}
+
+// ------------------------------------------------------------ the target layer's attention
+
+dspark_status check_rope(const dspark_qk_norm_rope_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_qk_norm_rope_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq > 1024 || a->Hkv > 1024) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->D < 2 || a->D > 1024 || a->D % 2 || a->rot < 0 || a->rot > a->D || a->rot % 2)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    if ((a->norm | 1) != 1 || (a->interleaved | 1) != 1 || a->reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (!(a->eps >= 0.f) || a->eps > FLT_MAX) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->request && a->R < 1) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->ctx_len && !a->request) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T == 0) return DSPARK_OK;
+    if (!a->q || !a->k || !a->q_out || !a->k_out || !a->position || (a->rot > 0 && !a->freq))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+dspark_status check_cache(const dspark_cache& c)
+{
+    if (!c.pages || !c.table || !c.ctx_len || c.reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (reinterpret_cast<uintptr_t>(c.pages) % 16) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (c.n_pages < 1 || c.n_pages > INT32_MAX || c.table_width < 1 || c.Hkv < 1 || c.R < 1)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (!dspark_cache_block_bytes(c.page_size, c.D)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (c.R > DSPARK_MAX_SLOTS || c.Hkv > 1024) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if ((long long)c.table_width * c.page_size > INT32_MAX) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    return DSPARK_OK;
+}
+
+// One thread takes 8 channels of a key or value row: the grid has to fit
+bool rows_fit(int T, const dspark_cache& c) { return (long long)T * 2 * c.Hkv * (c.D / 8) < (1ll << 38); }
+
+dspark_status check_append(const dspark_cache_append_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_cache_append_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T < 0 || a->reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    const dspark_status st = check_cache(a->cache);
+    if (st != DSPARK_OK) return st;
+    if (!rows_fit(a->T, a->cache)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (a->T > 0 && (!a->k || !a->v || !a->request || !a->position)) return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+dspark_status check_read(const dspark_cache_read_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_cache_read_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T < 0 || a->reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    const dspark_status st = check_cache(a->cache);
+    if (st != DSPARK_OK) return st;
+    if (!rows_fit(a->T, a->cache)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (a->T > 0 && (!a->k_out || !a->v_out || !a->request || !a->position)) return DSPARK_ERR_INVALID_ARGUMENT;
+    // 16-byte stores
+    if (reinterpret_cast<uintptr_t>(a->k_out) % 16 || reinterpret_cast<uintptr_t>(a->v_out) % 16)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+dspark_status check_attend(const dspark_cache_attend_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_cache_attend_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T < 0 || a->Hq < 1 || a->max_q < 1 || a->window < 0 || a->sinks < 0 || a->reserved != 0)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->path < DSPARK_PATH_AUTO || a->path > DSPARK_PATH_TENSOR_CORE) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (!(a->scale > 0.f) || a->scale > FLT_MAX / 2) return DSPARK_ERR_INVALID_ARGUMENT;
+    const dspark_status st = check_cache(a->cache);
+    if (st != DSPARK_OK) return st;
+    if (a->Hq % a->cache.Hkv) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->Hq / a->cache.Hkv > 1024) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (a->T > 0 && (!a->q || !a->offsets || !a->out)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (reinterpret_cast<uintptr_t>(a->out) % 16) return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+AttendParams attend_params(const dspark_cache_attend_args* a)
+{
+    AttendParams p;
+    memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.Hq = a->Hq;
+    p.G = a->Hq / a->cache.Hkv;
+    p.dtype = a->dtype;
+    p.max_q = a->max_q;
+    p.window = a->window;
+    p.sinks = a->sinks;
+    p.scale = a->scale;
+    p.c = a->cache;
+    p.q = a->q;
+    p.q_ts = a->q_token_stride;
+    p.q_hs = a->q_head_stride;
+    p.offsets = a->offsets;
+    p.out = a->out;
+    p.lse = a->lse;
+    return p;
 }
 
 template <typename T>
@@ -509,6 +612,145 @@ dspark_status dspark_verify(const dspark_verify_args* a, void* ws, size_t ws_byt
     return cuda_status(e);
 }
 
+size_t dspark_cache_block_bytes(int32_t page_size, int32_t D)
+{
+    if (page_size < 16 || page_size > 256 || page_size % 16 || D < 32 || D > 256 || D % 32) return 0;
+    return cache_block(page_size, D).bytes;
+}
+
+dspark_status dspark_qk_norm_rope_workspace_size(const dspark_qk_norm_rope_args* a, size_t* bytes)
+{
+    const dspark_status st = check_rope(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_qk_norm_rope(const dspark_qk_norm_rope_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_rope(a);
+    if (st != DSPARK_OK) return st;
+    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    if (a->T == 0) return DSPARK_OK;
+    RopeParams p;
+    p.T = a->T;
+    p.Hq = a->Hq;
+    p.Hkv = a->Hkv;
+    p.D = a->D;
+    p.rot = a->rot;
+    p.dtype = a->dtype;
+    p.norm = a->norm;
+    p.interleaved = a->interleaved;
+    p.R = a->R;
+    p.eps = a->eps;
+    p.q = a->q;
+    p.k = a->k;
+    p.q_ts = a->q_token_stride;
+    p.q_hs = a->q_head_stride;
+    p.k_ts = a->k_token_stride;
+    p.k_hs = a->k_head_stride;
+    p.q_gain = a->q_gain;
+    p.k_gain = a->k_gain;
+    p.freq = a->freq;
+    p.position = a->position;
+    p.request = a->request;
+    p.ctx_len = a->ctx_len;
+    p.q_out = a->q_out;
+    p.k_out = a->k_out;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_QK_NORM_ROPE, s, [&] { return launch_qk_norm_rope(p, s); }));
+}
+
+dspark_status dspark_cache_append_workspace_size(const dspark_cache_append_args* a, size_t* bytes)
+{
+    const dspark_status st = check_append(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_cache_append(const dspark_cache_append_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_append(a);
+    if (st != DSPARK_OK) return st;
+    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    if (a->T == 0) return DSPARK_OK;
+    CacheRowsParams p;
+    memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.dtype = a->dtype;
+    p.c = a->cache;
+    p.k = a->k;
+    p.v = a->v;
+    p.k_ts = a->k_token_stride;
+    p.k_hs = a->k_head_stride;
+    p.v_ts = a->v_token_stride;
+    p.v_hs = a->v_head_stride;
+    p.request = a->request;
+    p.position = a->position;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_CACHE_APPEND, s, [&] { return launch_cache_append(p, s); }));
+}
+
+dspark_status dspark_cache_read_workspace_size(const dspark_cache_read_args* a, size_t* bytes)
+{
+    const dspark_status st = check_read(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_cache_read(const dspark_cache_read_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_read(a);
+    if (st != DSPARK_OK) return st;
+    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    if (a->T == 0) return DSPARK_OK;
+    CacheRowsParams p;
+    memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.dtype = a->dtype;
+    p.c = a->cache;
+    p.request = a->request;
+    p.position = a->position;
+    p.k_out = a->k_out;
+    p.v_out = a->v_out;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_CACHE_READ, s, [&] { return launch_cache_read(p, s); }));
+}
+
+dspark_status dspark_cache_attend_workspace_size(const dspark_cache_attend_args* a, size_t* bytes)
+{
+    const dspark_status st = check_attend(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_cache_attend(const dspark_cache_attend_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_attend(a);
+    if (st != DSPARK_OK) return st;
+    if (a->path == DSPARK_PATH_TENSOR_CORE) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    AttendParams p = attend_params(a);
+    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    p.status = at<int>(ws, 0);
+    if (a->T == 0) return DSPARK_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_simt(p, s); }));
+}
+
 const char* dspark_last_error(void) { return g_last_error; }
 
 uint64_t dspark_set_wait_limit(uint64_t ns)
@@ -524,7 +766,7 @@ dspark_status dspark_time_kernel(int32_t kernel, dspark_event_pair* events, int3
         g_timer = KernelTimer();
         return DSPARK_OK;
     }
-    if (kernel > DSPARK_KERNEL_DRAFT_LOOP || !events || capacity < 0 || !count) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (kernel > DSPARK_KERNEL_CACHE_MERGE || !events || capacity < 0 || !count) return DSPARK_ERR_INVALID_ARGUMENT;
     g_timer.kernel = kernel;
     g_timer.events = events;
     g_timer.capacity = capacity;

@@ -117,6 +117,51 @@ struct AssembleParams {
     int* status;
 };
 
+// Head norms and rotation (dspark_qk_norm_rope).
+struct RopeParams {
+    int T, Hq, Hkv, D, rot, dtype, norm, interleaved, R;
+    float eps;
+    const void* q;
+    const void* k;
+    int64_t q_ts, q_hs, k_ts, k_hs;   // token and head strides, elements
+    const float* q_gain;
+    const float* k_gain;
+    const uint64_t* freq;
+    const int32_t* position;
+    const int32_t* request;
+    const int32_t* ctx_len;
+    void* q_out;
+    void* k_out;
+    int* status;
+};
+
+// Rows into and out of the 4-bit cache (dspark_cache_append, dspark_cache_read).
+struct CacheRowsParams {
+    int T, dtype;
+    dspark_cache c;
+    const void* k;                    // append: rows in
+    const void* v;
+    int64_t k_ts, k_hs, v_ts, v_hs;
+    const int32_t* request;
+    const int32_t* position;
+    void* k_out;                      // read: rows out
+    void* v_out;
+    int* status;
+};
+
+// Attention over the 4-bit cache (dspark_cache_attend).
+struct AttendParams {
+    int T, Hq, G, dtype, max_q, window, sinks;   // G = Hq / Hkv query heads a key / value head
+    float scale;
+    dspark_cache c;
+    const void* q;
+    int64_t q_ts, q_hs;
+    const int32_t* offsets;
+    void* out;
+    float* lse;
+    int* status;
+};
+
 // sample.cu
 cudaError_t launch_draft_setup(const DraftStep& p, cudaStream_t s);
 cudaError_t launch_draft_stats_simt(const DraftStep& p, cudaStream_t s);
@@ -160,6 +205,16 @@ cudaError_t launch_schedule(const ScheduleParams& p, cudaStream_t s);
 
 // assemble.cu
 cudaError_t launch_assemble(const AssembleParams& p, cudaStream_t s);
+
+// qk_norm_rope.cu
+cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s);
+
+// cache_rows.cu
+cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s);
+
+// cache_attend.cu
+cudaError_t launch_cache_attend_simt(const AttendParams& p, cudaStream_t s);
 
 // rnn.cu (RNN head)
 cudaError_t launch_rnn_hidden(const DraftStep& p, cudaStream_t s);   // rnn_hidden.cu: yh = W_rnn[:, 2r:] h, every position
