@@ -7,6 +7,7 @@
 
 #include <atomic>
 
+#include "attend_plan.cuh"
 #include "cache.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -321,6 +322,11 @@ AttendParams attend_params(const dspark_cache_attend_args* a)
     p.out = a->out;
     p.lse = a->lse;
     return p;
+}
+
+bool attend_uses_mma(const dspark_cache_attend_args* a, const AttendParams& p)
+{
+    return a->path != DSPARK_PATH_CUDA_CORE && attend_mma_supported(p);
 }
 
 template <typename T>
@@ -733,7 +739,8 @@ dspark_status dspark_cache_attend_workspace_size(const dspark_cache_attend_args*
     const dspark_status st = check_attend(a);
     if (st != DSPARK_OK) return st;
     if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
-    *bytes = kStatusBytes;
+    const AttendParams p = attend_params(a);
+    *bytes = kStatusBytes + (attend_uses_mma(a, p) ? attend_mma_scratch(p, nullptr, nullptr) : 0);
     return DSPARK_OK;
 }
 
@@ -742,13 +749,21 @@ dspark_status dspark_cache_attend(const dspark_cache_attend_args* a, void* ws, s
     clear_stale_error();
     const dspark_status st = check_attend(a);
     if (st != DSPARK_OK) return st;
-    if (a->path == DSPARK_PATH_TENSOR_CORE) return DSPARK_ERR_UNSUPPORTED_SHAPE;
     AttendParams p = attend_params(a);
+    if (a->path == DSPARK_PATH_TENSOR_CORE && !attend_uses_mma(a, p)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
     if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
     p.status = at<int>(ws, 0);
-    if (a->T == 0) return DSPARK_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_simt(p, s); }));
+    if (!attend_uses_mma(a, p)) {
+        if (a->T == 0) return DSPARK_OK;
+        return cuda_status(launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_simt(p, s); }));
+    }
+    AttendScratch scratch;
+    if (ws_bytes < kStatusBytes + attend_mma_scratch(p, &scratch, at<char>(ws, kStatusBytes))) return DSPARK_ERR_WORKSPACE;
+    if (a->T == 0) return DSPARK_OK;
+    cudaError_t e = launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_mma(p, scratch, s); });
+    if (e == cudaSuccess) e = launch(DSPARK_KERNEL_CACHE_MERGE, s, [&] { return launch_cache_merge(p, scratch, s); });
+    return cuda_status(e);
 }
 
 const char* dspark_last_error(void) { return g_last_error; }

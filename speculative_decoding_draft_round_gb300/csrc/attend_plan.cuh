@@ -1,0 +1,157 @@
+// attend_plan.cuh -- how the matrix kernels of dspark_cache_attend lay the keys of all requests, heads and
+// row blocks out as one line of 64-token tiles, from the lengths on the device.
+#pragma once
+
+#include "cache.cuh"
+#include "internal.h"
+
+namespace dspark {
+
+constexpr int kTile = 64;   // tokens of a tile
+
+// What a run leaves of an item that other runs share, and which runs start such an item.
+struct AttendScratch {
+    float* rows;    // [runs][2][block rows][D] weighted sums
+    float2* ml;     // [runs][2][block rows] maximum (log2 units) and sum of the weights
+    int4* todo;     // [runs] request (-1: none), item of the request, parts, slot of the first part
+};
+
+// A request's rows and the tiles its queries reach: the tiles of the sinks, then those from the first
+// query's window on (one range when they touch).
+struct RequestSpan {
+    int first, n_q, ctx, keys, tiles, sink_tiles, lo_tile, blocks;
+    __device__ __forceinline__ int key0(int u) const
+    {
+        return (u < sink_tiles ? u : lo_tile + u - sink_tiles) * kTile;
+    }
+};
+
+__device__ __forceinline__ RequestSpan request_span(const AttendParams& p, int r, int MB, bool report)
+{
+    RequestSpan s;
+    const int a = p.offsets[r], b = p.offsets[r + 1], ctx = p.c.ctx_len[r];
+    const int last = min(b, p.T);
+    bool odd = a < 0 || b < a || b > p.T || ctx < 0;
+    s.first = a;
+    s.n_q = a < 0 || ctx < 0 ? 0 : max(0, last - a);
+    if (s.n_q > p.max_q) {
+        odd = true;
+        s.n_q = p.max_q;
+    }
+    s.ctx = ctx;
+    const int cap = p.c.table_width * p.c.page_size;
+    long long keys = (long long)ctx + s.n_q;
+    if (s.n_q > 0 && keys > cap) {
+        odd = true;
+        keys = cap;
+    }
+    if (odd && report) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+    s.keys = s.n_q > 0 ? (int)keys : 0;
+    const int all = (s.keys + kTile - 1) / kTile;
+    s.sink_tiles = s.lo_tile = 0;
+    s.tiles = all;
+    if (p.window > 0 && s.n_q > 0) {
+        const int from = (int)max(0ll, (long long)ctx - p.window + 1);
+        const int sink_tiles = (int)(((long long)min(p.sinks, from) + kTile - 1) / kTile), lo = from / kTile;
+        if (sink_tiles < lo) {
+            s.sink_tiles = sink_tiles;
+            s.lo_tile = lo;
+            s.tiles = sink_tiles + max(0, all - lo);
+        }
+    }
+    s.tiles = max(s.tiles, 1);
+    s.blocks = (int)(((long long)s.n_q * p.G + MB - 1) / MB);
+    return s;
+}
+
+// pre[r] = tiles before request r's; returns the total. Called by all NT threads of the CTA, the first
+// `threads` of which do the work. pre has R + 1 entries, scan NT / 32 + 1.
+template <int NT>
+__device__ __forceinline__ int plan_line(const AttendParams& p, int MB, int* pre, int* scan, bool report)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.c.R;
+    const int each = (R + NT - 1) / NT, r0 = min(tid * each, R), r1 = min(r0 + each, R);
+    int sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const RequestSpan s = request_span(p, r, MB, report);
+        const int n = s.tiles * s.blocks * p.c.Hkv;
+        pre[r + 1] = n;
+        sum += n;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int before = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    if (tid == 0) pre[0] = 0;
+    for (int r = r0; r < r1; ++r) {
+        before += pre[r + 1];
+        pre[r + 1] = before;
+    }
+    __syncthreads();
+    return total;
+}
+
+// The item a tile of the line belongs to: request r, item q (head, row block) and tile u of the item.
+struct ItemWalk {
+    int r, q, u;
+    RequestSpan span;
+    __device__ __forceinline__ void start(const int* pre, int R, int at)
+    {
+        int lo = 0, hi = R;   // the request with pre[r] <= at < pre[r + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= at) lo = mid;
+            else hi = mid;
+        }
+        r = lo - 1;
+    }
+    __device__ __forceinline__ void settle(const AttendParams& p, int MB, const int* pre, int at)
+    {
+        if (r < 0 || at >= pre[r + 1]) {
+            do ++r;
+            while (at >= pre[r + 1]);
+            span = request_span(p, r, MB, false);
+        }
+        q = (at - pre[r]) / span.tiles;
+        u = (at - pre[r]) % span.tiles;
+    }
+    __device__ __forceinline__ int head() const { return q / span.blocks; }
+    __device__ __forceinline__ int block() const { return q % span.blocks; }
+};
+
+template <typename T>
+__device__ __forceinline__ void store1(T* p, float x);
+template <>
+__device__ __forceinline__ void store1<float>(float* p, float x) { *p = x; }
+template <>
+__device__ __forceinline__ void store1<__nv_bfloat16>(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// The rows of the batch before the first request's and after the last's: out = 0, lse = -inf. Thread
+// `index` of `threads`.
+template <typename T>
+__device__ __forceinline__ void zero_rows(const AttendParams& p, int D, int index, int threads)
+{
+    const int lo = min(max(p.offsets[0], 0), p.T), hi = max(lo, min(p.offsets[p.c.R], p.T));
+    const long long vecs = (long long)p.Hq * D * sizeof(T) / 16, rows = lo + (p.T - hi);
+    for (long long x = index; x < rows * vecs; x += threads) {
+        const long long k = x / vecs, t = k < lo ? k : hi + (k - lo);
+        reinterpret_cast<uint4*>(p.out)[t * vecs + x % vecs] = make_uint4(0, 0, 0, 0);
+    }
+    if (p.lse)
+        for (long long x = index; x < rows * p.Hq; x += threads) {
+            const long long k = x / p.Hq, t = k < lo ? k : hi + (k - lo);
+            p.lse[t * p.Hq + x % p.Hq] = -INFINITY;
+        }
+}
+
+}  // namespace dspark

@@ -156,6 +156,7 @@ struct AttendParams {
     dspark_cache c;
     const void* q;
     int64_t q_ts, q_hs;
+    int q_aligned;       // q's rows admit 16-byte loads
     const int32_t* offsets;
     void* out;
     float* lse;
@@ -215,6 +216,14 @@ cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s);
 
 // cache_attend.cu
 cudaError_t launch_cache_attend_simt(const AttendParams& p, cudaStream_t s);
+
+// cache_attend_mma.cu
+struct AttendScratch;
+bool attend_mma_supported(const AttendParams& p);
+// bytes of its workspace; with ws, the parts of the workspace at base
+size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base);
+cudaError_t launch_cache_attend_mma(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
+cudaError_t launch_cache_merge(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
 
 // rnn.cu (RNN head)
 cudaError_t launch_rnn_hidden(const DraftStep& p, cudaStream_t s);   // rnn_hidden.cu: yh = W_rnn[:, 2r:] h, every position
