@@ -1,13 +1,11 @@
 // attend_plan.cuh -- how the matrix kernels of dspark_cache_attend lay the keys of all requests, heads and
-// row blocks out as one line of 64-token tiles, from the lengths on the device.
+// row blocks out as one line of tiles of TILE tokens, from the lengths on the device.
 #pragma once
 
 #include "cache.cuh"
 #include "internal.h"
 
 namespace dspark {
-
-constexpr int kTile = 64;   // tokens of a tile
 
 // What a run leaves of an item that other runs share, and which runs start such an item.
 struct AttendScratch {
@@ -18,17 +16,19 @@ struct AttendScratch {
 
 // A request's rows and the tiles its queries reach: the tiles of the sinks, then those from the first
 // query's window on (one range when they touch).
+template <int TILE>
 struct RequestSpan {
     int first, n_q, ctx, keys, tiles, sink_tiles, lo_tile, blocks;
     __device__ __forceinline__ int key0(int u) const
     {
-        return (u < sink_tiles ? u : lo_tile + u - sink_tiles) * kTile;
+        return (u < sink_tiles ? u : lo_tile + u - sink_tiles) * TILE;
     }
 };
 
-__device__ __forceinline__ RequestSpan request_span(const AttendParams& p, int r, int MB, bool report)
+template <int TILE>
+__device__ __forceinline__ RequestSpan<TILE> request_span(const AttendParams& p, int r, int MB, bool report)
 {
-    RequestSpan s;
+    RequestSpan<TILE> s;
     const int a = p.offsets[r], b = p.offsets[r + 1], ctx = p.c.ctx_len[r];
     const int last = min(b, p.T);
     bool odd = a < 0 || b < a || b > p.T || ctx < 0;
@@ -47,12 +47,12 @@ __device__ __forceinline__ RequestSpan request_span(const AttendParams& p, int r
     }
     if (odd && report) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
     s.keys = s.n_q > 0 ? (int)keys : 0;
-    const int all = (s.keys + kTile - 1) / kTile;
+    const int all = (s.keys + TILE - 1) / TILE;
     s.sink_tiles = s.lo_tile = 0;
     s.tiles = all;
     if (p.window > 0 && s.n_q > 0) {
         const int from = (int)max(0ll, (long long)ctx - p.window + 1);
-        const int sink_tiles = (int)(((long long)min(p.sinks, from) + kTile - 1) / kTile), lo = from / kTile;
+        const int sink_tiles = (int)(((long long)min(p.sinks, from) + TILE - 1) / TILE), lo = from / TILE;
         if (sink_tiles < lo) {
             s.sink_tiles = sink_tiles;
             s.lo_tile = lo;
@@ -66,14 +66,14 @@ __device__ __forceinline__ RequestSpan request_span(const AttendParams& p, int r
 
 // pre[r] = tiles before request r's; returns the total. Called by all NT threads of the CTA, the first
 // `threads` of which do the work. pre has R + 1 entries, scan NT / 32 + 1.
-template <int NT>
+template <int NT, int TILE>
 __device__ __forceinline__ int plan_line(const AttendParams& p, int MB, int* pre, int* scan, bool report)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.c.R;
     const int each = (R + NT - 1) / NT, r0 = min(tid * each, R), r1 = min(r0 + each, R);
     int sum = 0;
     for (int r = r0; r < r1; ++r) {
-        const RequestSpan s = request_span(p, r, MB, report);
+        const RequestSpan<TILE> s = request_span<TILE>(p, r, MB, report);
         const int n = s.tiles * s.blocks * p.c.Hkv;
         pre[r + 1] = n;
         sum += n;
@@ -102,9 +102,10 @@ __device__ __forceinline__ int plan_line(const AttendParams& p, int MB, int* pre
 }
 
 // The item a tile of the line belongs to: request r, item q (head, row block) and tile u of the item.
+template <int TILE>
 struct ItemWalk {
     int r, q, u;
-    RequestSpan span;
+    RequestSpan<TILE> span;
     __device__ __forceinline__ void start(const int* pre, int R, int at)
     {
         int lo = 0, hi = R;   // the request with pre[r] <= at < pre[r + 1]
@@ -120,7 +121,7 @@ struct ItemWalk {
         if (r < 0 || at >= pre[r + 1]) {
             do ++r;
             while (at >= pre[r + 1]);
-            span = request_span(p, r, MB, false);
+            span = request_span<TILE>(p, r, MB, false);
         }
         q = (at - pre[r]) / span.tiles;
         u = (at - pre[r]) % span.tiles;
