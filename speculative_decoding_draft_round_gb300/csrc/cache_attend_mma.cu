@@ -4,13 +4,13 @@
 //   out = sum_i 2^(t_i - m) v_i / sum_i 2^(t_i - m),  t_i = log2(e) scale q . k_i, in one pass over the keys.
 //
 // What bounds it: a cached token is 9 D / 8 bytes a head, and its 2 D codes have to become fp16 before a
-// product. A warp therefore turns codes into the B fragments of m16n8k16 products in registers, with no
-// step through shared memory in fp16, and uses each for all rows of the block: the G heads of all the
-// request's queries, 16 rows at a time.
+// product. A warp therefore turns codes into the A fragments of m16n8k16 products in registers, with no
+// step through shared memory in fp16: 16 keys (then 16 channels of the values) by the block's rows, which
+// are the G heads of the request's queries, 8 at a time (NB column tiles). So few rows waste little.
 //  - The order of the channels inside q . k is free, so a lane takes the consecutive bytes of one key
 //    that make one load, and q's fragments are laid out to match. A lane's channels lie in one group: one
 //    scale a key. For the values the two tokens that share a register are joined by a byte permutation
-//    before their nibbles are taken apart.
+//    before their nibbles are taken apart; the weights turn by movmatrix.
 //  - (u - 8) s is exact in fp16 (the cache's scales have 8 bits), q is scaled by a power of two into
 //    fp16's range, exactly for bf16; so the scores carry fp32 rounding only. fp32 rows enter as two fp16 terms, and
 //    their weights too.
@@ -31,10 +31,8 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 32;                       // tokens of a tile
-constexpr int kStages = 3;                      // tiles a warp has in flight
 constexpr int kWarps = 4;                       // of a CTA, each with a run of its own
 constexpr int kThreads = kWarps * 32;
-constexpr int kMB = 16;                         // rows of a block
 constexpr int kBatch = 16;                      // tiles whose places the lanes look up at once
 constexpr float kShift = 10.f;                  // weights are 2^(t - m + kShift) <= 2^15
 constexpr float kSlack = 5.f;                   // m is raised when a score passes it by this
@@ -46,6 +44,14 @@ struct Tile {
     static constexpr uint32_t k_scales = kTile * D;
     static constexpr uint32_t v_scales = k_scales + kTile * D / 16;
     static constexpr uint32_t bytes = v_scales + kTile * D / 16;
+};
+
+// Variants: rows of a block, CTAs on an SM and the stages that shared memory then allows.
+template <typename T, int D, int NB>
+struct Variant {
+    static constexpr int rows = 8 * NB;
+    static constexpr int ctas = sizeof(T) == 4 ? (NB == 1 ? 3 : 2) : (NB == 1 ? 4 : 3);
+    static constexpr int stages = ctas == 4 && D == 128 ? 2 : 3;
 };
 
 __device__ __noinline__ bool a_wait_slow(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns)
@@ -79,11 +85,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the 8 x 8 matrix of 16-bit elements whose row g lanes (g, i) hold, two a lane, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
@@ -163,14 +178,17 @@ struct Place {
     uint32_t slot;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
     cache_attend_mma_kernel(AttendParams p, AttendScratch ws, unsigned long long wait_ns)
 {
     constexpr bool kSplit = sizeof(T) == 4;   // fp32 rows: two fp16 terms
-    constexpr int KS = D / 16;                // products a key tile
-    constexpr int NT = D / 8;                 // channel tiles
-    constexpr int CH = D / 4;                 // channels of a lane
+    constexpr int kMB = 8 * NB;               // rows of a block
+    constexpr int kStages = Variant<T, D, NB>::stages;   // tiles a warp has in flight
+    constexpr int KS = D / 16;                // products of 16 channels
+    constexpr int MT = D / 16;                // tiles of 16 value channels
+    constexpr int CH = D / 4;                 // q's channels of a lane
+    constexpr int CV = D / 8;                 // value channels of a lane
     constexpr int W = D / 32;                 // words of a key a lane holds
     using L = Tile<D>;
     extern __shared__ __align__(128) uint8_t smem[];                     // [kWarps][kStages] tiles, [R + 1] ints
@@ -266,17 +284,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
         it.settle(p, kMB, s_pre, at);
         const int u0 = it.u, u1 = min(it.span.tiles, u0 + (end - at));
         const int h = it.head(), row0 = it.block() * kMB, n_rows = it.span.n_q * p.G;
-        // q's fragments: lane (g, i) holds channels CH i .. of rows g and g + 8
-        uint32_t qa[KS][4], qb[kSplit ? KS : 1][4];
-        float fac[2];
-        int pos[2];
-        bool bad[2];
+        // q's fragments: lane (g, i) holds channels CH i .. of row g of each column tile
+        uint32_t qa[NB][KS][2], qb[kSplit ? NB : 1][kSplit ? KS : 1][2];
+        float fac[NB][2];     // of the rows 2 i and 2 i + 1, whose scores this lane gets
+        bool bad[NB][2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int row = row0 + hf * 8 + g;
+        for (int nb = 0; nb < NB; ++nb) {
+            const int row = row0 + nb * 8 + g;
             const bool real = row < n_rows;
             const int j = min(row, n_rows - 1) / p.G, hd = h * p.G + min(row, n_rows - 1) % p.G;
-            pos[hf] = it.span.ctx + j;
             const T* src = static_cast<const T*>(p.q) + (int64_t)(it.span.first + j) * p.q_ts + hd * p.q_hs + i * CH;
             float x[CH];
             if (p.q_aligned) {
@@ -307,37 +323,45 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const unsigned odds = __ballot_sync(0xffffffffu, odd);
-            bad[hf] = real && ((odds >> (lane & 28)) & 15u) != 0;
+            const unsigned odds = __ballot_sync(0xffffffffu, odd && real);
+            const bool mine = ((odds >> (lane & 28)) & 15u) != 0;
             // the row's largest element to 2^12 .. 2^13
             const int ex = (int)(__float_as_uint(top) >> 23);
             const float up = __uint_as_float((uint32_t)min(266 - ex, 254) << 23);
-            fac[hf] = fmaxf(to_log2 / up, 1e-37f);   // 0 times a masked score would be NaN
-            const bool keep = real && !bad[hf];
+            const float f = fmaxf(to_log2 / up, 1e-37f);   // 0 times a masked score would be NaN
+            const bool keep = real && !mine;
 #pragma unroll
             for (int c = 0; c < CH; ++c) x[c] = keep ? x[c] * up : 0.f;
             // word w of the lane's channels gives products 2 w and 2 w + 1
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int c = (ks / 2) * 8 + (ks % 2) * 2;
-                qa[ks][hf] = pack(x[c], x[c + 4]);
-                qa[ks][2 + hf] = pack(x[c + 1], x[c + 5]);
+                qa[nb][ks][0] = pack(x[c], x[c + 4]);
+                qa[nb][ks][1] = pack(x[c + 1], x[c + 5]);
                 if (kSplit) {
-                    qb[kSplit ? ks : 0][hf] = pack_rest(x[c], x[c + 4], qa[ks][hf]);
-                    qb[kSplit ? ks : 0][2 + hf] = pack_rest(x[c + 1], x[c + 5], qa[ks][2 + hf]);
+                    qb[kSplit ? nb : 0][kSplit ? ks : 0][0] = pack_rest(x[c], x[c + 4], qa[nb][ks][0]);
+                    qb[kSplit ? nb : 0][kSplit ? ks : 0][1] = pack_rest(x[c + 1], x[c + 5], qa[nb][ks][1]);
                 }
             }
-            if (bad[hf] && i == 0) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                fac[nb][e] = __shfl_sync(0xffffffffu, f, (2 * i + e) * 4);
+                bad[nb][e] = ((odds >> ((2 * i + e) * 4)) & 15u) != 0;
+            }
+            if (mine && i == 0) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
         }
         const int pos_lo = it.span.ctx + row0 / p.G;                                    // of the block's rows
         const int pos_hi = it.span.ctx + min(row0 + kMB - 1, n_rows - 1) / p.G;
-        float o[NT][4], top[2], sum[2];
+        float o[NB][MT][4], top[NB][2], sum[NB][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        top[0] = top[1] = -INFINITY;
-        sum[0] = sum[1] = 0.f;
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nb][m][e] = 0.f;
+            top[nb][0] = top[nb][1] = -INFINITY;
+            sum[nb][0] = sum[nb][1] = 0.f;
+        }
 #pragma unroll 1
         for (int u = u0; u < u1; ++u, ++count) {
             const int st = count % kStages;
@@ -349,28 +373,41 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
             }
             const uint32_t have = (there[(count / kBatch) & 1] >> (2 * (count % kBatch))) & 3u;
             if (ok && have != 0) {
-                // ---------------- scores of 32 keys
-                float s[4][4];
+                // ---------------- scores of 32 keys: lane (g, i) gets keys g, g + 8 of each 16 by rows 2 i, 2 i + 1
+                float s[2][NB][4];
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const int tok = nt * 8 + g;
-                    const uint32_t* src = reinterpret_cast<const uint32_t*>(tile + tok * (D / 2) + i * (D / 8));
-                    uint32_t w[W];
-                    if (W == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(src);
-                    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(src);
-                    const __half2 sc = __half2half2(
-                        *reinterpret_cast<const __half*>(tile + L::k_scales + (tok * (D / 32) + i * D / 128) * 2));
+                for (int sl = 0; sl < 2; ++sl) {
+                    uint32_t w[2][W];
+                    __half2 sc[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+                    for (int k = 0; k < 2; ++k) {
+                        const int tok = sl * 16 + k * 8 + g;
+                        const uint32_t* src = reinterpret_cast<const uint32_t*>(tile + tok * (D / 2) + i * (D / 8));
+                        if (W == 4) *reinterpret_cast<uint4*>(w[k]) = *reinterpret_cast<const uint4*>(src);
+                        else *reinterpret_cast<uint2*>(w[k]) = *reinterpret_cast<const uint2*>(src);
+                        sc[k] = __half2half2(
+                            *reinterpret_cast<const __half*>(tile + L::k_scales + (tok * (D / 32) + i * D / 128) * 2));
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[sl][nb][e] = 0.f;
 #pragma unroll
                     for (int x = 0; x < W; ++x) {
-                        uint32_t b[4];
-                        dequant(w[x], sc, dq, b);
-                        mma16816(s[nt], qa[2 * x], b[0], b[1]);
-                        mma16816(s[nt], qa[2 * x + 1], b[2], b[3]);
-                        if (kSplit) {
-                            mma16816(s[nt], qb[kSplit ? 2 * x : 0], b[0], b[1]);
-                            mma16816(s[nt], qb[kSplit ? 2 * x + 1 : 0], b[2], b[3]);
+                        uint32_t a[4], b[4];
+                        dequant(w[0][x], sc[0], dq, a);
+                        dequant(w[1][x], sc[1], dq, b);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                mma16816(s[sl][nb], a[2 * k], b[2 * k], a[2 * k + 1], b[2 * k + 1], qa[nb][2 * x + k][0],
+                                         qa[nb][2 * x + k][1]);
+                                if (kSplit)
+                                    mma16816(s[sl][nb], a[2 * k], b[2 * k], a[2 * k + 1], b[2 * k + 1],
+                                             qb[kSplit ? nb : 0][kSplit ? 2 * x + k : 0][0],
+                                             qb[kSplit ? nb : 0][kSplit ? 2 * x + k : 0][1]);
+                            }
                         }
                     }
                 }
@@ -379,52 +416,58 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
                                   (p.window > 0 && (long long)key0 <= (long long)pos_hi - p.window);
                 if (edge) {
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + nt * 8 + 2 * i + (e & 1), own = pos[e >> 1];
-                            bool see = key <= own && key < it.span.keys && ((have >> (nt >> 1)) & 1u);
-                            if (p.window > 0) see = see && ((long long)key > (long long)own - p.window || key < p.sinks);
-                            if (!see) s[nt][e] = -INFINITY;
+                        for (int r2 = 0; r2 < 2; ++r2) {
+                            const int own = it.span.ctx + min(row0 + nb * 8 + 2 * i + r2, n_rows - 1) / p.G;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int key = key0 + k * 8 + g;
+                                bool see = key <= own && key < it.span.keys && ((have >> (k >> 1)) & 1u);
+                                if (p.window > 0)
+                                    see = see && ((long long)key > (long long)own - p.window || key < p.sinks);
+                                if (!see) s[k >> 1][nb][2 * (k & 1) + r2] = -INFINITY;
+                            }
                         }
                 }
-                float mx[2];
+                uint32_t pa[2][NB][2], pb[2][NB][2];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float m = fmaxf(s[0][2 * hf], s[0][2 * hf + 1]);
+                for (int nb = 0; nb < NB; ++nb) {
+                    float mx[2];
 #pragma unroll
-                    for (int nt = 1; nt < 4; ++nt) m = fmaxf(m, fmaxf(s[nt][2 * hf], s[nt][2 * hf + 1]));
-                    mx[hf] = fac[hf] * m;
-                }
-                if (__any_sync(0xffffffffu, mx[0] > top[0] + kSlack || mx[1] > top[1] + kSlack)) {
+                    for (int e = 0; e < 2; ++e)
+                        mx[e] = fac[nb][e] * fmaxf(fmaxf(s[0][nb][e], s[0][nb][2 + e]), fmaxf(s[1][nb][e], s[1][nb][2 + e]));
+                    if (__any_sync(0xffffffffu, mx[0] > top[nb][0] + kSlack || mx[1] > top[nb][1] + kSlack)) {
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float m = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                        m = fmaxf(m, top[hf]);
-                        const float keep = m == top[hf] ? 1.f : ex2(top[hf] - m);
-                        top[hf] = m;
-                        sum[hf] *= keep;
+                        for (int e = 0; e < 2; ++e) {
+                            float m = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            m = fmaxf(m, top[nb][e]);
+                            const float keep = m == top[nb][e] ? 1.f : ex2(top[nb][e] - m);
+                            top[nb][e] = m;
+                            sum[nb][e] *= keep;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            o[n][2 * hf] *= keep;
-                            o[n][2 * hf + 1] *= keep;
+                            for (int n = 0; n < MT; ++n) {
+                                o[nb][n][e] *= keep;
+                                o[nb][n][2 + e] *= keep;
+                            }
                         }
                     }
-                }
-                uint32_t pa[2][4], pb[2][4];
+                    const float base0 = top[nb][0] == -INFINITY ? 0.f : kShift - top[nb][0];
+                    const float base1 = top[nb][1] == -INFINITY ? 0.f : kShift - top[nb][1];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const float base = top[hf] == -INFINITY ? 0.f : kShift - top[hf];
+                    for (int sl = 0; sl < 2; ++sl)
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        const float e0 = ex2(fmaf(s[nt][2 * hf], fac[hf], base));
-                        const float e1 = ex2(fmaf(s[nt][2 * hf + 1], fac[hf], base));
-                        sum[hf] += e0 + e1;
-                        const uint32_t hi = pack(e0, e1);
-                        pa[nt >> 1][2 * (nt & 1) + hf] = hi;
-                        if (kSplit) pb[nt >> 1][2 * (nt & 1) + hf] = pack_rest(e0, e1, hi);
-                    }
+                        for (int k = 0; k < 2; ++k) {
+                            const float e0 = ex2(fmaf(s[sl][nb][2 * k], fac[nb][0], base0));
+                            const float e1 = ex2(fmaf(s[sl][nb][2 * k + 1], fac[nb][1], base1));
+                            sum[nb][0] += e0;
+                            sum[nb][1] += e1;
+                            const uint32_t hi = pack(e0, e1);
+                            pa[sl][nb][k] = transpose8(hi);   // row g, tokens 2 i and 2 i + 1 of 8
+                            if (kSplit) pb[sl][nb][k] = transpose8(pack_rest(e0, e1, hi));
+                        }
                 }
                 // ---------------- values: tokens 2 i, 2 i + 1 and 8 above; lanes of odd i take the odd token
                 // first, so that the four i of a load touch both halves of 128 bytes
@@ -463,11 +506,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
                             const uint32_t sel = z == 0 ? sel_lo : sel_hi;
                             dequant(__byte_perm(va[0][x], vb[0][x], sel), vs[0], dq, b0);
                             dequant(__byte_perm(va[1][x], vb[1][x], sel), vs[1], dq, b1);
+                            // tile m has channels CV g + 2 m in rows g and CV g + 2 m + 1 in rows g + 8
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                mma16816(o[x * 8 + z * 4 + e], pa[sl], b0[e], b1[e]);
-                                if (kSplit) mma16816(o[x * 8 + z * 4 + e], pb[sl], b0[e], b1[e]);
-                            }
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) {
+                                    float(&acc)[4] = o[nb][x * 4 + z * 2 + e];
+                                    mma16816(acc, b0[2 * e], b0[2 * e + 1], b1[2 * e], b1[2 * e + 1], pa[sl][nb][0],
+                                             pa[sl][nb][1]);
+                                    if (kSplit)
+                                        mma16816(acc, b0[2 * e], b0[2 * e + 1], b1[2 * e], b1[2 * e + 1], pb[sl][nb][0],
+                                                 pb[sl][nb][1]);
+                                }
                         }
                 }
             }
@@ -488,38 +538,38 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
         const bool whole = u0 == 0 && u1 == it.span.tiles;
         const int slot = at == begin ? 0 : 1;   // a run's first item, or its last
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            float l = sum[hf];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if (bad[hf]) l = NAN;
-            const int row = hf * 8 + g, rr = row0 + row;
-            if (rr >= n_rows) continue;
-            if (!whole) {
-                const size_t part_row = ((size_t)run_id * 2 + slot) * kMB + row;
-                float* dst = ws.rows + part_row * D + i * CH;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int c = 0; c < CH; c += 4) {
-                    float v[4];
+            for (int e = 0; e < 2; ++e) {
+                float l = sum[nb][e];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = o[(c + e) % NT][2 * hf + (c + e) / NT];
-                    *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
+                for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+                if (bad[nb][e]) l = NAN;
+                // lane (g, i): channels CV g .. of row 2 i + e
+                const int row = nb * 8 + 2 * i + e, rr = row0 + row;
+                if (rr >= n_rows) continue;
+                if (!whole) {
+                    const size_t part_row = ((size_t)run_id * 2 + slot) * kMB + row;
+                    float* dst = ws.rows + part_row * D + g * CV;
+#pragma unroll
+                    for (int c = 0; c < CV; c += 4)
+                        *reinterpret_cast<float4*>(dst + c) = make_float4(o[nb][c / 2][e], o[nb][c / 2][2 + e],
+                                                                         o[nb][c / 2 + 1][e], o[nb][c / 2 + 1][2 + e]);
+                    if (g == 0) ws.ml[part_row] = make_float2(top[nb][e], l);
+                } else {
+                    const size_t dst = (size_t)(it.span.first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
+                    // no visible key: zeros; a row that is not finite: NaN
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                    for (int c = 0; c < CV; c += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = o[nb][(c + k) / 2][2 * (k & 1) + e] * inv;
+                        store8<T>(static_cast<T*>(p.out) + dst * D + g * CV + c, v);
+                    }
+                    if (g == 0 && p.lse) p.lse[dst] = l == 0.f ? -INFINITY : (top[nb][e] + log2f(l) - kShift) * kLn2;
                 }
-                if (i == 0) ws.ml[part_row] = make_float2(top[hf], l);
-            } else {
-                const size_t dst = (size_t)(it.span.first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
-                // no visible key: zeros; a row that is not finite: NaN
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                for (int c = 0; c < CH; c += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = o[(c + e) % NT][2 * hf + (c + e) / NT] * inv;
-                    store8<T>(static_cast<T*>(p.out) + dst * D + i * CH + c, v);
-                }
-                if (i == 0 && p.lse) p.lse[dst] = l == 0.f ? -INFINITY : (top[hf] + log2f(l) - kShift) * kLn2;
             }
-        }
         // an item that starts here and goes on: the next kernel joins its parts
         if (u0 == 0 && u1 < it.span.tiles) todo = make_int4(it.r, it.q, (at + it.span.tiles - 1) / per - run_id + 1, slot);
         at += u1 - u0;
@@ -533,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
 // or, where an item has many parts, the whole CTA one row after the other. Also zeros the rows of the batch
 // that no request has.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, AttendScratch ws)
+__global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, AttendScratch ws, int kMB)
 {
     pdl_enter();
     __shared__ float s_l[kWarps];
@@ -602,23 +652,41 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, A
     zero_rows<T>(p, D, (blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x, gridDim.x * gridDim.y * kThreads);
 }
 
-int grid_ctas(const AttendParams& p) { return num_sms() * (p.dtype == DSPARK_BF16 ? 3 : 2); }
+// Rows of a block: 8 where no request has more, else 16
+int block_rows(const AttendParams& p) { return (long long)p.max_q * p.G <= 8 ? 8 : 16; }
+
+int grid_ctas(const AttendParams& p)
+{
+    const bool bf = p.dtype == DSPARK_BF16, few = block_rows(p) == 8;
+    static_assert(Variant<float, 64, 1>::ctas == Variant<float, 128, 1>::ctas, "independent of the width");
+    const int ctas = bf ? (few ? Variant<__nv_bfloat16, 128, 1>::ctas : Variant<__nv_bfloat16, 128, 2>::ctas)
+                        : (few ? Variant<float, 128, 1>::ctas : Variant<float, 128, 2>::ctas);
+    return num_sms() * ctas;
+}
+
+template <typename T, int D, int NB>
+cudaError_t launch_rows(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
+{
+    const size_t smem = kWarps * Variant<T, D, NB>::stages * Tile<D>::bytes + sizeof(int) * (p.c.R + 1);
+    const cudaError_t e = cudaFuncSetAttribute(cache_attend_mma_kernel<T, D, NB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_attend_mma_kernel<T, D, NB>, dim3(grid_ctas(p)), dim3(kThreads), smem, s, p, ws, wait_limit_ns());
+}
 
 template <typename T, int D>
 cudaError_t launch_mma(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
 {
-    const size_t smem = kWarps * kStages * Tile<D>::bytes + sizeof(int) * (p.c.R + 1);
-    const cudaError_t e = cudaFuncSetAttribute(cache_attend_mma_kernel<T, D>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attend_mma_kernel<T, D>, dim3(grid_ctas(p)), dim3(kThreads), smem, s, p, ws, wait_limit_ns());
+    return block_rows(p) == 8 ? launch_rows<T, D, 1>(p, ws, s) : launch_rows<T, D, 2>(p, ws, s);
 }
 
 template <typename T, int D>
 cudaError_t launch_merge(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
 {
-    const int rows = (int)(p.max_q >= kMB ? kMB : p.max_q * (p.G < kMB ? p.G : kMB));
-    return launch_pdl(cache_merge_kernel<T, D>, dim3(grid_ctas(p), rows < kMB ? rows : kMB), dim3(kThreads), 0, s, p, ws);
+    const int MB = block_rows(p);
+    const long long rows = (long long)p.max_q * p.G;
+    return launch_pdl(cache_merge_kernel<T, D>, dim3(grid_ctas(p), (unsigned)(rows < MB ? rows : MB)), dim3(kThreads), 0, s,
+                      p, ws, MB);
 }
 
 template <typename T>
@@ -635,7 +703,7 @@ bool attend_mma_supported(const AttendParams& p)
     // tiles and rows are counted in 32 bits
     const long long rows = (long long)p.max_q * p.G;
     const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
-    return rows < (1ll << 30) && (double)p.c.R * p.c.Hkv * (double)(rows / kMB + 1) * (double)tiles < 2147483647.0;
+    return rows < (1ll << 30) && (double)p.c.R * p.c.Hkv * (double)(rows / block_rows(p) + 1) * (double)tiles < 2147483647.0;
 }
 
 size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base)
@@ -643,9 +711,9 @@ size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base)
     const size_t runs = (size_t)grid_ctas(p) * kWarps;
     size_t o = 0;
     const size_t rows = o;
-    o = align_up(o + sizeof(float) * runs * 2 * kMB * p.c.D, 256);
+    o = align_up(o + sizeof(float) * runs * 2 * block_rows(p) * p.c.D, 256);
     const size_t ml = o;
-    o = align_up(o + sizeof(float2) * runs * 2 * kMB, 256);
+    o = align_up(o + sizeof(float2) * runs * 2 * block_rows(p), 256);
     const size_t todo = o;
     o = align_up(o + sizeof(int4) * runs, 256);
     if (ws) {
