@@ -7,11 +7,18 @@
 
 namespace dspark {
 
-// What a run leaves of an item that other runs share, and which runs start such an item.
+// The item that a run starts and does not end: its rows, and how many runs have parts of it (0: none).
+struct __align__(16) AttendTodo {
+    int parts, slot;               // and the run's slot that holds the first
+    int first, head, row0, rows;   // flat row of the request, key / value head, first row and rows of the block
+    int pad[2];
+};
+
+// What a run leaves of items that other runs share.
 struct AttendScratch {
     float* rows;    // [runs][2][block rows][D] weighted sums
     float2* ml;     // [runs][2][block rows] maximum (log2 units) and sum of the weights
-    int4* todo;     // [runs] request (-1: none), item of the request, parts, slot of the first part
+    AttendTodo* todo;   // [runs]
 };
 
 // A request's rows and the tiles its queries reach: the tiles of the sinks, then those from the first

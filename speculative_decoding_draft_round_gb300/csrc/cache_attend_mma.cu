@@ -18,13 +18,13 @@
 //    factor 2^10, so that they stay below fp16's largest number and small ones above its smallest.
 // The keys of all (request, head, row block) items form one line of 32-token tiles, cut into equal runs,
 // one a warp, whatever the lengths are. A warp works alone: it copies its tiles into stages of its own by
-// bulk copies issued kStages ahead, and no barrier joins it to others. A run that ends inside an item
+// 16-byte asynchronous copies, stages - 1 tiles ahead, and no barrier joins it to others (bulk copies of the
+// tile's four parts cost more: their operands are uniform, a divergent loop of about 60 instructions a tile). A run that ends inside an item
 // leaves a part (maximum, sum, unnormalised rows) in the workspace, and a second small kernel joins the
 // parts in order.
 #include "attend_plan.cuh"
 #include "cache.cuh"
 #include "internal.h"
-#include "tma.cuh"
 
 namespace dspark {
 
@@ -36,7 +36,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBatch = 16;                      // tiles whose places the lanes look up at once
 constexpr float kShift = 10.f;                  // weights are 2^(t - m + kShift) <= 2^15
 constexpr float kSlack = 5.f;                   // m is raised when a score passes it by this
-constexpr unsigned long long kDrainNs = 4000000000ull;
 
 template <int D>
 struct Tile {
@@ -54,35 +53,12 @@ struct Variant {
     static constexpr int stages = ctas == 4 && D == 128 ? 2 : 3;
 };
 
-__device__ __noinline__ bool a_wait_slow(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns)
-{
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer() - t0 > limit_ns) {
-            raise_status(status, DSPARK_ERR_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
+__device__ __forceinline__ uint32_t shared_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ bool a_wait(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns)
+// 16 bytes; zeros where there is nothing to copy
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
 {
-    return mbar_try_wait(bar, parity) || a_wait_slow(bar, parity, status, limit_ns);
-}
-
-__device__ __noinline__ void a_drain(uint32_t bar, uint32_t parity)
-{
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < kDrainNs) {
-    }
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -172,15 +148,16 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
 }
 
 // What lane 2 j + half of a warp knows of tile j of a batch: the block that holds its 16 tokens of that
-// half (NULL: beyond the keys, or a page out of range) and the slot of the first.
+// half, the slot of the first, and whether they are there: not beyond the keys, nor in a page out of range.
 struct Place {
     const uint8_t* block;
     uint32_t slot;
+    bool there;
 };
 
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
-    cache_attend_mma_kernel(AttendParams p, AttendScratch ws, unsigned long long wait_ns)
+    cache_attend_mma_kernel(AttendParams p, AttendScratch ws)
 {
     constexpr bool kSplit = sizeof(T) == 4;   // fp32 rows: two fp16 terms
     constexpr int kMB = 8 * NB;               // rows of a block
@@ -193,18 +170,12 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
     using L = Tile<D>;
     extern __shared__ __align__(128) uint8_t smem[];                     // [kWarps][kStages] tiles, [R + 1] ints
     int* s_pre = reinterpret_cast<int*>(smem + kWarps * kStages * L::bytes);
-    __shared__ uint64_t s_bar[kWarps * kStages];
     __shared__ int s_scan[kWarps + 1];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, i = lane & 3;
     uint8_t* const stages = smem + warp * kStages * L::bytes;
-    const uint32_t sbase = smem_addr(stages), bar0 = smem_addr(s_bar + warp * kStages);
-    if (lane == 0) {
-        for (int k = 0; k < kStages; ++k) mbar_init(bar0 + 8u * k, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_proxy_async();
-    }
+    const uint32_t sbase = shared_addr(stages);
     pdl_wait();
     pdl_trigger();
     // ---------------- the line of tiles and this warp's run of it
@@ -214,13 +185,13 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
     const int begin = (int)min((long long)run_id * per, (long long)total);
     const int end = min(begin + per, total);
     if (begin >= end) {
-        if (lane == 0) ws.todo[run_id] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) ws.todo[run_id].parts = 0;
         return;
     }
     const CacheBlock cb = cache_block(p.c.page_size, D);
     // Where the tiles from `at` on are: one lane looks up each half tile, kBatch tiles at a time.
     auto look_up = [&](int at) {
-        Place w{nullptr, 0};
+        Place w{static_cast<const uint8_t*>(p.c.pages), 0, false};
         const int tile = at + (lane >> 1);
         if (tile < end) {
             ItemWalk<kTile> it;
@@ -232,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
                 if (page >= 0 && page < p.c.n_pages) {
                     w.block = cache_page_block(p.c, page, it.head(), cb.bytes);
                     w.slot = key0 % p.c.page_size;
+                    w.there = true;
                 } else {
                     raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
                 }
@@ -239,46 +211,54 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
         }
         return w;
     };
-    // Tile n of the run into its stage: lanes (half, part) copy 16 tokens of one part each, or the lanes of
-    // half 0 both halves where pages hold whole tiles.
-    const int part = lane & 3, half = (lane >> 2) & 1;
-    const bool joined = p.c.page_size % kTile == 0;
-    const uint32_t row_bytes = part < 2 ? D / 2 : D / 16;   // of a token
-    const uint32_t part_from = part == 0 ? 0u : part == 1 ? cb.v_codes : part == 2 ? cb.k_scales : cb.v_scales;
-    const uint32_t part_to = part == 0 ? 0u : part == 1 ? L::v_codes : part == 2 ? L::k_scales : L::v_scales;
-    auto issue = [&](int n, const Place& w) {
-        const int st = n % kStages, from = 2 * (n % kBatch) + half;
-        const unsigned long long blk = __shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)w.block, from);
-        const uint32_t slot = __shfl_sync(0xffffffffu, w.slot, from);
-        // with whole tiles in a page both halves are there when the first is: what lies past the keys is masked
-        const bool mine = lane < (joined ? 4 : 8) && blk != 0;
-        const uint32_t bytes = mine ? row_bytes * (joined ? kTile : 16) : 0u;
-        uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
-        const uint32_t bar = bar0 + 8u * st;
-        if (lane == 0) {
-            if (sum) mbar_expect_tx(bar, sum);
-            else mbar_arrive(bar);
+    // Tile n of the run into its stage. Chunks of 512 bytes, 16 a lane: those of the K and V codes, and one of
+    // the scales, whose lanes are (part, half, 16 bytes).
+    constexpr int kChunks = kTile * D / 2 / 512, kScaleLanes = D / 16;
+    const int sc_half = (lane / kScaleLanes) & 1;
+    const bool sc_v = lane >= 2 * kScaleLanes;
+    const uint32_t sc_from = (sc_v ? cb.v_scales : cb.k_scales) + (lane % kScaleLanes) * 16;
+    const uint32_t sc_to = (sc_v ? L::v_scales : L::k_scales) + (lane % (2 * kScaleLanes)) * 16;
+    auto issue = [&](int n, uint32_t dst, const Place& w, uint32_t have) {
+        const uint8_t* blk[2];
+        uint32_t slot[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int from = 2 * (n % kBatch) + hf;
+            blk[hf] = reinterpret_cast<const uint8_t*>(
+                (uintptr_t)__shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)w.block, from));
+            slot[hf] = __shfl_sync(0xffffffffu, w.slot, from);
         }
-        __syncwarp();
-        if (bytes)
-            bulk_load(sbase + st * L::bytes + part_to + half * 16 * row_bytes,
-                      reinterpret_cast<const uint8_t*>((uintptr_t)blk) + part_from + slot * row_bytes, bytes, bar);
+        dst += sbase;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int hf = c / (kChunks / 2);
+            const uint8_t* src = blk[hf] + slot[hf] * (D / 2) + (c % (kChunks / 2)) * 512 + lane * 16;
+            const bool in = (have >> hf) & 1u;
+            copy16(dst + c * 512 + lane * 16, src, in);
+            copy16(dst + L::v_codes + c * 512 + lane * 16, src + cb.v_codes, in);
+        }
+        if (lane < 4 * kScaleLanes)
+            copy16(dst + sc_to, (sc_half ? blk[1] : blk[0]) + sc_from + (sc_half ? slot[1] : slot[0]) * (D / 16),
+                   (have >> sc_half) & 1u);
     };
     Place place = look_up(begin);
     uint32_t there[2];                     // by batch parity: which half tiles hold keys
-    there[0] = __ballot_sync(0xffffffffu, place.block != nullptr);
+    there[0] = __ballot_sync(0xffffffffu, place.there);
     there[1] = 0;
     const int n_tiles = end - begin;
 #pragma unroll 1
-    for (int n = 0; n < min(kStages, n_tiles); ++n) issue(n, place);
+    for (int n = 0; n < kStages - 1; ++n) {   // at most kBatch - 1
+        if (n < n_tiles) issue(n, n * L::bytes, place, there[0] >> (2 * n));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
 
     const float to_log2 = p.scale * kLog2e;
     const DequantConst dq = dequant_const();
-    bool ok = true;
-    int at = begin, count = 0, failed = 0;
+    int at = begin, count = 0;
+    uint32_t st = 0;                       // the stage of tile `count`, in bytes
     ItemWalk<kTile> it;
     it.start(s_pre, p.c.R, begin);
-    int4 todo = make_int4(-1, 0, 0, 0);
+    AttendTodo todo = {};
 #pragma unroll 1
     while (at < end) {
         it.settle(p, kMB, s_pre, at);
@@ -352,6 +332,9 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
         }
         const int pos_lo = it.span.ctx + row0 / p.G;                                    // of the block's rows
         const int pos_hi = it.span.ctx + min(row0 + kMB - 1, n_rows - 1) / p.G;
+        // tiles from in_lo to in_hi are seen by every row to their ends
+        const int in_hi = min(pos_lo, it.span.keys - 1) - (kTile - 1);
+        const int in_lo = p.window > 0 ? (int)max(0ll, (long long)pos_hi - p.window + 1) : 0;
         float o[NB][MT][4], top[NB][2], sum[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -364,15 +347,27 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
         }
 #pragma unroll 1
         for (int u = u0; u < u1; ++u, ++count) {
-            const int st = count % kStages;
-            const uint8_t* tile = stages + st * L::bytes;
+            const uint8_t* tile = stages + st;
             const int key0 = it.span.key0(u);
-            if (ok) {
-                ok = __all_sync(0xffffffffu, a_wait(bar0 + 8u * st, (count / kStages) & 1u, p.status, wait_ns));
-                if (!ok) failed = count;
+            const uint32_t have = (((count / kBatch) & 1 ? there[1] : there[0]) >> (2 * (count % kBatch))) & 3u;
+            {
+                // the tile kStages - 1 further on into the stage that the last iteration left
+                const int next = count + kStages - 1;
+                if (next < n_tiles) {
+                    if (next % kBatch == 0) {
+                        place = look_up(begin + next);
+                        const uint32_t b = __ballot_sync(0xffffffffu, place.there);
+                        if ((next / kBatch) & 1) there[1] = b;
+                        else there[0] = b;
+                    }
+                    issue(next, st == 0 ? (kStages - 1) * L::bytes : st - L::bytes, place,
+                          ((next / kBatch) & 1 ? there[1] : there[0]) >> (2 * (next % kBatch)));
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+                __syncwarp();
             }
-            const uint32_t have = (there[(count / kBatch) & 1] >> (2 * (count % kBatch))) & 3u;
-            if (ok && have != 0) {
+            if (have != 0) {
                 // ---------------- scores of 32 keys: lane (g, i) gets keys g, g + 8 of each 16 by rows 2 i, 2 i + 1
                 float s[2][NB][4];
 #pragma unroll
@@ -412,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
                     }
                 }
                 // ---------------- mask; weights 2^(t - m + kShift)
-                const bool edge = key0 + kTile - 1 > pos_lo || key0 + kTile > it.span.keys || have != 3u ||
-                                  (p.window > 0 && (long long)key0 <= (long long)pos_hi - p.window);
+                const bool edge = key0 > in_hi || key0 < in_lo || have != 3u;
                 if (edge) {
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
@@ -521,18 +515,8 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
                         }
                 }
             }
-            // ---------------- the stage is free: the tile kStages further on into it
-            const int next = count + kStages;
+            st = st == (kStages - 1) * L::bytes ? 0 : st + L::bytes;
             __syncwarp();
-            if (ok && next < n_tiles) {
-                if (next % kBatch == 0) {
-                    place = look_up(begin + next);
-                    const uint32_t b = __ballot_sync(0xffffffffu, place.block != nullptr);
-                    if ((next / kBatch) & 1) there[1] = b;
-                    else there[0] = b;
-                }
-                issue(next, place);
-            }
         }
         // ---------------- the item's end in this run
         const bool whole = u0 == 0 && u1 == it.span.tiles;
@@ -571,82 +555,106 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
                 }
             }
         // an item that starts here and goes on: the next kernel joins its parts
-        if (u0 == 0 && u1 < it.span.tiles) todo = make_int4(it.r, it.q, (at + it.span.tiles - 1) / per - run_id + 1, slot);
+        if (u0 == 0 && u1 < it.span.tiles) {
+            todo.parts = (at + it.span.tiles - 1) / per - run_id + 1;
+            todo.slot = slot;
+            todo.first = it.span.first;
+            todo.head = h;
+            todo.row0 = row0;
+            todo.rows = min(kMB, n_rows - row0);
+        }
         at += u1 - u0;
     }
     if (lane == 0) ws.todo[run_id] = todo;
-    if (!ok)   // copies still in flight land before the warp leaves
-        for (int n = failed; n < min(failed + kStages, n_tiles); ++n) a_drain(bar0 + 8u * (n % kStages), (n / kStages) & 1u);
 }
 
 // Joins the parts of the items that started in the runs of one CTA and went on: a warp takes one run's item,
-// or, where an item has many parts, the whole CTA one row after the other. Also zeros the rows of the batch
+// or, where an item has many parts, the whole CTA one row after the other. Loads of several parts are in
+// flight at once: two dependent loads, of the run's note and of the parts, are what this costs. Also zeros the rows of the batch
 // that no request has.
+constexpr int kMergeMany = 8;   // parts of an item from which on the CTA shares it
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, AttendScratch ws, int kMB)
 {
     pdl_enter();
-    __shared__ float s_l[kWarps];
+    __shared__ float2 s_ml[kWarps];
     __shared__ float s_o[kWarps][D];
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, kAhead = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     struct Sum {
         float m, l, v[E];
     };
+    auto combine = [&](Sum& s, float m, float l, const float (&v)[E]) {
+        const float top = fmaxf(s.m, m), base = top == -INFINITY ? 0.f : top;
+        const float f = ex2(s.m - base), h = ex2(m - base);
+        s.m = top;
+        s.l = s.l * f + l * h;   // NaN of a row that is not finite stays
+#pragma unroll
+        for (int c = 0; c < E; ++c) s.v[c] = s.v[c] * f + v[c] * h;
+    };
     // part 0 is in its run's slot, the others first in the runs that follow
-    auto add = [&](const int4& todo, int run, int row, int k0, int step) {
-        auto at = [&](int k) { return ((size_t)(run + k) * 2 + (k == 0 ? todo.w : 0)) * kMB + row; };
+    auto add = [&](const AttendTodo& todo, int run, int row, int k0, int step) {
         Sum s = {};
         s.m = -INFINITY;
-        for (int k = lane; k < todo.z; k += 32) s.m = fmaxf(s.m, ws.ml[at(k)].x);
-        s.m = warp_max(s.m);
-        const float base = s.m == -INFINITY ? 0.f : s.m;
-#pragma unroll 4
-        for (int k = k0; k < todo.z; k += step) {
-            const size_t a = at(k);
-            const float2 ml = ws.ml[a];
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - base);
-            s.l = fmaf(f, ml.y, s.l);   // NaN of a row that is not finite stays
-            const float* src = ws.rows + a * D + lane * E;
+        for (int k = k0; k < todo.parts; k += step * kAhead) {
+            float2 ml[kAhead];
+            float v[kAhead][E];
 #pragma unroll
-            for (int c = 0; c < E; ++c) s.v[c] = fmaf(f, src[c], s.v[c]);
+            for (int x = 0; x < kAhead; ++x) {
+                const int kk = k + x * step;
+                ml[x] = make_float2(-INFINITY, 0.f);
+                if (kk < todo.parts) {
+                    const size_t a = ((size_t)(run + kk) * 2 + (kk == 0 ? todo.slot : 0)) * kMB + row;
+                    ml[x] = ws.ml[a];
+                    const float* src = ws.rows + a * D + lane * E;
+#pragma unroll
+                    for (int c = 0; c < E; ++c) v[x][c] = src[c];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < E; ++c) v[x][c] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) combine(s, ml[x].x, ml[x].y, v[x]);
         }
         return s;
     };
-    auto write = [&](const RequestSpan<kTile>& sp, int h, int rr, const Sum& s) {
+    auto write = [&](const AttendTodo& todo, int row, const Sum& s) {
         const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
-        const size_t dst = (size_t)(sp.first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
+        const int rr = todo.row0 + row;
+        const size_t dst = (size_t)(todo.first + rr / p.G) * p.Hq + todo.head * p.G + rr % p.G;
         T* out = static_cast<T*>(p.out) + dst * D + lane * E;
 #pragma unroll
         for (int c = 0; c < E; ++c) store1(out + c, s.v[c] * inv);
         if (lane == 0 && p.lse) p.lse[dst] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l) - kShift) * kLn2;
     };
-    for (int w = 0; w < kWarps; ++w) {
-        const int run = blockIdx.x * kWarps + w;
-        const int4 todo = ws.todo[run];
-        const bool many = todo.z > 2 * kWarps;
-        if (todo.x < 0 || (!many && w != warp)) continue;
-        const RequestSpan<kTile> sp = request_span<kTile>(p, todo.x, kMB, false);
-        const int h = todo.y / sp.blocks, row0 = (todo.y % sp.blocks) * kMB;
-        const int rows = min(kMB, sp.n_q * p.G - row0);
-        for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-            if (!many) {
-                write(sp, h, row0 + row, add(todo, run, row, 0, 1));
-                continue;
-            }
-            Sum s = add(todo, run, row, warp, kWarps);
-            __syncthreads();
-            if (lane == 0) s_l[warp] = s.l;
+    AttendTodo own = ws.todo[blockIdx.x * kWarps + warp];
+    if (own.parts > 0 && own.parts < kMergeMany)
+        for (int row = blockIdx.y; row < own.rows; row += gridDim.y)
+            write(own, row, add(own, blockIdx.x * kWarps + warp, row, 0, 1));
+    const int many = __syncthreads_or(own.parts >= kMergeMany);
+    if (many) {
+        for (int w = 0; w < kWarps; ++w) {
+            const int run = blockIdx.x * kWarps + w;
+            const AttendTodo todo = ws.todo[run];
+            if (todo.parts < kMergeMany) continue;
+            for (int row = blockIdx.y; row < todo.rows; row += gridDim.y) {
+                Sum s = add(todo, run, row, warp, kWarps);
+                __syncthreads();
+                if (lane == 0) s_ml[warp] = make_float2(s.m, s.l);
 #pragma unroll
-            for (int c = 0; c < E; ++c) s_o[warp][lane * E + c] = s.v[c];
-            __syncthreads();
-            if (warp != 0) continue;
-            for (int x = 1; x < kWarps; ++x) {
-                s.l += s_l[x];
+                for (int c = 0; c < E; ++c) s_o[warp][lane * E + c] = s.v[c];
+                __syncthreads();
+                if (warp != 0) continue;
+                for (int x = 1; x < kWarps; ++x) {
+                    float v[E];
 #pragma unroll
-                for (int c = 0; c < E; ++c) s.v[c] += s_o[x][lane * E + c];
+                    for (int c = 0; c < E; ++c) v[c] = s_o[x][lane * E + c];
+                    combine(s, s_ml[x].x, s_ml[x].y, v);
+                }
+                write(todo, row, s);
             }
-            write(sp, h, row0 + row, s);
         }
     }
     zero_rows<T>(p, D, (blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x, gridDim.x * gridDim.y * kThreads);
@@ -671,7 +679,7 @@ cudaError_t launch_rows(const AttendParams& p, const AttendScratch& ws, cudaStre
     const cudaError_t e = cudaFuncSetAttribute(cache_attend_mma_kernel<T, D, NB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attend_mma_kernel<T, D, NB>, dim3(grid_ctas(p)), dim3(kThreads), smem, s, p, ws, wait_limit_ns());
+    return launch_pdl(cache_attend_mma_kernel<T, D, NB>, dim3(grid_ctas(p)), dim3(kThreads), smem, s, p, ws);
 }
 
 template <typename T, int D>
@@ -715,12 +723,12 @@ size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base)
     const size_t ml = o;
     o = align_up(o + sizeof(float2) * runs * 2 * block_rows(p), 256);
     const size_t todo = o;
-    o = align_up(o + sizeof(int4) * runs, 256);
+    o = align_up(o + sizeof(AttendTodo) * runs, 256);
     if (ws) {
         char* b = static_cast<char*>(base);
         ws->rows = reinterpret_cast<float*>(b + rows);
         ws->ml = reinterpret_cast<float2*>(b + ml);
-        ws->todo = reinterpret_cast<int4*>(b + todo);
+        ws->todo = reinterpret_cast<AttendTodo*>(b + todo);
     }
     return o;
 }
