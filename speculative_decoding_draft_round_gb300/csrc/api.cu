@@ -740,7 +740,7 @@ dspark_status dspark_cache_attend_workspace_size(const dspark_cache_attend_args*
     if (st != DSPARK_OK) return st;
     if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
     const AttendParams p = attend_params(a);
-    *bytes = kStatusBytes + (attend_uses_mma(a, p) ? attend_mma_scratch(p, nullptr, nullptr) : 0);
+    *bytes = kStatusBytes + (attend_uses_mma(a, p) ? attend_scratch(p, nullptr, nullptr) : 0);
     return DSPARK_OK;
 }
 
@@ -759,9 +759,9 @@ dspark_status dspark_cache_attend(const dspark_cache_attend_args* a, void* ws, s
         return cuda_status(launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_simt(p, s); }));
     }
     AttendScratch scratch;
-    if (ws_bytes < kStatusBytes + attend_mma_scratch(p, &scratch, at<char>(ws, kStatusBytes))) return DSPARK_ERR_WORKSPACE;
+    if (ws_bytes < kStatusBytes + attend_scratch(p, &scratch, at<char>(ws, kStatusBytes))) return DSPARK_ERR_WORKSPACE;
     if (a->T == 0) return DSPARK_OK;
-    cudaError_t e = launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_mma(p, scratch, s); });
+    cudaError_t e = launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend(p, scratch, s); });
     if (e == cudaSuccess) e = launch(DSPARK_KERNEL_CACHE_MERGE, s, [&] { return launch_cache_merge(p, scratch, s); });
     return cuda_status(e);
 }

@@ -19,6 +19,7 @@ struct AttendScratch {
     float* rows;    // [runs][2][block rows][D] weighted sums
     float2* ml;     // [runs][2][block rows] maximum (log2 units) and sum of the weights
     AttendTodo* todo;   // [runs]
+    int runs, block_rows;
 };
 
 // A request's rows and the tiles its queries reach: the tiles of the sinks, then those from the first

@@ -22,6 +22,7 @@
 // tile's four parts cost more: their operands are uniform, a divergent loop of about 60 instructions a tile). A run that ends inside an item
 // leaves a part (maximum, sum, unnormalised rows) in the workspace, and a second small kernel joins the
 // parts in order.
+#include "attend_convert.cuh"
 #include "attend_plan.cuh"
 #include "cache.cuh"
 #include "internal.h"
@@ -34,8 +35,6 @@ constexpr int kTile = 32;                       // tokens of a tile
 constexpr int kWarps = 4;                       // of a CTA, each with a run of its own
 constexpr int kThreads = kWarps * 32;
 constexpr int kBatch = 16;                      // tiles whose places the lanes look up at once
-constexpr float kShift = 10.f;                  // weights are 2^(t - m + kShift) <= 2^15
-constexpr float kSlack = 5.f;                   // m is raised when a score passes it by this
 
 template <int D>
 struct Tile {
@@ -45,10 +44,9 @@ struct Tile {
     static constexpr uint32_t bytes = v_scales + kTile * D / 16;
 };
 
-// Variants: rows of a block, CTAs on an SM and the stages that shared memory then allows.
+// Variants: CTAs on an SM, and the stages that shared memory then allows.
 template <typename T, int D, int NB>
 struct Variant {
-    static constexpr int rows = 8 * NB;
     static constexpr int ctas = sizeof(T) == 4 ? (NB == 1 ? 3 : 2) : (NB == 1 ? 4 : 3);
     static constexpr int stages = ctas == 4 && D == 128 ? 2 : 3;
 };
@@ -76,48 +74,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
-
-// (w & mask) | or_bits in one instruction; or_bits in a register
-template <uint32_t kMask>
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t or_bits)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(kMask), "r"(or_bits));
-    return r;
-}
-
-// Constants of the conversion, kept in registers for a whole item: 1024 in both halves, 1032, 1/16, -72
-struct DequantConst {
-    uint32_t magic, off, sixteenth, m72;
-};
-
-__device__ __forceinline__ DequantConst dequant_const()
-{
-    DequantConst c;
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(c.magic));
-    asm volatile("mov.b32 %0, 0x64086408;" : "=r"(c.off));
-    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(c.sixteenth));
-    asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(c.m72));
-    return c;
-}
-
-// The 8 codes of a word times the scale pair s: h[j] = nibbles j and j + 4. 0x6400 | u is 1024 + u in fp16
-// and 0x6400 | 16 u is 1024 + 16 u; the differences and products are exact.
-__device__ __forceinline__ void dequant(uint32_t w, __half2 s, const DequantConst& c, uint32_t (&h)[4])
-{
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t lo = and_or<0x000F000Fu>(w, c.magic), hi = and_or<0x00F000F0u>(w, c.magic);
-        h[2 * k] = as_u32(__hmul2(__hsub2(as_half2(lo), as_half2(c.off)), s));
-        h[2 * k + 1] = as_u32(__hmul2(__hfma2(as_half2(hi), as_half2(c.sixteenth), as_half2(c.m72)), s));
-        w >>= 8;
-    }
-}
-
-__device__ __forceinline__ uint32_t pack(float a, float b) { return as_u32(__floats2half2_rn(a, b)); }
 
 // the rounding error of pack(a, b), packed
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi)
@@ -305,10 +261,7 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const unsigned odds = __ballot_sync(0xffffffffu, odd && real);
             const bool mine = ((odds >> (lane & 28)) & 15u) != 0;
-            // the row's largest element to 2^12 .. 2^13
-            const int ex = (int)(__float_as_uint(top) >> 23);
-            const float up = __uint_as_float((uint32_t)min(266 - ex, 254) << 23);
-            const float f = fmaxf(to_log2 / up, 1e-37f);   // 0 times a masked score would be NaN
+            const float up = row_up((int)(__float_as_uint(top) >> 23)), f = row_factor(to_log2, up);
             const bool keep = real && !mine;
 #pragma unroll
             for (int c = 0; c < CH; ++c) x[c] = keep ? x[c] * up : 0.f;
@@ -575,12 +528,13 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
 constexpr int kMergeMany = 8;   // parts of an item from which on the CTA shares it
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, AttendScratch ws, int kMB)
+__global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, AttendScratch ws)
 {
     pdl_enter();
     __shared__ float2 s_ml[kWarps];
     __shared__ float s_o[kWarps][D];
     constexpr int E = D / 32, kAhead = 8;
+    const int kMB = ws.block_rows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     struct Sum {
         float m, l, v[E];
@@ -629,7 +583,8 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, A
         for (int c = 0; c < E; ++c) store1(out + c, s.v[c] * inv);
         if (lane == 0 && p.lse) p.lse[dst] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l) - kShift) * kLn2;
     };
-    AttendTodo own = ws.todo[blockIdx.x * kWarps + warp];
+    AttendTodo own = {};
+    if ((int)blockIdx.x * kWarps + warp < ws.runs) own = ws.todo[blockIdx.x * kWarps + warp];
     if (own.parts > 0 && own.parts < kMergeMany)
         for (int row = blockIdx.y; row < own.rows; row += gridDim.y)
             write(own, row, add(own, blockIdx.x * kWarps + warp, row, 0, 1));
@@ -637,6 +592,7 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, A
     if (many) {
         for (int w = 0; w < kWarps; ++w) {
             const int run = blockIdx.x * kWarps + w;
+            if (run >= ws.runs) break;
             const AttendTodo todo = ws.todo[run];
             if (todo.parts < kMergeMany) continue;
             for (int row = blockIdx.y; row < todo.rows; row += gridDim.y) {
@@ -691,10 +647,9 @@ cudaError_t launch_mma(const AttendParams& p, const AttendScratch& ws, cudaStrea
 template <typename T, int D>
 cudaError_t launch_merge(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
 {
-    const int MB = block_rows(p);
-    const long long rows = (long long)p.max_q * p.G;
-    return launch_pdl(cache_merge_kernel<T, D>, dim3(grid_ctas(p), (unsigned)(rows < MB ? rows : MB)), dim3(kThreads), 0, s,
-                      p, ws, MB);
+    const long long most = (long long)p.max_q * p.G < ws.block_rows ? (long long)p.max_q * p.G : ws.block_rows;
+    return launch_pdl(cache_merge_kernel<T, D>, dim3(cdiv(ws.runs, kWarps), (unsigned)(most < 32 ? most : 32)), dim3(kThreads), 0,
+                      s, p, ws);
 }
 
 template <typename T>
@@ -714,14 +669,16 @@ bool attend_mma_supported(const AttendParams& p)
     return rows < (1ll << 30) && (double)p.c.R * p.c.Hkv * (double)(rows / block_rows(p) + 1) * (double)tiles < 2147483647.0;
 }
 
-size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base)
+size_t attend_scratch(const AttendParams& p, AttendScratch* ws, void* base)
 {
-    const size_t runs = (size_t)grid_ctas(p) * kWarps;
+    const bool tc = attend_tc_supported(p);
+    const int MB = tc ? attend_tc_block_rows() : block_rows(p);
+    const size_t runs = tc ? num_sms() : (size_t)grid_ctas(p) * kWarps;
     size_t o = 0;
     const size_t rows = o;
-    o = align_up(o + sizeof(float) * runs * 2 * block_rows(p) * p.c.D, 256);
+    o = align_up(o + sizeof(float) * runs * 2 * MB * p.c.D, 256);
     const size_t ml = o;
-    o = align_up(o + sizeof(float2) * runs * 2 * block_rows(p), 256);
+    o = align_up(o + sizeof(float2) * runs * 2 * MB, 256);
     const size_t todo = o;
     o = align_up(o + sizeof(AttendTodo) * runs, 256);
     if (ws) {
@@ -729,15 +686,18 @@ size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base)
         ws->rows = reinterpret_cast<float*>(b + rows);
         ws->ml = reinterpret_cast<float2*>(b + ml);
         ws->todo = reinterpret_cast<AttendTodo*>(b + todo);
+        ws->runs = (int)runs;
+        ws->block_rows = MB;
     }
     return o;
 }
 
-cudaError_t launch_cache_attend_mma(const AttendParams& p0, const AttendScratch& ws, cudaStream_t s)
+cudaError_t launch_cache_attend(const AttendParams& p0, const AttendScratch& ws, cudaStream_t s)
 {
     AttendParams p = p0;
     const bool bf = p.dtype == DSPARK_BF16;
     p.q_aligned = bf ? q_aligned<__nv_bfloat16>(p) : q_aligned<float>(p);
+    if (attend_tc_supported(p)) return launch_cache_attend_tc(p, ws, s);
     const cudaError_t e =
         p.c.D == 64 ? (bf ? launch_mma<__nv_bfloat16, 64>(p, ws, s) : launch_mma<float, 64>(p, ws, s))
                     : (bf ? launch_mma<__nv_bfloat16, 128>(p, ws, s) : launch_mma<float, 128>(p, ws, s));

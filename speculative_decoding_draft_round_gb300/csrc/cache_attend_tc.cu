@@ -1,0 +1,744 @@
+// cache_attend_tc.cu -- attention of the flat batch over the 4-bit cache on the fifth-generation tensor
+// cores (dspark_cache_attend, bf16, D = 64 or 128, where requests have many rows).
+//
+//   out = sum_i 2^(t_i - m) v_i / sum_i 2^(t_i - m),  t_i = log2(e) scale q . k_i, in one pass over the keys.
+//
+// An item is 128 rows (query heads of consecutive queries) of one request and key / value head, a tile 128
+// tokens. The items' tiles form one line that is cut into equal runs, one a CTA and SM, whatever the lengths
+// are; a block's tiles are those its own rows reach. Per tile, by warp:
+//   8 - 15  turn codes into fp16 (exact: scales have 8 bits) in shared memory: K by token, V transposed
+//           by channel, both K-major with the 128-byte swizzle; the next tile's codes are loaded before.
+//           A thread takes 8 tokens of 8 value channels, so the transposition is its choice of registers.
+//   0       issues S = Q K^T (128 x 128 x D, operands in shared memory) and O += P V (128 x D x 128, P in
+//           tensor memory), S of a tile before P V of the one before.
+//   4 - 7   one row a thread: the row's maximum, weights 2^(t - m + 10) as fp16 into the tensor memory that
+//           S had, their sum. m only has to be near the maximum: O is rescaled when a score passes m by 2^5.
+//   2, 3    rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory.
+// All waits are bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT and ends the CTA's
+// loops, its MMAs land, and tensor memory is freed.
+#include "attend_convert.cuh"
+#include "attend_plan.cuh"
+#include "cache.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kTile = 128;                     // tokens
+constexpr int kMB = 128;                       // rows of a block
+constexpr int kThreads = 512;
+constexpr int kWarpMma = 0, kWarpAlloc = 1, kWarpQ = 2, kWarpSoft = 4, kWarpConv = 8;
+constexpr unsigned long long kDrainNs = 4000000000ull;
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;   // S of even tiles at 0, of odd tiles at 128, O at 256
+// instruction descriptors, kind::f16: D fp32, A and B fp16, both K-major, M = 128
+constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kMB >> 4) << 24);
+template <int D>
+constexpr uint32_t kIdescO = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kMB >> 4) << 24);
+
+// ------------------------------------------------------------------ the line of tiles
+
+struct Request {
+    int first, n_q, ctx, keys, n_rows, blocks;
+};
+
+__device__ __forceinline__ Request request_of(const AttendParams& p, int r, bool report)
+{
+    const RequestSpan<kTile> s = request_span<kTile>(p, r, kMB, report);
+    return Request{s.first, s.n_q, s.ctx, s.keys, s.n_q * p.G, s.blocks};
+}
+
+// The tiles of one block: those of the sinks, then those from its first query's window to its last query's
+// own key (one range when they touch).
+struct BlockTiles {
+    int tiles, sink_tiles, lo_tile;
+    __device__ __forceinline__ int key0(int u) const { return (u < sink_tiles ? u : lo_tile + u - sink_tiles) * kTile; }
+};
+
+__device__ __forceinline__ BlockTiles block_tiles(const AttendParams& p, const Request& q, int b)
+{
+    const int j0 = b * kMB / p.G, j1 = min((b + 1) * kMB - 1, q.n_rows - 1) / p.G;
+    const int keys = (int)min((long long)q.keys, (long long)q.ctx + j1 + 1);
+    BlockTiles t;
+    const int all = (keys + kTile - 1) / kTile;
+    t.sink_tiles = t.lo_tile = 0;
+    t.tiles = all;
+    if (p.window > 0) {
+        const int from = (int)max(0ll, (long long)q.ctx + j0 - p.window + 1);
+        const int sink_tiles = (int)(((long long)min(p.sinks, from) + kTile - 1) / kTile), lo = from / kTile;
+        if (sink_tiles < lo) {
+            t.sink_tiles = sink_tiles;
+            t.lo_tile = lo;
+            t.tiles = sink_tiles + max(0, all - lo);
+        }
+    }
+    t.tiles = max(t.tiles, 1);
+    return t;
+}
+
+// Tiles of one head of request q; by a whole warp, or by one thread.
+template <bool kWarpWide>
+__device__ __forceinline__ int head_tiles(const AttendParams& p, const Request& q)
+{
+    int sum = 0;
+    for (int b = kWarpWide ? (threadIdx.x & 31) : 0; b < q.blocks; b += kWarpWide ? 32 : 1) sum += block_tiles(p, q, b).tiles;
+    return kWarpWide ? __reduce_add_sync(0xffffffffu, sum) : sum;
+}
+
+// pre[r] = tiles before request r's; the total is returned. All threads of the CTA.
+__device__ __forceinline__ int plan(const AttendParams& p, int* pre, int* scan, bool report)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.c.R;
+    if (R <= 4 * kThreads / 32) {   // few requests, perhaps of many blocks: a warp each
+        for (int r = warp; r < R; r += kThreads / 32) {
+            const int n = head_tiles<true>(p, request_of(p, r, report && lane == 0)) * p.c.Hkv;
+            if (lane == 0) pre[r + 1] = n;
+        }
+    } else {
+        for (int r = tid; r < R; r += kThreads) pre[r + 1] = head_tiles<false>(p, request_of(p, r, report)) * p.c.Hkv;
+    }
+    __syncthreads();
+    const int each = (R + kThreads - 1) / kThreads, r0 = min(tid * each, R), r1 = min(r0 + each, R);
+    int sum = 0;
+    for (int r = r0; r < r1; ++r) sum += pre[r + 1];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int before = inc - sum, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    if (tid == 0) pre[0] = 0;
+    for (int r = r0; r < r1; ++r) {
+        before += pre[r + 1];
+        pre[r + 1] = before;
+    }
+    __syncthreads();
+    return total;
+}
+
+// Items of a run one after the other: request r, head h, block b, from tile u on. Warp-wide.
+struct Walk {
+    int r = 0, h = 0, b = 0, u = 0;
+    Request q;
+    BlockTiles t;
+    __device__ void start(const AttendParams& p, const int* pre, int at)
+    {
+        int lo = 0, hi = p.c.R;   // the request with pre[r] <= at < pre[r + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= at) lo = mid;
+            else hi = mid;
+        }
+        r = lo;
+        q = request_of(p, r, false);
+        const int per_head = (pre[r + 1] - pre[r]) / p.c.Hkv;
+        h = (at - pre[r]) / per_head;
+        int rem = (at - pre[r]) % per_head;
+        for (int b0 = 0; b0 < q.blocks; b0 += 32) {
+            const int lane = threadIdx.x & 31;
+            const int n = b0 + lane < q.blocks ? block_tiles(p, q, b0 + lane).tiles : 0;
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, rem < inc);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                b = b0 + k;
+                u = rem - __shfl_sync(0xffffffffu, inc - n, k);
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        t = block_tiles(p, q, b);
+    }
+    __device__ void advance(const AttendParams& p, const int* pre)
+    {
+        u = 0;
+        if (++b == q.blocks) {
+            b = 0;
+            if (++h == p.c.Hkv) {
+                h = 0;
+                do ++r;
+                while (r + 1 < p.c.R && pre[r + 1] == pre[r]);
+                q = request_of(p, r, false);
+            }
+        }
+        t = block_tiles(p, q, b);
+    }
+};
+
+// ------------------------------------------------------------------ waits
+
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
+                                       unsigned long long limit_ns)
+{
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (globaltimer() - t0 > limit_ns) {
+            *abort = 1;
+            raise_status(status, DSPARK_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Warp-wide: true where every lane saw the phase end.
+struct Waits {
+    volatile int* abort;
+    int* status;
+    unsigned long long limit_ns;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
+    {
+        const bool ok = mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
+        return __all_sync(0xffffffffu, ok);
+    }
+};
+
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < kDrainNs) {
+    }
+}
+
+__device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Barriers, pairs by the parity of the tile (Q: of the item) first. A waiter is never two phases behind: each
+// phase needs an arrival that the waiter, or one that waits for it, makes after it saw the phase before.
+enum Bar {
+    kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kQEmpty = 10, kSFull = 12, kPFull = 14,
+    kPvDone = 16,   // O += P V of a tile has landed
+    kODone = 17,    // that of an item's last tile in this run
+    kOFree = 18,    // the item's rows are out of O
+    kFin = 19, kBars = 20
+};
+
+// The codes of a tile that one converting thread takes: 64 (32 for D = 64) channels of one key, and 8 tokens
+// of 8 value channels.
+template <int D>
+struct Raw {
+    uint32_t k[D / 16];
+    uint32_t ks;      // the scales of its one or two groups
+    uint32_t v[8];
+    uint4 vs;         // of the 8 tokens
+    bool valid;       // the value tokens' page is there
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attend_tc_kernel(AttendParams p, AttendScratch ws, unsigned long long wait_ns)
+{
+    constexpr uint32_t kOperand = 128 * D * 2;   // bytes of Q, K or V of a tile
+    constexpr int kVWarps = D == 128 ? 8 : 4;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t q_buf = smem_addr(smem), k_buf = q_buf + 2 * kOperand, v_buf = q_buf + 4 * kOperand;
+    int* s_pre = reinterpret_cast<int*>(smem + 6 * kOperand);
+    __shared__ uint64_t s_bar[kBars];
+    __shared__ float s_fac[2][kMB];
+    __shared__ __align__(8) uint8_t s_valid[4][8];   // of tile n & 3: which runs of 16 tokens hold keys
+    __shared__ int s_scan[kThreads / 32];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bar0 = smem_addr(s_bar);
+    auto bar = [&](int k) { return bar0 + 8u * k; };
+    if (tid == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(kKFull + b), 8);
+            mbar_init(bar(kVFull + b), kVWarps);
+            mbar_init(bar(kKEmpty + b), 1);
+            mbar_init(bar(kVEmpty + b), 1);
+            mbar_init(bar(kQFull + b), 2);
+            mbar_init(bar(kQEmpty + b), 5);   // its MMAs, and the four warps that read the factors
+            mbar_init(bar(kSFull + b), 2);    // its MMAs, and the issuing thread for what it saw (s_valid)
+            mbar_init(bar(kPFull + b), 4);
+        }
+        mbar_init(bar(kPvDone), 1);
+        mbar_init(bar(kODone), 1);
+        mbar_init(bar(kOFree), 4);
+        mbar_init(bar(kFin), 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == kWarpAlloc) tc5::alloc(&s_tmem, kTmemCols);
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+    pdl_trigger();
+    const int total = plan(p, s_pre, s_scan, blockIdx.x == 0);
+    const int per = (total + gridDim.x - 1) / gridDim.x;
+    const int begin = (int)min((long long)blockIdx.x * per, (long long)total);
+    const int end = min(begin + per, total);
+    const Waits wait{&s_abort, p.status, wait_ns};
+    AttendTodo todo = {};
+
+    if (begin < end && warp == kWarpMma) {
+        // ---------------- MMA issuer
+        Walk w;
+        w.start(p, s_pre, begin);
+        bool ok = true, prev_first = false, prev_last = false;
+        int n = 0, prev_item = 0;
+        // O (+)= P V of tile m of the run; `first` and `last` tile of the item in this run
+        auto pv = [&](int m, bool first, bool last, int item) {
+            const int b = m & 1;
+            if (!wait(bar(kPFull + b), (m >> 1) & 1u)) return false;
+            if (!wait(bar(kVFull + b), (m >> 1) & 1u)) return false;
+            if (first && item > 0 && !wait(bar(kOFree), (item - 1) & 1u)) return false;
+            tc5::fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    tc5::mma_ts(tmem + kTmemO, tmem + b * 128 + kk * 8,
+                                tc5::desc_sw128(v_buf + b * kOperand + (kk / 4) * (D * 128) + (kk % 4) * 32), kIdescO<D>,
+                                !(first && kk == 0));
+                tc5::commit(bar(kPvDone));
+                tc5::commit(bar(kVEmpty + b));
+                if (last) tc5::commit(bar(kODone));
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int at = begin, item = 0; at < end && ok; ++item) {
+            const int u0 = w.u, u1 = min(w.t.tiles, u0 + (end - at));
+            for (int u = u0; u < u1; ++u, ++n) {
+                const int b = n & 1;
+                ok = wait(bar(kKFull + b), (n >> 1) & 1u);
+                if (ok && u == u0) ok = wait(bar(kQFull + (item & 1)), (item >> 1) & 1u);
+                if (ok && n >= 2) ok = wait(bar(kPvDone), n & 1u);   // of tile n - 2, whose weights S replaces
+                if (!ok) break;
+                tc5::fence_after();
+                if (lane == 0) {
+                    const uint32_t qa = q_buf + (item & 1) * kOperand, kb = k_buf + b * kOperand;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
+                        tc5::mma_ss(tmem + b * 128, tc5::desc_sw128(qa + off), tc5::desc_sw128(kb + off), kIdescS, kk != 0);
+                    }
+                    tc5::commit(bar(kSFull + b));
+                    tc5::commit(bar(kKEmpty + b));
+                    if (u + 1 == u1) tc5::commit(bar(kQEmpty + (item & 1)));
+                    mbar_arrive(bar(kSFull + b));
+                }
+                __syncwarp();
+                if (n > 0) ok = pv(n - 1, prev_first, prev_last, prev_item);
+                if (!ok) break;
+                prev_first = u == u0;
+                prev_last = u + 1 == u1;
+                prev_item = item;
+            }
+            at += u1 - u0;
+            if (at < end) w.advance(p, s_pre);
+        }
+        if (ok && n > 0) pv(n - 1, prev_first, prev_last, prev_item);
+        // every MMA issued above lands before tensor memory is freed
+        if (lane == 0) {
+            tc5::commit(bar(kFin));
+            drain(bar(kFin), 0u);
+        }
+        __syncwarp();
+    } else if (begin < end && (warp == kWarpQ || warp == kWarpQ + 1)) {
+        // ---------------- rows of q, one item ahead
+        Walk w;
+        w.start(p, s_pre, begin);
+        const float to_log2 = p.scale * kLog2e;
+        for (int at = begin, item = 0; at < end; ++item) {
+            const int u1 = min(w.t.tiles, w.u + (end - at)), b = item & 1;
+            if (item >= 2 && !wait(bar(kQEmpty + b), ((item >> 1) - 1) & 1u)) break;
+            for (int row = tid - kWarpQ * 32; row < kMB; row += 64) {
+                const int rr = w.b * kMB + row;
+                const bool real = rr < w.q.n_rows;
+                uint4 raw[D / 8];
+                if (real) {
+                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.q.first + rr / p.G) * p.q_ts +
+                                               (int64_t)(w.h * p.G + rr % p.G) * p.q_hs;
+                    if (p.q_aligned) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) raw[c] = reinterpret_cast<const uint4*>(src)[c];
+                    } else {
+                        const uint16_t* s16 = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] = s16[c * 8 + 2 * e] | ((uint32_t)s16[c * 8 + 2 * e + 1] << 16);
+                            raw[c] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
+                }
+                uint32_t top = 0;   // magnitudes of bf16 order like their bits
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+                }
+                const bool bad = top >= 0x7F80u;   // an infinity or NaN
+                if (bad) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
+                const float up = row_up((int)(top >> 7));
+                // a row that is not finite has the factor NaN and so weights, sum and result
+                s_fac[b][row] = bad ? NAN : row_factor(to_log2, up);
+                const uint32_t dst = q_buf + b * kOperand + row * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[2 * e] = bad ? 0.f : __uint_as_float(x[e] << 16) * up;
+                        f[2 * e + 1] = bad ? 0.f : __uint_as_float(x[e] & 0xFFFF0000u) * up;
+                    }
+                    // in the order of converted codes: channels 0 4 1 5 2 6 3 7
+                    store16(dst + (c / 8) * 16384 + (((c % 8) ^ (row & 7)) * 16), pack(f[0], f[4]), pack(f[1], f[5]),
+                            pack(f[2], f[6]), pack(f[3], f[7]));
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kQFull + b));
+            at += u1 - w.u;
+            if (at < end) w.advance(p, s_pre);
+        }
+    } else if (begin < end && warp >= kWarpConv) {
+        // ---------------- codes to fp16
+        const int cw = warp - kWarpConv;
+        const int k_tok = (cw & 3) * 32 + lane, k_half = cw >> 2;
+        const bool has_v = cw < kVWarps;
+        const int v_tg = (D == 128 ? cw >> 2 : (cw >> 1) & 1) * 8 + (lane & 7);     // 8 tokens
+        const int v_word = (D == 128 ? cw & 3 : cw & 1) * 4 + (lane >> 3);          // 8 channels
+        const CacheBlock cb = cache_block(p.c.page_size, D);
+        const DequantConst dq = dequant_const();
+        Walk w;
+        w.start(p, s_pre, begin);
+        int at = begin, u = w.u;
+        // the codes of the walk's tile u
+        auto load = [&](Raw<D>& x) {
+            const int key0 = w.t.key0(u), P = p.c.page_size;
+            const int32_t* row = p.c.table + (size_t)w.r * p.c.table_width;
+            const int kk = key0 + k_tok, vk = key0 + v_tg * 8;
+            int k_page = -1, v_page = -1;
+            if (kk < w.q.keys) k_page = row[kk / P];
+            if (vk < w.q.keys) v_page = row[vk / P];
+            const bool k_in = k_page >= 0 && k_page < p.c.n_pages;
+            x.valid = v_page >= 0 && v_page < p.c.n_pages;
+            if ((kk < w.q.keys && !k_in) || (vk < w.q.keys && !x.valid)) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+            x.ks = 0;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) x.k[c] = 0;
+            if (k_in) {
+                const uint8_t* blk = cache_page_block(p.c, k_page, w.h, cb.bytes);
+                const int slot = kk % P;
+                const uint4* src = reinterpret_cast<const uint4*>(blk + slot * (D / 2) + k_half * (D / 4));
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 y = src[c];
+                    x.k[4 * c] = y.x;
+                    x.k[4 * c + 1] = y.y;
+                    x.k[4 * c + 2] = y.z;
+                    x.k[4 * c + 3] = y.w;
+                }
+                const uint8_t* sc = blk + cb.k_scales + slot * (D / 16);
+                if (D == 128) x.ks = *reinterpret_cast<const uint32_t*>(sc + k_half * 4);
+                else x.ks = *reinterpret_cast<const uint16_t*>(sc + k_half * 2);
+            }
+            x.vs = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x.v[c] = 0;
+            if (x.valid && has_v) {
+                const uint8_t* blk = cache_page_block(p.c, v_page, w.h, cb.bytes);
+                const int slot = vk % P;
+                const uint8_t* src = blk + cb.v_codes + slot * (D / 2) + v_word * 4;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x.v[c] = *reinterpret_cast<const uint32_t*>(src + c * (D / 2));
+                x.vs = *reinterpret_cast<const uint4*>(blk + cb.v_scales + v_scale_at(slot, v_word / 4, D / kCacheGroup));
+                // what no token wrote may be anything: its scale becomes 0
+                const int left = w.q.keys - vk;
+                if (left < 8) {
+                    x.vs.x &= keep_halves(left);
+                    x.vs.y &= keep_halves(left - 2);
+                    x.vs.z &= keep_halves(left - 4);
+                    x.vs.w &= keep_halves(left - 6);
+                }
+            }
+        };
+        Raw<D> now, next;
+        load(now);
+        const int tiles = end - begin;
+        for (int n = 0; n < tiles; ++n) {
+            const int b = n & 1;
+            ++at;
+            if (at < end) {   // the run's next tile
+                if (++u == w.t.tiles) {
+                    w.advance(p, s_pre);
+                    u = 0;
+                }
+                load(next);
+            }
+            if (n >= 2 && !wait(bar(kKEmpty + b), ((n >> 1) - 1) & 1u)) break;
+            {
+                const uint32_t dst = k_buf + b * kOperand + (D == 128 ? k_half * 16384 : 0) + k_tok * 128;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t h[4];
+                    const __half2 s = c < 4 ? __low2half2(as_half2(now.ks)) : __high2half2(as_half2(now.ks));
+                    dequant(now.k[c], s, dq, h);
+                    const int unit = D == 128 ? c : k_half * 4 + c;
+                    store16(dst + ((unit ^ (k_tok & 7)) * 16), h[0], h[1], h[2], h[3]);
+                }
+                if (has_v && v_word == 0 && (v_tg & 1) == 0) s_valid[n & 3][v_tg >> 1] = now.valid;
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kKFull + b));
+            }
+            if (has_v) {
+                if (n >= 2 && !wait(bar(kVEmpty + b), ((n >> 1) - 1) & 1u)) break;
+                const uint32_t dst = v_buf + b * kOperand + (v_tg >> 3) * (D * 128) + v_word * 8 * 128;
+                const uint32_t sc[4] = {now.vs.x, now.vs.y, now.vs.z, now.vs.w};
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {   // channels 4 z .. of the word
+                    uint32_t h[4][4];           // [pair of tokens][channel]
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        dequant(__byte_perm(now.v[2 * m], now.v[2 * m + 1], z == 0 ? 0x5410u : 0x7632u), as_half2(sc[m]), dq, h[m]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int d = z * 4 + c;
+                        store16(dst + d * 128 + (((v_tg & 7) ^ d) * 16), h[0][c], h[1][c], h[2][c], h[3][c]);
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kVFull + b));
+            }
+            now = next;
+        }
+    } else if (begin < end && warp >= kWarpSoft) {
+        // ---------------- weights: one row a thread
+        const int row = tid - kWarpSoft * 32;
+        const uint32_t lanes = tmem + ((uint32_t)((warp - kWarpSoft) * 32) << 16);
+        Walk w;
+        w.start(p, s_pre, begin);
+        bool ok = true;
+        int n = 0;
+        for (int at = begin, item = 0; at < end; ++item) {
+            const int u0 = w.u, u1 = min(w.t.tiles, u0 + (end - at));
+            const int row0 = w.b * kMB, rr = row0 + row;
+            const bool any = row0 + (warp - kWarpSoft) * 32 < w.q.n_rows;   // the warp has rows of the item
+            ok = wait(bar(kQFull + (item & 1)), (item >> 1) & 1u);
+            if (!ok) break;
+            const float fac = s_fac[item & 1][row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kQEmpty + (item & 1)));
+            // keys this row sees: from lo (and below the sinks) to hi
+            const int own = w.q.ctx + min(rr, w.q.n_rows - 1) / p.G;
+            const int hi = min(own, w.q.keys - 1);
+            const int lo = p.window > 0 ? (int)max(0ll, (long long)own - p.window + 1) : 0;
+            // tiles from in_lo to in_hi are seen by every row to their ends
+            const int pos_lo = w.q.ctx + row0 / p.G, pos_hi = w.q.ctx + min(row0 + kMB - 1, w.q.n_rows - 1) / p.G;
+            const int in_hi = min(pos_lo, w.q.keys - 1) - (kTile - 1);
+            const int in_lo = p.window > 0 ? (int)max(0ll, (long long)pos_hi - p.window + 1) : 0;
+            float top = -INFINITY, sum = 0.f;
+            for (int u = u0; u < u1; ++u, ++n) {
+                const int b = n & 1, key0 = w.t.key0(u);
+                ok = wait(bar(kSFull + b), (n >> 1) & 1u);
+                if (!ok) break;
+                if (any) {
+                    tc5::fence_after();
+                    const uint32_t s_at = lanes + b * 128;
+                    const unsigned long long valid = *reinterpret_cast<const unsigned long long*>(s_valid[n & 3]);
+                    const bool edge = key0 > in_hi || key0 < in_lo || valid != 0x0101010101010101ull;
+                    auto seen = [&](int c) {   // bit j: key key0 + 32 c + j is visible
+                        const int base = key0 + c * 32;
+                        const uint32_t v = ((valid >> (16 * c)) & 1u ? 0xFFFFu : 0u) |
+                                           ((valid >> (16 * c + 8)) & 1u ? 0xFFFF0000u : 0u);
+                        return below(hi + 1 - base) & (~below(lo - base) | below(p.window > 0 ? p.sinks - base : 0)) & v;
+                    };
+                    float mx = -INFINITY;
+                    uint32_t x[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tc5::ld32(s_at + c * 32, x);
+                        if (edge) {
+                            const uint32_t see = seen(c);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, (see >> j) & 1u ? __uint_as_float(x[j]) : -INFINITY);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+                        }
+                    }
+                    mx *= fac;
+                    if (u == u0) {
+                        top = mx == mx ? mx : -INFINITY;   // NaN: a row that is not finite
+                    } else if (__any_sync(0xffffffffu, mx > top + kSlack)) {
+                        const float m = fmaxf(mx, top);
+                        const float keep = m == top ? 1.f : ex2(top - m);
+                        top = m;
+                        sum *= keep;
+                        ok = wait(bar(kPvDone), (n - 1) & 1u);
+                        if (!ok) break;
+                        tc5::fence_after();
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            tc5::ld16(lanes + kTmemO + c * 16, y);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * keep);
+                            tc5::st16(lanes + kTmemO + c * 16, y);
+                        }
+                    }
+                    const float base = top == -INFINITY ? 0.f : kShift - top;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tc5::ld32(s_at + c * 32, x);
+                        if (edge) {
+                            const uint32_t see = seen(c);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = (see >> j) & 1u ? x[j] : 0xFF800000u;   // -infinity
+                        }
+                        uint32_t y[16];
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float e0 = ex2(fmaf(__uint_as_float(x[2 * j]), fac, base));
+                            const float e1 = ex2(fmaf(__uint_as_float(x[2 * j + 1]), fac, base));
+                            s0 += e0;
+                            s1 += e1;
+                            y[j] = pack(e0, e1);
+                        }
+                        sum += s0 + s1;
+                        tc5::st16(s_at + c * 16, y);   // over scores that this thread has read
+                    }
+                    tc5::wait_st();
+                    tc5::fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kPFull + b));
+            }
+            if (!ok) break;
+            // ---------------- the item's end in this run
+            const bool whole = u0 == 0 && u1 == w.t.tiles;
+            const int slot = at == begin ? 0 : 1;   // a run's first item, or its last
+            // warps without rows wait too: their arrival below must not count for the item before
+            ok = wait(bar(kODone), item & 1u);
+            if (!ok) break;
+            if (any) {
+                tc5::fence_after();
+                const bool real = rr < w.q.n_rows;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const size_t part = ((size_t)blockIdx.x * 2 + slot) * kMB + row;
+                const size_t dst = (size_t)(w.q.first + rr / p.G) * p.Hq + w.h * p.G + rr % p.G;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t x[32];
+                    tc5::ld32(lanes + kTmemO + c * 32, x);
+                    if (real && whole) {
+                        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + dst * D + c * 32);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]) * inv,
+                                                                               __uint_as_float(x[8 * k + 2 * e + 1]) * inv);
+                                y[e] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                            o[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    } else if (real) {
+                        uint4* o = reinterpret_cast<uint4*>(ws.rows + part * D + c * 32);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (real) {
+                    if (!whole) ws.ml[part] = make_float2(top, sum);
+                    else if (p.lse) p.lse[dst] = sum == 0.f ? -INFINITY : (top + log2f(sum) - kShift) * kLn2;
+                }
+                tc5::fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kOFree));
+            // an item that starts here and goes on: the next kernel joins its parts
+            if (u0 == 0 && u1 < w.t.tiles) {
+                todo.parts = (at + w.t.tiles - 1) / per - (int)blockIdx.x + 1;
+                todo.slot = slot;
+                todo.first = w.q.first;
+                todo.head = w.h;
+                todo.row0 = row0;
+                todo.rows = min(kMB, w.q.n_rows - row0);
+            }
+            at += u1 - u0;
+            if (at < end) w.advance(p, s_pre);
+        }
+        if (!ok) todo.parts = 0;
+    }
+    if (tid == kWarpSoft * 32) ws.todo[blockIdx.x] = todo;
+    tc5::fence_before();
+    __syncthreads();
+    if (warp == kWarpAlloc) {
+        tc5::fence_after();
+        tc5::dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+size_t tc_smem(int R) { return 6 * 128 * D * 2 + sizeof(int) * (R + 1) + 1024; }
+
+template <int D>
+cudaError_t launch_tc(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
+{
+    const size_t smem = tc_smem<D>(p.c.R);
+    const cudaError_t e =
+        cudaFuncSetAttribute(cache_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_attend_tc_kernel<D>, dim3(ws.runs), dim3(kThreads), smem, s, p, ws, wait_limit_ns());
+}
+
+}  // namespace
+
+bool attend_tc_supported(const AttendParams& p)
+{
+    if (p.dtype != DSPARK_BF16 || (p.c.D != 64 && p.c.D != 128)) return false;
+    const long long rows = (long long)p.max_q * p.G;
+    if (rows <= 16 || rows >= (1ll << 30)) return false;
+    if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - 2048) return false;
+    // tiles are counted in 32 bits
+    const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
+    return (double)p.c.R * p.c.Hkv * (double)(rows / kMB + 1) * (double)tiles < 2147483647.0;
+}
+
+int attend_tc_block_rows() { return kMB; }
+
+cudaError_t launch_cache_attend_tc(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
+{
+    const cudaError_t e = p.c.D == 64 ? launch_tc<64>(p, ws, s) : launch_tc<128>(p, ws, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace dspark

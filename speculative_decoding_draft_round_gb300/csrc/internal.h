@@ -221,9 +221,13 @@ cudaError_t launch_cache_attend_simt(const AttendParams& p, cudaStream_t s);
 struct AttendScratch;
 bool attend_mma_supported(const AttendParams& p);
 // bytes of its workspace; with ws, the parts of the workspace at base
-size_t attend_mma_scratch(const AttendParams& p, AttendScratch* ws, void* base);
-cudaError_t launch_cache_attend_mma(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
+size_t attend_scratch(const AttendParams& p, AttendScratch* ws, void* base);
+cudaError_t launch_cache_attend(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
 cudaError_t launch_cache_merge(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
+// cache_attend_tc.cu
+bool attend_tc_supported(const AttendParams& p);
+int attend_tc_block_rows();
+cudaError_t launch_cache_attend_tc(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
 
 // rnn.cu (RNN head)
 cudaError_t launch_rnn_hidden(const DraftStep& p, cudaStream_t s);   // rnn_hidden.cu: yh = W_rnn[:, 2r:] h, every position
