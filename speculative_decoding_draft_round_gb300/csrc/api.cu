@@ -315,6 +315,7 @@ AttendParams attend_params(const dspark_cache_attend_args* a)
     p.sinks = a->sinks;
     p.scale = a->scale;
     p.c = a->cache;
+    p.page_magic = page_magic(a->cache.page_size);
     p.q = a->q;
     p.q_ts = a->q_token_stride;
     p.q_hs = a->q_head_stride;

@@ -30,6 +30,21 @@ __device__ __forceinline__ uint32_t v_scale_at(int slot, int g, int groups)
     return (uint32_t)(((slot / kScaleTokens) * groups + g) * kScaleTokens + slot % kScaleTokens) * 2u;
 }
 
+// Pages a multiple of 16 tokens: the page of token `at` is (at / 16) / (page / 16), with the quotient by a
+// multiplication: magic = ceil(2^32 / (page / 16)), 0 for pages of 16. Exact below 2^31 tokens (the error of
+// the magic number, below page / 16 <= 16, times at / 16 < 2^27 stays below 2^32).
+inline int page_magic(int page_size)
+{
+    const unsigned d = (unsigned)page_size / 16;
+    return d == 1 ? 0 : (int)(unsigned)(((1ull << 32) + d - 1) / d);
+}
+
+__device__ __forceinline__ int page_of(int at, int magic)
+{
+    const uint32_t n = (uint32_t)at >> 4;
+    return (int)(magic == 0 ? n : __umulhi(n, (uint32_t)magic));
+}
+
 // The block of head h in `page`
 __device__ __forceinline__ uint8_t* cache_page_block(const dspark_cache& c, int page, int h, uint32_t block_bytes)
 {

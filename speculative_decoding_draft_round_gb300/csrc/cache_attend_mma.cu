@@ -155,10 +155,11 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
             it.settle(p, kMB, s_pre, tile);
             const int key0 = it.span.key0(it.u) + (lane & 1) * 16;
             if (key0 < it.span.keys) {
-                const int page = p.c.table[(size_t)it.r * p.c.table_width + key0 / p.c.page_size];
+                const int at_page = page_of(key0, p.page_magic);
+                const int page = p.c.table[(size_t)it.r * p.c.table_width + at_page];
                 if (page >= 0 && page < p.c.n_pages) {
                     w.block = cache_page_block(p.c, page, it.head(), cb.bytes);
-                    w.slot = key0 % p.c.page_size;
+                    w.slot = key0 - at_page * p.c.page_size;
                     w.there = true;
                 } else {
                     raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);

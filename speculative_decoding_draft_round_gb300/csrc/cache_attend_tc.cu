@@ -125,12 +125,13 @@ __device__ __forceinline__ int plan(const AttendParams& p, int* pre, int* scan, 
     return total;
 }
 
-// Items of a run one after the other: request r, head h, block b, from tile u on. Warp-wide.
+// Items of a run one after the other: request r, head h, block b, from tile u on. Warp-wide; not inlined,
+// since the four roles' code has to stay in the instruction cache.
 struct Walk {
     int r = 0, h = 0, b = 0, u = 0;
     Request q;
     BlockTiles t;
-    __device__ void start(const AttendParams& p, const int* pre, int at)
+    __device__ __noinline__ void start(const AttendParams& p, const int* pre, int at)
     {
         int lo = 0, hi = p.c.R;   // the request with pre[r] <= at < pre[r + 1]
         while (hi - lo > 1) {
@@ -163,7 +164,7 @@ struct Walk {
         }
         t = block_tiles(p, q, b);
     }
-    __device__ void advance(const AttendParams& p, const int* pre)
+    __device__ __noinline__ void advance(const AttendParams& p, const int* pre)
     {
         u = 0;
         if (++b == q.blocks) {
@@ -218,6 +219,17 @@ __device__ __noinline__ void drain(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 8 channels of a row of q
+__device__ __forceinline__ uint4 load_q8(const __nv_bfloat16* src, int aligned)
+{
+    if (aligned) return *reinterpret_cast<const uint4*>(src);
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+    uint32_t x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
+    return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // Barriers, pairs by the parity of the tile (Q: of the item) first. A waiter is never two phases behind: each
@@ -298,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- MMA issuer
         Walk w;
         w.start(p, s_pre, begin);
+        const uint64_t q_desc = tc5::desc_sw128(q_buf), k_desc = tc5::desc_sw128(k_buf), v_desc = tc5::desc_sw128(v_buf);
         bool ok = true, prev_first = false, prev_last = false;
         int n = 0, prev_item = 0;
         // O (+)= P V of tile m of the run; `first` and `last` tile of the item in this run
@@ -307,17 +320,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(bar(kVFull + b), (m >> 1) & 1u)) return false;
             if (first && item > 0 && !wait(bar(kOFree), (item - 1) & 1u)) return false;
             tc5::fence_after();
-            if (lane == 0) {
+            // the start address of a descriptor counts 16 bytes: 16 K elements on are 2
+            const uint64_t vd = v_desc + (uint64_t)(b * (kOperand >> 4));
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    tc5::mma_ts(tmem + kTmemO, tmem + b * 128 + kk * 8,
-                                tc5::desc_sw128(v_buf + b * kOperand + (kk / 4) * (D * 128) + (kk % 4) * 32), kIdescO<D>,
-                                !(first && kk == 0));
-                tc5::commit(bar(kPvDone));
-                tc5::commit(bar(kVEmpty + b));
-                if (last) tc5::commit(bar(kODone));
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kTile / 16; ++kk)
+                tc5::mma_ts_warp(tmem + kTmemO, tmem + b * 128 + kk * 8, vd + (kk / 4) * (D * 128 / 16) + (kk % 4) * 2,
+                                 kIdescO<D>, kk > 0 || !first);
+            tc5::commit_warp(bar(kPvDone));
+            tc5::commit_warp(bar(kVEmpty + b));
+            if (last) tc5::commit_warp(bar(kODone));
             return true;
         };
         for (int at = begin, item = 0; at < end && ok; ++item) {
@@ -329,18 +340,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && n >= 2) ok = wait(bar(kPvDone), n & 1u);   // of tile n - 2, whose weights S replaces
                 if (!ok) break;
                 tc5::fence_after();
-                if (lane == 0) {
-                    const uint32_t qa = q_buf + (item & 1) * kOperand, kb = k_buf + b * kOperand;
+                const uint64_t qd = q_desc + (uint64_t)((item & 1) * (kOperand >> 4)), kd = k_desc + (uint64_t)(b * (kOperand >> 4));
+                tc5::mma_ss_warp<false>(tmem + b * 128, qd, kd, kIdescS);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
-                        tc5::mma_ss(tmem + b * 128, tc5::desc_sw128(qa + off), tc5::desc_sw128(kb + off), kIdescS, kk != 0);
-                    }
-                    tc5::commit(bar(kSFull + b));
-                    tc5::commit(bar(kKEmpty + b));
-                    if (u + 1 == u1) tc5::commit(bar(kQEmpty + (item & 1)));
-                    mbar_arrive(bar(kSFull + b));
+                for (int kk = 1; kk < D / 16; ++kk) {
+                    const uint64_t off = (kk / 4) * (16384 / 16) + (kk % 4) * 2;
+                    tc5::mma_ss_warp<true>(tmem + b * 128, qd + off, kd + off, kIdescS);
                 }
+                tc5::commit_warp(bar(kSFull + b));
+                tc5::commit_warp(bar(kKEmpty + b));
+                if (u + 1 == u1) tc5::commit_warp(bar(kQEmpty + (item & 1)));
+                if (lane == 0) mbar_arrive(bar(kSFull + b));
                 __syncwarp();
                 if (n > 0) ok = pv(n - 1, prev_first, prev_last, prev_item);
                 if (!ok) break;
@@ -353,10 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && n > 0) pv(n - 1, prev_first, prev_last, prev_item);
         // every MMA issued above lands before tensor memory is freed
-        if (lane == 0) {
-            tc5::commit(bar(kFin));
-            drain(bar(kFin), 0u);
-        }
+        tc5::commit_warp(bar(kFin));
+        drain(bar(kFin), 0u);
         __syncwarp();
     } else if (begin < end && (warp == kWarpQ || warp == kWarpQ + 1)) {
         // ---------------- rows of q, one item ahead
@@ -366,51 +374,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int at = begin, item = 0; at < end; ++item) {
             const int u1 = min(w.t.tiles, w.u + (end - at)), b = item & 1;
             if (item >= 2 && !wait(bar(kQEmpty + b), ((item >> 1) - 1) & 1u)) break;
+#pragma unroll 1
             for (int row = tid - kWarpQ * 32; row < kMB; row += 64) {
                 const int rr = w.b * kMB + row;
                 const bool real = rr < w.q.n_rows;
-                uint4 raw[D / 8];
-                if (real) {
-                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.q.first + rr / p.G) * p.q_ts +
-                                               (int64_t)(w.h * p.G + rr % p.G) * p.q_hs;
-                    if (p.q_aligned) {
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c) raw[c] = reinterpret_cast<const uint4*>(src)[c];
-                    } else {
-                        const uint16_t* s16 = reinterpret_cast<const uint16_t*>(src);
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] = s16[c * 8 + 2 * e] | ((uint32_t)s16[c * 8 + 2 * e + 1] << 16);
-                            raw[c] = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
-                }
+                const int rc = min(rr, w.q.n_rows - 1);
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.q.first + rc / p.G) * p.q_ts +
+                                           (int64_t)(w.h * p.G + rc % p.G) * p.q_hs;
                 uint32_t top = 0;   // magnitudes of bf16 order like their bits
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                    const uint4 v = load_q8(src + c * 8, p.q_aligned);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
                 }
-                const bool bad = top >= 0x7F80u;   // an infinity or NaN
+                const bool bad = real && top >= 0x7F80u;   // an infinity or NaN
                 if (bad) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
                 const float up = row_up((int)(top >> 7));
                 // a row that is not finite has the factor NaN and so weights, sum and result
                 s_fac[b][row] = bad ? NAN : row_factor(to_log2, up);
+                const bool keep = real && !bad;
                 const uint32_t dst = q_buf + b * kOperand + row * 128;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll 2
+                for (int c = 0; c < D / 8; ++c) {   // again, out of the cache
+                    const uint4 v = load_q8(src + c * 8, p.q_aligned);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        f[2 * e] = bad ? 0.f : __uint_as_float(x[e] << 16) * up;
-                        f[2 * e + 1] = bad ? 0.f : __uint_as_float(x[e] & 0xFFFF0000u) * up;
+                        f[2 * e] = keep ? __uint_as_float(x[e] << 16) * up : 0.f;
+                        f[2 * e + 1] = keep ? __uint_as_float(x[e] & 0xFFFF0000u) * up : 0.f;
                     }
                     // in the order of converted codes: channels 0 4 1 5 2 6 3 7
                     store16(dst + (c / 8) * 16384 + (((c % 8) ^ (row & 7)) * 16), pack(f[0], f[4]), pack(f[1], f[5]),
@@ -434,15 +428,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const DequantConst dq = dequant_const();
         Walk w;
         w.start(p, s_pre, begin);
-        int at = begin, u = w.u;
+        int at = begin, u = w.u - 1;
+        const int magic = p.page_magic, P = p.c.page_size;
         // the codes of the walk's tile u
         auto load = [&](Raw<D>& x) {
-            const int key0 = w.t.key0(u), P = p.c.page_size;
+            const int key0 = w.t.key0(u);
             const int32_t* row = p.c.table + (size_t)w.r * p.c.table_width;
             const int kk = key0 + k_tok, vk = key0 + v_tg * 8;
             int k_page = -1, v_page = -1;
-            if (kk < w.q.keys) k_page = row[kk / P];
-            if (vk < w.q.keys) v_page = row[vk / P];
+            const int k_at = page_of(kk, magic), v_at = page_of(vk, magic);
+            if (kk < w.q.keys) k_page = row[k_at];
+            if (vk < w.q.keys) v_page = row[v_at];
             const bool k_in = k_page >= 0 && k_page < p.c.n_pages;
             x.valid = v_page >= 0 && v_page < p.c.n_pages;
             if ((kk < w.q.keys && !k_in) || (vk < w.q.keys && !x.valid)) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
@@ -451,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < D / 16; ++c) x.k[c] = 0;
             if (k_in) {
                 const uint8_t* blk = cache_page_block(p.c, k_page, w.h, cb.bytes);
-                const int slot = kk % P;
+                const int slot = kk - k_at * P;
                 const uint4* src = reinterpret_cast<const uint4*>(blk + slot * (D / 2) + k_half * (D / 4));
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -470,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 8; ++c) x.v[c] = 0;
             if (x.valid && has_v) {
                 const uint8_t* blk = cache_page_block(p.c, v_page, w.h, cb.bytes);
-                const int slot = vk % P;
+                const int slot = vk - v_at * P;
                 const uint8_t* src = blk + cb.v_codes + slot * (D / 2) + v_word * 4;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) x.v[c] = *reinterpret_cast<const uint32_t*>(src + c * (D / 2));
@@ -485,19 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         };
-        Raw<D> now, next;
-        load(now);
+        Raw<D> now = {}, next = {};
         const int tiles = end - begin;
-        for (int n = 0; n < tiles; ++n) {
+#pragma unroll 1
+        for (int n = -1; n < tiles; ++n, now = next) {   // loads tile n + 1, then converts tile n
             const int b = n & 1;
-            ++at;
-            if (at < end) {   // the run's next tile
+            if (at < end) {
                 if (++u == w.t.tiles) {
                     w.advance(p, s_pre);
                     u = 0;
                 }
                 load(next);
+                ++at;
             }
+            if (n < 0) continue;
             if (n >= 2 && !wait(bar(kKEmpty + b), ((n >> 1) - 1) & 1u)) break;
             {
                 const uint32_t dst = k_buf + b * kOperand + (D == 128 ? k_half * 16384 : 0) + k_tok * 128;
@@ -518,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n >= 2 && !wait(bar(kVEmpty + b), ((n >> 1) - 1) & 1u)) break;
                 const uint32_t dst = v_buf + b * kOperand + (v_tg >> 3) * (D * 128) + v_word * 8 * 128;
                 const uint32_t sc[4] = {now.vs.x, now.vs.y, now.vs.z, now.vs.w};
-#pragma unroll
+#pragma unroll 1
                 for (int z = 0; z < 2; ++z) {   // channels 4 z .. of the word
                     uint32_t h[4][4];           // [pair of tokens][channel]
 #pragma unroll
@@ -534,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kVFull + b));
             }
-            now = next;
         }
     } else if (begin < end && warp >= kWarpSoft) {
         // ---------------- weights: one row a thread
@@ -579,18 +575,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     float mx = -INFINITY;
                     uint32_t x[32];
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         tc5::ld32(s_at + c * 32, x);
-                        if (edge) {
+                        if (edge) {   // hidden scores become -infinity, there too
                             const uint32_t see = seen(c);
+                            uint32_t y[16];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, (see >> j) & 1u ? __uint_as_float(x[j]) : -INFINITY);
-                        } else {
+                            for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+                                for (int j = 0; j < 16; ++j)
+                                    y[j] = x[hf * 16 + j] = (see >> (hf * 16 + j)) & 1u ? x[hf * 16 + j] : 0xFF800000u;
+                                tc5::st16(s_at + c * 32 + hf * 16, y);
+                            }
                         }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
                     }
+                    if (edge) tc5::wait_st();
                     mx *= fac;
                     if (u == u0) {
                         top = mx == mx ? mx : -INFINITY;   // NaN: a row that is not finite
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = wait(bar(kPvDone), (n - 1) & 1u);
                         if (!ok) break;
                         tc5::fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t y[16];
                             tc5::ld16(lanes + kTmemO + c * 16, y);
@@ -612,14 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float base = top == -INFINITY ? 0.f : kShift - top;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         tc5::ld32(s_at + c * 32, x);
-                        if (edge) {
-                            const uint32_t see = seen(c);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = (see >> j) & 1u ? x[j] : 0xFF800000u;   // -infinity
-                        }
                         uint32_t y[16];
                         float s0 = 0.f, s1 = 0.f;
 #pragma unroll

@@ -157,6 +157,7 @@ struct AttendParams {
     const void* q;
     int64_t q_ts, q_hs;
     int q_aligned;       // q's rows admit 16-byte loads
+    int page_magic;      // see page_of in cache.cuh
     const int32_t* offsets;
     void* out;
     float* lse;
