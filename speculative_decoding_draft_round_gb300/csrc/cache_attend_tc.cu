@@ -9,8 +9,8 @@
 //   8 - 15  turn codes into fp16 (exact: scales have 8 bits) in shared memory: K by token, V transposed
 //           by channel, both K-major with the 128-byte swizzle; the next tile's codes are loaded before.
 //           A thread takes 8 tokens of 8 value channels, so the transposition is its choice of registers.
-//   0       issues S = Q K^T (128 x 128 x D, operands in shared memory) and O += P V (128 x D x 128, P in
-//           tensor memory), S of a tile before P V of the one before.
+//   0       issues S = Q K^T (128 x 128 x D, operands in shared memory), a tile ahead.
+//   1       issues O += P V (128 x D x 128, P in tensor memory).
 //   4 - 7   one row a thread: the row's maximum, weights 2^(t - m + 10) as fp16 into the tensor memory that
 //           S had, their sum. m only has to be near the maximum: O is rescaled when a score passes m by 2^5.
 //   2, 3    rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory.
@@ -30,7 +30,7 @@ namespace {
 constexpr int kTile = 128;                     // tokens
 constexpr int kMB = 128;                       // rows of a block
 constexpr int kThreads = 512;
-constexpr int kWarpMma = 0, kWarpAlloc = 1, kWarpQ = 2, kWarpSoft = 4, kWarpConv = 8;
+constexpr int kWarpS = 0, kWarpPv = 1, kWarpQ = 2, kWarpSoft = 4, kWarpConv = 8;
 constexpr unsigned long long kDrainNs = 4000000000ull;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;   // S of even tiles at 0, of odd tiles at 128, O at 256
 // instruction descriptors, kind::f16: D fp32, A and B fp16, both K-major, M = 128
@@ -237,9 +237,9 @@ __device__ __forceinline__ uint4 load_q8(const __nv_bfloat16* src, int aligned)
 enum Bar {
     kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kQEmpty = 10, kSFull = 12, kPFull = 14,
     kPvDone = 16,   // O += P V of a tile has landed
-    kODone = 17,    // that of an item's last tile in this run
-    kOFree = 18,    // the item's rows are out of O
-    kFin = 19, kBars = 20
+    kODone = 18,    // that of an item's last tile in this run
+    kOFree = 19,    // the item's rows are out of O
+    kFin = 20, kBars = 22
 };
 
 // The codes of a tile that one converting thread takes: 64 (32 for D = 64) channels of one key, and 8 tokens
@@ -283,16 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kQEmpty + b), 5);   // its MMAs, and the four warps that read the factors
             mbar_init(bar(kSFull + b), 2);    // its MMAs, and the issuing thread for what it saw (s_valid)
             mbar_init(bar(kPFull + b), 4);
+            mbar_init(bar(kPvDone + b), 1);
+            mbar_init(bar(kFin + b), 1);
         }
-        mbar_init(bar(kPvDone), 1);
         mbar_init(bar(kODone), 1);
         mbar_init(bar(kOFree), 4);
-        mbar_init(bar(kFin), 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
-    if (warp == kWarpAlloc) tc5::alloc(&s_tmem, kTmemCols);
+    if (warp == kWarpPv) tc5::alloc(&s_tmem, kTmemCols);
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
@@ -306,65 +306,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waits wait{&s_abort, p.status, wait_ns};
     AttendTodo todo = {};
 
-    if (begin < end && warp == kWarpMma) {
-        // ---------------- MMA issuer
+    if (begin < end && warp == kWarpS) {
+        // ---------------- S = Q K^T
         Walk w;
         w.start(p, s_pre, begin);
-        const uint64_t q_desc = tc5::desc_sw128(q_buf), k_desc = tc5::desc_sw128(k_buf), v_desc = tc5::desc_sw128(v_buf);
-        bool ok = true, prev_first = false, prev_last = false;
-        int n = 0, prev_item = 0;
-        // O (+)= P V of tile m of the run; `first` and `last` tile of the item in this run
-        auto pv = [&](int m, bool first, bool last, int item) {
-            const int b = m & 1;
-            if (!wait(bar(kPFull + b), (m >> 1) & 1u)) return false;
-            if (!wait(bar(kVFull + b), (m >> 1) & 1u)) return false;
-            if (first && item > 0 && !wait(bar(kOFree), (item - 1) & 1u)) return false;
-            tc5::fence_after();
-            // the start address of a descriptor counts 16 bytes: 16 K elements on are 2
-            const uint64_t vd = v_desc + (uint64_t)(b * (kOperand >> 4));
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-                tc5::mma_ts_warp(tmem + kTmemO, tmem + b * 128 + kk * 8, vd + (kk / 4) * (D * 128 / 16) + (kk % 4) * 2,
-                                 kIdescO<D>, kk > 0 || !first);
-            tc5::commit_warp(bar(kPvDone));
-            tc5::commit_warp(bar(kVEmpty + b));
-            if (last) tc5::commit_warp(bar(kODone));
-            return true;
-        };
+        const uint64_t q_desc = tc5::desc_sw128(q_buf), k_desc = tc5::desc_sw128(k_buf);
+        bool ok = true;
+        int n = 0;
         for (int at = begin, item = 0; at < end && ok; ++item) {
-            const int u0 = w.u, u1 = min(w.t.tiles, u0 + (end - at));
-            for (int u = u0; u < u1; ++u, ++n) {
+            const int tiles = min(w.t.tiles - w.u, end - at);
+            ok = wait(bar(kQFull + (item & 1)), (item >> 1) & 1u);
+            for (int u = 0; u < tiles && ok; ++u, ++n) {
                 const int b = n & 1;
-                ok = wait(bar(kKFull + b), (n >> 1) & 1u);
-                if (ok && u == u0) ok = wait(bar(kQFull + (item & 1)), (item >> 1) & 1u);
-                if (ok && n >= 2) ok = wait(bar(kPvDone), n & 1u);   // of tile n - 2, whose weights S replaces
+                if (!wait(bar(kKFull + b), (n >> 1) & 1u)) ok = false;
+                if (ok && n >= 2 && !wait(bar(kPvDone + b), ((n >> 1) - 1) & 1u)) ok = false;   // S replaces its weights
                 if (!ok) break;
                 tc5::fence_after();
+                // the start address of a descriptor counts 16 bytes: 16 K elements on are 2
                 const uint64_t qd = q_desc + (uint64_t)((item & 1) * (kOperand >> 4)), kd = k_desc + (uint64_t)(b * (kOperand >> 4));
-                tc5::mma_ss_warp<false>(tmem + b * 128, qd, kd, kIdescS);
-#pragma unroll
-                for (int kk = 1; kk < D / 16; ++kk) {
-                    const uint64_t off = (kk / 4) * (16384 / 16) + (kk % 4) * 2;
-                    tc5::mma_ss_warp<true>(tmem + b * 128, qd + off, kd + off, kIdescS);
+                uint32_t acc = 0;
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint64_t off = c * (16384 / 16);
+#pragma unroll 1
+                    for (int kk = 0; kk < 4; ++kk, off += 2, acc = 1) tc5::mma_ss_warp(tmem + b * 128, qd + off, kd + off, kIdescS, acc);
                 }
                 tc5::commit_warp(bar(kSFull + b));
                 tc5::commit_warp(bar(kKEmpty + b));
-                if (u + 1 == u1) tc5::commit_warp(bar(kQEmpty + (item & 1)));
+                if (u + 1 == tiles) tc5::commit_warp(bar(kQEmpty + (item & 1)));
                 if (lane == 0) mbar_arrive(bar(kSFull + b));
                 __syncwarp();
-                if (n > 0) ok = pv(n - 1, prev_first, prev_last, prev_item);
-                if (!ok) break;
-                prev_first = u == u0;
-                prev_last = u + 1 == u1;
-                prev_item = item;
             }
-            at += u1 - u0;
+            at += tiles;
             if (at < end) w.advance(p, s_pre);
         }
-        if (ok && n > 0) pv(n - 1, prev_first, prev_last, prev_item);
         // every MMA issued above lands before tensor memory is freed
         tc5::commit_warp(bar(kFin));
         drain(bar(kFin), 0u);
+        __syncwarp();
+    } else if (begin < end && warp == kWarpPv) {
+        // ---------------- O (+)= P V
+        Walk w;
+        w.start(p, s_pre, begin);
+        const uint64_t v_desc = tc5::desc_sw128(v_buf);
+        bool ok = true;
+        int n = 0;
+        for (int at = begin, item = 0; at < end && ok; ++item) {
+            const int tiles = min(w.t.tiles - w.u, end - at);
+            for (int u = 0; u < tiles && ok; ++u, ++n) {
+                const int b = n & 1;
+                if (!wait(bar(kVFull + b), (n >> 1) & 1u) || !wait(bar(kPFull + b), (n >> 1) & 1u)) ok = false;
+                if (ok && u == 0 && item > 0 && !wait(bar(kOFree), (item - 1) & 1u)) ok = false;
+                if (!ok) break;
+                tc5::fence_after();
+                uint32_t pt = tmem + b * 128, acc = u > 0;
+                const uint64_t vd = v_desc + (uint64_t)(b * (kOperand >> 4));
+#pragma unroll 1
+                for (int c = 0; c < kTile / 64; ++c) {
+                    uint64_t d = vd + c * (D * 128 / 16);
+#pragma unroll 1
+                    for (int kk = 0; kk < 4; ++kk, d += 2, pt += 8, acc = 1) tc5::mma_ts_warp(tmem + kTmemO, pt, d, kIdescO<D>, acc);
+                }
+                tc5::commit_warp(bar(kPvDone + b));
+                tc5::commit_warp(bar(kVEmpty + b));
+                if (u + 1 == tiles) tc5::commit_warp(bar(kODone));
+            }
+            at += tiles;
+            if (at < end) w.advance(p, s_pre);
+        }
+        tc5::commit_warp(bar(kFin + 1));
+        drain(bar(kFin + 1), 0u);
         __syncwarp();
     } else if (begin < end && (warp == kWarpQ || warp == kWarpQ + 1)) {
         // ---------------- rows of q, one item ahead
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.q.first + rc / p.G) * p.q_ts +
                                            (int64_t)(w.h * p.G + rc % p.G) * p.q_hs;
                 uint32_t top = 0;   // magnitudes of bf16 order like their bits
-#pragma unroll 4
+#pragma unroll 8
                 for (int c = 0; c < D / 8; ++c) {
                     const uint4 v = load_q8(src + c * 8, p.q_aligned);
                     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -601,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float keep = m == top ? 1.f : ex2(top - m);
                         top = m;
                         sum *= keep;
-                        ok = wait(bar(kPvDone), (n - 1) & 1u);
+                        ok = wait(bar(kPvDone + (b ^ 1)), ((n - 1) >> 1) & 1u);
                         if (!ok) break;
                         tc5::fence_after();
 #pragma unroll 1
@@ -698,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == kWarpSoft * 32) ws.todo[blockIdx.x] = todo;
     tc5::fence_before();
     __syncthreads();
-    if (warp == kWarpAlloc) {
+    if (warp == kWarpPv) {
         tc5::fence_after();
         tc5::dealloc(tmem, kTmemCols);
     }
