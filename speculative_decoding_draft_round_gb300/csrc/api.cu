@@ -316,6 +316,7 @@ AttendParams attend_params(const dspark_cache_attend_args* a)
     p.scale = a->scale;
     p.c = a->cache;
     p.page_magic = page_magic(a->cache.page_size);
+    p.g_magic = p.G > 1 ? (uint32_t)(((1ull << 32) + p.G - 1) / p.G) : 0u;
     p.q = a->q;
     p.q_ts = a->q_token_stride;
     p.q_hs = a->q_head_stride;

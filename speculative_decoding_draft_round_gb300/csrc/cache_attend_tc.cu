@@ -13,7 +13,8 @@
 //   1       issues O += P V (128 x D x 128, P in tensor memory).
 //   4 - 7   one row a thread: the row's maximum, weights 2^(t - m + 10) as fp16 into the tensor memory that
 //           S had, their sum. m only has to be near the maximum: O is rescaled when a score passes m by 2^5.
-//   2, 3    rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory.
+//   2, 3, 16, 17  rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory;
+//           finished rows out of the same buffer.
 // All waits are bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT and ends the CTA's
 // loops, its MMAs land, and tensor memory is freed.
 #include "attend_convert.cuh"
@@ -29,8 +30,9 @@ namespace {
 
 constexpr int kTile = 128;                     // tokens
 constexpr int kMB = 128;                       // rows of a block
-constexpr int kThreads = 512;
-constexpr int kWarpS = 0, kWarpPv = 1, kWarpQ = 2, kWarpSoft = 4, kWarpConv = 8;
+constexpr int kThreads = 576;
+constexpr int kWarpS = 0, kWarpPv = 1, kWarpSoft = 4, kWarpConv = 8;
+constexpr int kQWarps = 4;   // warps 2, 3, 16, 17
 constexpr unsigned long long kDrainNs = 4000000000ull;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;   // S of even tiles at 0, of odd tiles at 128, O at 256
 // instruction descriptors, kind::f16: D fp32, A and B fp16, both K-major, M = 128
@@ -91,7 +93,7 @@ __device__ __forceinline__ int head_tiles(const AttendParams& p, const Request& 
 __device__ __forceinline__ int plan(const AttendParams& p, int* pre, int* scan, bool report)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.c.R;
-    if (R <= 4 * kThreads / 32) {   // few requests, perhaps of many blocks: a warp each
+    if (R <= 64) {   // few requests, perhaps of many blocks: a warp each
         for (int r = warp; r < R; r += kThreads / 32) {
             const int n = head_tiles<true>(p, request_of(p, r, report && lane == 0)) * p.c.Hkv;
             if (lane == 0) pre[r + 1] = n;
@@ -182,11 +184,25 @@ struct Walk {
 
 // ------------------------------------------------------------------ waits
 
+// a try that may sleep some microseconds in the hardware, so that waiting warps leave the issue slots alone
+__device__ __forceinline__ bool try_wait_sleep(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                        unsigned long long limit_ns)
 {
     const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!try_wait_sleep(bar, parity)) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
@@ -221,10 +237,54 @@ __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, u
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 8 channels of a row of q
-__device__ __forceinline__ uint4 load_q8(const __nv_bfloat16* src, int aligned)
+__device__ __forceinline__ uint4 load16(uint32_t addr)
 {
-    if (aligned) return *reinterpret_cast<const uint4*>(src);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// two fp32 values an instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Query and head in the group of the rows of a block. The quotients by G of numbers below 2048 come by a
+// multiplication: g_magic = ceil(2^32 / G), off by less than G <= 1024, is exact there.
+struct RowMap {
+    int j0, g0, G;
+    uint32_t magic;
+    __device__ __forceinline__ RowMap(int row0, int G_, uint32_t m) : j0(row0 / G_), g0(row0 % G_), G(G_), magic(m) {}
+    __device__ __forceinline__ void at(int row, int& j, int& g) const
+    {
+        const int x = g0 + row, q = magic == 0 ? x : (int)__umulhi((uint32_t)x, magic);
+        j = j0 + q;
+        g = x - q * G;
+    }
+};
+
+// 8 channels of a row of q off 16-byte boundaries
+__device__ __forceinline__ uint4 load_halves(const __nv_bfloat16* src)
+{
     const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
     uint32_t x[4];
 #pragma unroll
@@ -235,11 +295,15 @@ __device__ __forceinline__ uint4 load_q8(const __nv_bfloat16* src, int aligned)
 // Barriers, pairs by the parity of the tile (Q: of the item) first. A waiter is never two phases behind: each
 // phase needs an arrival that the waiter, or one that waits for it, makes after it saw the phase before.
 enum Bar {
-    kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kQEmpty = 10, kSFull = 12, kPFull = 14,
+    kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8,
+    kStaged = 10,   // an item's rows are in q's buffer, or written elsewhere
+    kSFull = 12, kPFull = 14,
     kPvDone = 16,   // O += P V of a tile has landed
     kODone = 18,    // that of an item's last tile in this run
     kOFree = 19,    // the item's rows are out of O
-    kFin = 20, kBars = 22
+    kFin = 20,
+    kCopied = 22,   // the q warps have written out their parts of the staged rows
+    kBars = 24
 };
 
 // The codes of a tile that one converting thread takes: 64 (32 for D = 64) channels of one key, and 8 tokens
@@ -279,12 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kVFull + b), kVWarps);
             mbar_init(bar(kKEmpty + b), 1);
             mbar_init(bar(kVEmpty + b), 1);
-            mbar_init(bar(kQFull + b), 2);
-            mbar_init(bar(kQEmpty + b), 5);   // its MMAs, and the four warps that read the factors
+            mbar_init(bar(kQFull + b), kQWarps);
+            mbar_init(bar(kStaged + b), 4);
             mbar_init(bar(kSFull + b), 2);    // its MMAs, and the issuing thread for what it saw (s_valid)
             mbar_init(bar(kPFull + b), 4);
             mbar_init(bar(kPvDone + b), 1);
             mbar_init(bar(kFin + b), 1);
+            mbar_init(bar(kCopied + b), kQWarps);
         }
         mbar_init(bar(kODone), 1);
         mbar_init(bar(kOFree), 4);
@@ -333,7 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc5::commit_warp(bar(kSFull + b));
                 tc5::commit_warp(bar(kKEmpty + b));
-                if (u + 1 == tiles) tc5::commit_warp(bar(kQEmpty + (item & 1)));
                 if (lane == 0) mbar_arrive(bar(kSFull + b));
                 __syncwarp();
             }
@@ -377,57 +441,111 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc5::commit_warp(bar(kFin + 1));
         drain(bar(kFin + 1), 0u);
         __syncwarp();
-    } else if (begin < end && (warp == kWarpQ || warp == kWarpQ + 1)) {
-        // ---------------- rows of q, one item ahead
+    } else if (begin < end && (warp == 2 || warp == 3 || warp >= 16)) {
+        // ---------------- rows of q, one item ahead; finished rows out of the buffer before it is filled again
         Walk w;
         w.start(p, s_pre, begin);
         const float to_log2 = p.scale * kLog2e;
-        for (int at = begin, item = 0; at < end; ++item) {
-            const int u1 = min(w.t.tiles, w.u + (end - at)), b = item & 1;
-            if (item >= 2 && !wait(bar(kQEmpty + b), ((item >> 1) - 1) & 1u)) break;
-#pragma unroll 1
-            for (int row = tid - kWarpQ * 32; row < kMB; row += 64) {
-                const int rr = w.b * kMB + row;
-                const bool real = rr < w.q.n_rows;
-                const int rc = min(rr, w.q.n_rows - 1);
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.q.first + rc / p.G) * p.q_ts +
-                                           (int64_t)(w.h * p.G + rc % p.G) * p.q_hs;
-                uint32_t top = 0;   // magnitudes of bf16 order like their bits
-#pragma unroll 8
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = load_q8(src + c * 8, p.q_aligned);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // a row of D channels is D / 8 lanes
+        constexpr int kFlight = 4;                           // loads in flight
+        const int c = lane % kLanes, sub = (warp < 4 ? warp - 2 : warp - 14) * kRows + lane / kLanes;
+        Walk prev[2];            // the items whose rows the two buffers hold
+        bool whole[2] = {false, false};
+        auto put = [&](int b, uint32_t item) {   // the staged rows of item `item` out of buffer b
+            if (!wait(bar(kStaged + b), (item >> 1) & 1u)) return false;
+            if (whole[b]) {
+                const Walk& x = prev[b];
+                const RowMap map(x.b * kMB, p.G, p.g_magic);
+                const int left = min(kMB, x.q.n_rows - x.b * kMB);
+                __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(p.out) + ((size_t)x.q.first * p.Hq + x.h * p.G) * D + c * 8;
+                const uint32_t stage = q_buf + b * kOperand;
+#pragma unroll 4
+                for (int row = sub; row < left; row += kQWarps * kRows) {
+                    int j, g;
+                    map.at(row, j, g);
+                    *reinterpret_cast<uint4*>(o0 + ((size_t)j * p.Hq + g) * D) = load16(stage + row * (D * 2) + ((c ^ (row & 7)) * 16));
                 }
-                const bool bad = real && top >= 0x7F80u;   // an infinity or NaN
-                if (bad) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
-                const float up = row_up((int)(top >> 7));
-                // a row that is not finite has the factor NaN and so weights, sum and result
-                s_fac[b][row] = bad ? NAN : row_factor(to_log2, up);
-                const bool keep = real && !bad;
-                const uint32_t dst = q_buf + b * kOperand + row * 128;
-#pragma unroll 2
-                for (int c = 0; c < D / 8; ++c) {   // again, out of the cache
-                    const uint4 v = load_q8(src + c * 8, p.q_aligned);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = true;
+        int item = 0;
+        for (int at = begin; at < end && ok; ++item) {
+            const int tiles = min(w.t.tiles - w.u, end - at), b = item & 1;
+            if (item >= 2) {
+                // the item two before: its products are done when its rows are staged; and all four warps have
+                // read what any of them fills next
+                ok = put(b, item - 2);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar(kCopied + b));
+                ok = wait(bar(kCopied + b), ((item >> 1) - 1) & 1u);
+                if (!ok) break;
+            }
+            prev[b] = w;
+            whole[b] = w.u == 0 && tiles == w.t.tiles;
+            const RowMap map(w.b * kMB, p.G, p.g_magic);
+            const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)w.q.first * p.q_ts +
+                                      (int64_t)w.h * p.G * p.q_hs + c * 8;
+            const int left = min(kMB, w.q.n_rows - w.b * kMB);
+#pragma unroll 1
+            for (int r = sub; r < kMB; r += kFlight * kQWarps * kRows) {
+                uint4 v[kFlight];
+                if (p.q_aligned) {   // one test for all: a test each would make the loads wait for one another
+#pragma unroll
+                    for (int e = 0; e < kFlight; ++e) {
+                        const int row = r + e * kQWarps * kRows;
+                        int j, g;
+                        map.at(min(row, left - 1), j, g);
+                        v[e] = *reinterpret_cast<const uint4*>(q0 + (int64_t)j * p.q_ts + (int64_t)g * p.q_hs);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < kFlight; ++e) {
+                        const int row = r + e * kQWarps * kRows;
+                        int j, g;
+                        map.at(min(row, left - 1), j, g);
+                        const uint4 y = load_halves(q0 + (int64_t)j * p.q_ts + (int64_t)g * p.q_hs);
+#pragma unroll
+                        for (int k = 0; k < kFlight; ++k)
+                            if (k == e) v[k] = y;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kFlight; ++e) {
+                    const int row = r + e * kQWarps * kRows;
+                    const uint32_t x[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+                    // magnitudes of bf16 order like their bits, two at a time
+                    uint32_t two = x[0] & 0x7FFF7FFFu;
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) two = __vmaxu2(two, x[k] & 0x7FFF7FFFu);
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+                    const uint32_t top = max(two & 0xFFFFu, two >> 16);
+                    const bool bad = top >= 0x7F80u;   // an infinity or NaN
+                    if (bad && row < left && c == 0) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
+                    const float up = row_up((int)(top >> 7));
+                    // a row that is not finite has the factor NaN and so weights, sum and result; rows past the
+                    // request's repeat its last one and are not written
+                    if (c == 0) s_fac[b][row] = bad ? NAN : row_factor(to_log2, up);
                     float f[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[2 * e] = keep ? __uint_as_float(x[e] << 16) * up : 0.f;
-                        f[2 * e + 1] = keep ? __uint_as_float(x[e] & 0xFFFF0000u) * up : 0.f;
+                    for (int k = 0; k < 4; ++k) {
+                        f[2 * k] = __uint_as_float(x[k] << 16) * up;
+                        f[2 * k + 1] = __uint_as_float(x[k] & 0xFFFF0000u) * up;
                     }
                     // in the order of converted codes: channels 0 4 1 5 2 6 3 7
-                    store16(dst + (c / 8) * 16384 + (((c % 8) ^ (row & 7)) * 16), pack(f[0], f[4]), pack(f[1], f[5]),
-                            pack(f[2], f[6]), pack(f[3], f[7]));
+                    store16(q_buf + b * kOperand + (c / 8) * 16384 + row * 128 + (((c % 8) ^ (row & 7)) * 16), pack(f[0], f[4]),
+                            pack(f[1], f[5]), pack(f[2], f[6]), pack(f[3], f[7]));
                 }
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kQFull + b));
-            at += u1 - w.u;
+            at += tiles;
             if (at < end) w.advance(p, s_pre);
         }
+        for (int x = max(0, item - 2); x < item && ok; ++x) ok = put(x & 1, x);
     } else if (begin < end && warp >= kWarpConv) {
         // ---------------- codes to fp16
         const int cw = warp - kWarpConv;
@@ -439,26 +557,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const DequantConst dq = dequant_const();
         Walk w;
         w.start(p, s_pre, begin);
-        int at = begin, u = w.u - 1;
         const int magic = p.page_magic, P = p.c.page_size;
-        // the codes of the walk's tile u
-        auto load = [&](Raw<D>& x) {
-            const int key0 = w.t.key0(u);
+        // What a tile's loads need, found a conversion before them: its first key, its head, the keys there are
+        // and the pages of this thread's tokens.
+        struct Place {
+            int key0, h, keys, k_page, v_page;
+        };
+        auto find = [&](int u) {
+            Place x;
+            x.key0 = w.t.key0(u);
+            x.h = w.h;
+            x.keys = w.q.keys;
             const int32_t* row = p.c.table + (size_t)w.r * p.c.table_width;
-            const int kk = key0 + k_tok, vk = key0 + v_tg * 8;
-            int k_page = -1, v_page = -1;
-            const int k_at = page_of(kk, magic), v_at = page_of(vk, magic);
-            if (kk < w.q.keys) k_page = row[k_at];
-            if (vk < w.q.keys) v_page = row[v_at];
-            const bool k_in = k_page >= 0 && k_page < p.c.n_pages;
-            x.valid = v_page >= 0 && v_page < p.c.n_pages;
-            if ((kk < w.q.keys && !k_in) || (vk < w.q.keys && !x.valid)) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+            const int kk = x.key0 + k_tok, vk = x.key0 + v_tg * 8;
+            x.k_page = kk < x.keys ? row[page_of(kk, magic)] : -1;
+            x.v_page = vk < x.keys ? row[page_of(vk, magic)] : -1;
+            return x;
+        };
+        Raw<D> x = {};
+        auto load_k = [&](const Place& a) {
+            const int kk = a.key0 + k_tok;
+            const bool in = kk < a.keys && a.k_page >= 0 && a.k_page < p.c.n_pages;
+            if (kk < a.keys && !in) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
             x.ks = 0;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) x.k[c] = 0;
-            if (k_in) {
-                const uint8_t* blk = cache_page_block(p.c, k_page, w.h, cb.bytes);
-                const int slot = kk - k_at * P;
+            if (in) {
+                const uint8_t* blk = cache_page_block(p.c, a.k_page, a.h, cb.bytes);
+                const int slot = kk - page_of(kk, magic) * P;
                 const uint4* src = reinterpret_cast<const uint4*>(blk + slot * (D / 2) + k_half * (D / 4));
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -472,18 +598,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (D == 128) x.ks = *reinterpret_cast<const uint32_t*>(sc + k_half * 4);
                 else x.ks = *reinterpret_cast<const uint16_t*>(sc + k_half * 2);
             }
+        };
+        auto load_v = [&](const Place& a) {
+            const int vk = a.key0 + v_tg * 8;
+            const bool in = vk < a.keys && a.v_page >= 0 && a.v_page < p.c.n_pages;
+            x.valid = in;
             x.vs = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int c = 0; c < 8; ++c) x.v[c] = 0;
-            if (x.valid && has_v) {
-                const uint8_t* blk = cache_page_block(p.c, v_page, w.h, cb.bytes);
-                const int slot = vk - v_at * P;
+            if (in && has_v) {
+                const uint8_t* blk = cache_page_block(p.c, a.v_page, a.h, cb.bytes);
+                const int slot = vk - page_of(vk, magic) * P;
                 const uint8_t* src = blk + cb.v_codes + slot * (D / 2) + v_word * 4;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) x.v[c] = *reinterpret_cast<const uint32_t*>(src + c * (D / 2));
                 x.vs = *reinterpret_cast<const uint4*>(blk + cb.v_scales + v_scale_at(slot, v_word / 4, D / kCacheGroup));
                 // what no token wrote may be anything: its scale becomes 0
-                const int left = w.q.keys - vk;
+                const int left = a.keys - vk;
                 if (left < 8) {
                     x.vs.x &= keep_halves(left);
                     x.vs.y &= keep_halves(left - 2);
@@ -492,46 +623,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         };
-        Raw<D> now = {}, next = {};
         const int tiles = end - begin;
+        int u = w.u;
+        Place place = find(u);
+        load_k(place);
+        load_v(place);
 #pragma unroll 1
-        for (int n = -1; n < tiles; ++n, now = next) {   // loads tile n + 1, then converts tile n
+        for (int n = 0; n < tiles; ++n) {
+            // The registers that a conversion frees take the next tile's codes at once: their way is as long as
+            // the other conversion and the waits. (A second set that is copied at the loop's end stops there for
+            // the loads instead.)
             const int b = n & 1;
-            if (at < end) {
+            const bool more = n + 1 < tiles, valid = x.valid;
+            if (more) {
                 if (++u == w.t.tiles) {
                     w.advance(p, s_pre);
                     u = 0;
                 }
-                load(next);
-                ++at;
+                place = find(u);
             }
-            if (n < 0) continue;
             if (n >= 2 && !wait(bar(kKEmpty + b), ((n >> 1) - 1) & 1u)) break;
             {
                 const uint32_t dst = k_buf + b * kOperand + (D == 128 ? k_half * 16384 : 0) + k_tok * 128;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t h[4];
-                    const __half2 s = c < 4 ? __low2half2(as_half2(now.ks)) : __high2half2(as_half2(now.ks));
-                    dequant(now.k[c], s, dq, h);
+                    const __half2 s = c < 4 ? __low2half2(as_half2(x.ks)) : __high2half2(as_half2(x.ks));
+                    dequant(x.k[c], s, dq, h);
                     const int unit = D == 128 ? c : k_half * 4 + c;
                     store16(dst + ((unit ^ (k_tok & 7)) * 16), h[0], h[1], h[2], h[3]);
                 }
-                if (has_v && v_word == 0 && (v_tg & 1) == 0) s_valid[n & 3][v_tg >> 1] = now.valid;
+                if (has_v && v_word == 0 && (v_tg & 1) == 0) s_valid[n & 3][v_tg >> 1] = valid;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kKFull + b));
+                if (more) load_k(place);
             }
             if (has_v) {
                 if (n >= 2 && !wait(bar(kVEmpty + b), ((n >> 1) - 1) & 1u)) break;
                 const uint32_t dst = v_buf + b * kOperand + (v_tg >> 3) * (D * 128) + v_word * 8 * 128;
-                const uint32_t sc[4] = {now.vs.x, now.vs.y, now.vs.z, now.vs.w};
+                const uint32_t sc[4] = {x.vs.x, x.vs.y, x.vs.z, x.vs.w};
 #pragma unroll 1
                 for (int z = 0; z < 2; ++z) {   // channels 4 z .. of the word
                     uint32_t h[4][4];           // [pair of tokens][channel]
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-                        dequant(__byte_perm(now.v[2 * m], now.v[2 * m + 1], z == 0 ? 0x5410u : 0x7632u), as_half2(sc[m]), dq, h[m]);
+                        dequant(__byte_perm(x.v[2 * m], x.v[2 * m + 1], z == 0 ? 0x5410u : 0x7632u), as_half2(sc[m]), dq, h[m]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int d = z * 4 + c;
@@ -542,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kVFull + b));
             }
+            if (more) load_v(place);
         }
     } else if (begin < end && warp >= kWarpSoft) {
         // ---------------- weights: one row a thread
@@ -558,8 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar(kQFull + (item & 1)), (item >> 1) & 1u);
             if (!ok) break;
             const float fac = s_fac[item & 1][row];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kQEmpty + (item & 1)));
+            const uint64_t fac2 = pack2(fac, fac);
             // keys this row sees: from lo (and below the sinks) to hi
             const int own = w.q.ctx + min(rr, w.q.n_rows - 1) / p.G;
             const int hi = min(own, w.q.keys - 1);
@@ -625,24 +762,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float base = top == -INFINITY ? 0.f : kShift - top;
+                    const uint64_t base2 = pack2(base, base);
+                    uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         tc5::ld32(s_at + c * 32, x);
                         uint32_t y[16];
-                        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float e0 = ex2(fmaf(__uint_as_float(x[2 * j]), fac, base));
-                            const float e1 = ex2(fmaf(__uint_as_float(x[2 * j + 1]), fac, base));
-                            s0 += e0;
-                            s1 += e1;
+                            float t0, t1;
+                            unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), fac2, base2), t0, t1);
+                            const float e0 = ex2(t0), e1 = ex2(t1);
+                            sum2[j & 1] = add2(sum2[j & 1], pack2(e0, e1));
                             y[j] = pack(e0, e1);
                         }
-                        sum += s0 + s1;
                         tc5::st16(s_at + c * 16, y);   // over scores that this thread has read
                     }
                     tc5::wait_st();
                     tc5::fence_before();
+                    float s0, s1;
+                    unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                    sum += s0 + s1;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kPFull + b));
@@ -658,14 +798,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc5::fence_after();
                 const bool real = rr < w.q.n_rows;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const size_t part = ((size_t)blockIdx.x * 2 + slot) * kMB + row;
-                const size_t dst = (size_t)(w.q.first + rr / p.G) * p.Hq + w.h * p.G + rr % p.G;
+                if (whole) {
+                    // rows as bf16 into q's buffer, whose products are done, each row's 16-byte units turned by
+                    // the row; the q warps write them out
+                    const uint32_t stage = q_buf + (item & 1) * kOperand + (uint32_t)(warp - kWarpSoft) * 32 * (D * 2);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t x[32];
-                    tc5::ld32(lanes + kTmemO + c * 32, x);
-                    if (real && whole) {
-                        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + dst * D + c * 32);
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t x[32];
+                        tc5::ld32(lanes + kTmemO + c * 32, x);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t y[4];
@@ -675,23 +815,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                __uint_as_float(x[8 * k + 2 * e + 1]) * inv);
                                 y[e] = *reinterpret_cast<const uint32_t*>(&v);
                             }
-                            o[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                            store16(stage + lane * (D * 2) + (((c * 4 + k) ^ (lane & 7)) * 16), y[0], y[1], y[2], y[3]);
                         }
-                    } else if (real) {
-                        uint4* o = reinterpret_cast<uint4*>(ws.rows + part * D + c * 32);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    }
+                    tc5::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kOFree));
+                    if (real && p.lse) {
+                        p.lse[(size_t)(w.q.first + rr / p.G) * p.Hq + w.h * p.G + rr % p.G] =
+                            sum == 0.f ? -INFINITY : (top + log2f(sum) - kShift) * kLn2;
                     }
                     __syncwarp();
+                } else {
+                    const size_t part = ((size_t)blockIdx.x * 2 + slot) * kMB + row;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t x[32];
+                        tc5::ld32(lanes + kTmemO + c * 32, x);
+                        if (real) {
+                            uint4* o = reinterpret_cast<uint4*>(ws.rows + part * D + c * 32);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (real) ws.ml[part] = make_float2(top, sum);
+                    tc5::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kOFree));
                 }
-                if (real) {
-                    if (!whole) ws.ml[part] = make_float2(top, sum);
-                    else if (p.lse) p.lse[dst] = sum == 0.f ? -INFINITY : (top + log2f(sum) - kShift) * kLn2;
-                }
-                tc5::fence_before();
+            } else if (lane == 0) {
+                mbar_arrive(bar(kOFree));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kOFree));
+            if (lane == 0) mbar_arrive(bar(kStaged + (item & 1)));
             // an item that starts here and goes on: the next kernel joins its parts
             if (u0 == 0 && u1 < w.t.tiles) {
                 todo.parts = (at + w.t.tiles - 1) / per - (int)blockIdx.x + 1;

@@ -158,6 +158,7 @@ struct AttendParams {
     int64_t q_ts, q_hs;
     int q_aligned;       // q's rows admit 16-byte loads
     int page_magic;      // see page_of in cache.cuh
+    uint32_t g_magic;    // ceil(2^32 / G), 0 for G = 1
     const int32_t* offsets;
     void* out;
     float* lse;
