@@ -255,9 +255,6 @@ dspark_status check_cache(const dspark_cache& c)
     return DSPARK_OK;
 }
 
-// One thread takes 8 channels of a key or value row: the grid has to fit
-bool rows_fit(int T, const dspark_cache& c) { return (long long)T * 2 * c.Hkv * (c.D / 8) < (1ll << 38); }
-
 dspark_status check_append(const dspark_cache_append_args* a)
 {
     if (!a || a->struct_size != sizeof(dspark_cache_append_args)) return DSPARK_ERR_INVALID_ARGUMENT;
@@ -265,7 +262,6 @@ dspark_status check_append(const dspark_cache_append_args* a)
     if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
     const dspark_status st = check_cache(a->cache);
     if (st != DSPARK_OK) return st;
-    if (!rows_fit(a->T, a->cache)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
     if (a->T > 0 && (!a->k || !a->v || !a->request || !a->position)) return DSPARK_ERR_INVALID_ARGUMENT;
     return DSPARK_OK;
 }
@@ -277,7 +273,6 @@ dspark_status check_read(const dspark_cache_read_args* a)
     if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
     const dspark_status st = check_cache(a->cache);
     if (st != DSPARK_OK) return st;
-    if (!rows_fit(a->T, a->cache)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
     if (a->T > 0 && (!a->k_out || !a->v_out || !a->request || !a->position)) return DSPARK_ERR_INVALID_ARGUMENT;
     // 16-byte stores
     if (reinterpret_cast<uintptr_t>(a->k_out) % 16 || reinterpret_cast<uintptr_t>(a->v_out) % 16)

@@ -53,116 +53,139 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[kVe
     *reinterpret_cast<uint4*>(p) = v;
 }
 
-// x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0). The remainder x - c s of the
+// x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8. The remainder x - c s of the
 // guess c is one rounding of an exact difference, so its comparison with s / 2 decides exactly.
-__device__ __forceinline__ int nearest_code(float x, float s, float inv)
+__device__ __forceinline__ uint32_t nearest_code(float x, float s, float inv)
 {
-    float c = fminf(fmaxf(rintf(x * inv), -8.f), 8.f);
-    const float r = fmaf(-c, s, x), h = 0.5f * s;
-    const bool odd = ((int)c & 1) != 0;
-    if (r > h || (r == h && odd)) c += 1.f;
-    else if (r < -h || (r == -h && odd)) c -= 1.f;
-    return (int)fminf(fmaxf(c, -7.f), 7.f);
+    float c = rintf(fminf(fmaxf(x * inv, -8.f), 8.f));
+    const float r = fmaf(-c, s, x), off = fabsf(r), h = 0.5f * s;
+    if (off > h || (off == h && ((int)c & 1))) c += copysignf(1.f, r);
+    return (uint32_t)((int)fminf(fmaxf(c, -7.f), 7.f) + 8);
 }
 
-// Flat index = ((token * 2 + (0 = K, 1 = V)) * Hkv + head) * (D / 8) + vec: a warp's threads read
-// consecutive channels; the 4 threads of a group are 4 aligned lanes.
+// A CTA takes `tokens` consecutive tokens. Their pages and slots are looked up once, then thread after thread
+// takes a piece of 8 channels: piece = ((token * 2 + (0 = K, 1 = V)) * Hkv + head) * (D / 8) + vec, so that a
+// warp's threads read consecutive channels and the 4 threads of a group are 4 aligned lanes.
+constexpr int kMaxTokens = 64;
+
 struct RowAt {
     int t, half, h, vec;
 };
 
-__device__ __forceinline__ RowAt row_at(long long i, int Hkv, int vecs)
+__device__ __forceinline__ RowAt row_at(uint32_t i, uint32_t each, int Hkv, uint32_t vecs)
 {
     RowAt a;
-    a.vec = (int)(i % vecs);
-    const long long row = i / vecs;
-    a.h = (int)(row % Hkv);
-    const long long th = row / Hkv;
-    a.half = (int)(th & 1);
-    a.t = (int)(th >> 1);
+    a.t = (int)(i / each);
+    const uint32_t in = i % each;
+    a.vec = (int)(in % vecs);
+    const int row = (int)(in / vecs);
+    a.half = row >= Hkv;
+    a.h = row - a.half * Hkv;
     return a;
 }
 
+__device__ __forceinline__ void look_up(const CacheRowsParams& p, int first, int count, int2* s_at)
+{
+    if ((int)threadIdx.x < count) {
+        int page = -1, slot = 0;
+        const int t = first + threadIdx.x;
+        if (!cache_slot(p.c, p.request[t], p.position[t], p.status, page, slot)) page = -1;
+        s_at[threadIdx.x] = make_int2(page, slot);
+    }
+    __syncthreads();
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsParams p, int aligned)
+__global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsParams p, int aligned, int tokens)
 {
     pdl_enter();
-    const int vecs = p.c.D / kVec, groups = p.c.D / kCacheGroup;
-    const long long n = (long long)p.T * 2 * p.c.Hkv * vecs;
-    const long long i = (long long)blockIdx.x * kRowsThreads + threadIdx.x;
-    const bool in = i < n;
-    const RowAt a = row_at(in ? i : n - 1, p.c.Hkv, vecs);
-    int page = 0, slot = 0;
-    const bool live = in && cache_slot(p.c, p.request[a.t], p.position[a.t], p.status, page, slot);
-    float x[kVec] = {};
-    if (live) {
-        const T* src = a.half == 0 ? static_cast<const T*>(p.k) + a.t * p.k_ts + a.h * p.k_hs
-                                   : static_cast<const T*>(p.v) + a.t * p.v_ts + a.h * p.v_hs;
-        load_vec<T>(src + a.vec * kVec, aligned, x);
-    }
-    float top = 0.f;
-    bool odd_input = false;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const float m = fabsf(x[j]);
-        if (m <= FLT_MAX) {
-            top = fmaxf(top, m);
-        } else {   // an infinity takes the largest code, NaN the code of 0
-            odd_input = true;
-            x[j] = x[j] != x[j] ? 0.f : copysignf(FLT_MAX, x[j]);
-        }
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    if (!live) return;
-    if (odd_input) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
-    const float s8 = __bfloat162float(__float2bfloat16_rn(top * (1.f / 7.f)));
-    const __half sh = __float2half_rn(fminf(s8, kCacheMaxScale));
-    const float s = __half2float(sh);
-    uint32_t word = 0x88888888u;   // the code of 0
-    if (s > 0.f) {
-        const float inv = 1.f / s;
-        word = 0;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) word |= (uint32_t)(nearest_code(x[j], s, inv) + 8) << (4 * j);
-    }
+    __shared__ int2 s_at[kMaxTokens];
+    const uint32_t vecs = p.c.D / kVec, groups = p.c.D / kCacheGroup, each = 2 * p.c.Hkv * vecs;
+    const int first = blockIdx.x * tokens, count = min(tokens, p.T - first);
+    look_up(p, first, count, s_at);
+    const uint32_t n = count * each;   // a multiple of 8: the 4 lanes of a group stay together
     const CacheBlock b = cache_block(p.c.page_size, p.c.D);
-    uint8_t* blk = cache_page_block(p.c, page, a.h, b.bytes);
-    const uint32_t codes = a.half == 0 ? 0u : b.v_codes;
-    *reinterpret_cast<uint32_t*>(blk + codes + (uint32_t)slot * (p.c.D / 2) + a.vec * 4) = word;
-    if (a.vec % 4 == 0) {
-        const int g = a.vec / 4;
-        const uint32_t at = a.half == 0 ? b.k_scales + (uint32_t)(slot * groups + g) * 2u
-                                        : b.v_scales + v_scale_at(slot, g, groups);
-        *reinterpret_cast<__half*>(blk + at) = sh;
+    for (uint32_t i = threadIdx.x; i < (n + 31) / 32 * 32; i += kRowsThreads) {
+        const RowAt a = row_at(min(i, n - 1), each, p.c.Hkv, vecs);
+        const int2 at = s_at[a.t];
+        const bool live = i < n && at.x >= 0;
+        float x[kVec] = {};
+        if (live) {
+            const int64_t t = first + a.t;
+            const T* src = a.half == 0 ? static_cast<const T*>(p.k) + t * p.k_ts + a.h * p.k_hs
+                                       : static_cast<const T*>(p.v) + t * p.v_ts + a.h * p.v_hs;
+            load_vec<T>(src + a.vec * kVec, aligned, x);
+        }
+        float top = 0.f;
+        bool odd_input = false;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const float m = fabsf(x[j]);
+            odd_input |= !(m <= FLT_MAX);
+            top = fmaxf(top, m);   // NaN does not count
+        }
+        if (odd_input) {   // an infinity takes the largest code, NaN the code of 0
+            top = 0.f;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                if (fabsf(x[j]) <= FLT_MAX) top = fmaxf(top, fabsf(x[j]));
+                else x[j] = x[j] != x[j] ? 0.f : copysignf(FLT_MAX, x[j]);
+            }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (!live) continue;
+        if (odd_input) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
+        const float s8 = __bfloat162float(__float2bfloat16_rn(top * (1.f / 7.f)));
+        const __half sh = __float2half_rn(fminf(s8, kCacheMaxScale));
+        const float s = __half2float(sh);
+        uint32_t word = 0x88888888u;   // the code of 0
+        if (s > 0.f) {
+            const float inv = 1.f / s;
+            word = 0;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) word |= nearest_code(x[j], s, inv) << (4 * j);
+        }
+        uint8_t* blk = cache_page_block(p.c, at.x, a.h, b.bytes);
+        const uint32_t codes = a.half == 0 ? 0u : b.v_codes;
+        *reinterpret_cast<uint32_t*>(blk + codes + (uint32_t)at.y * (p.c.D / 2) + a.vec * 4) = word;
+        if (a.vec % 4 == 0) {
+            const int g = a.vec / 4;
+            const uint32_t to = a.half == 0 ? b.k_scales + (uint32_t)(at.y * groups + g) * 2u
+                                            : b.v_scales + v_scale_at(at.y, g, groups);
+            *reinterpret_cast<__half*>(blk + to) = sh;
+        }
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(CacheRowsParams p)
+__global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(CacheRowsParams p, int tokens)
 {
     pdl_enter();
-    const int vecs = p.c.D / kVec, groups = p.c.D / kCacheGroup;
-    const long long n = (long long)p.T * 2 * p.c.Hkv * vecs;
-    const long long i = (long long)blockIdx.x * kRowsThreads + threadIdx.x;
-    if (i >= n) return;
-    const RowAt a = row_at(i, p.c.Hkv, vecs);
-    int page = 0, slot = 0;
-    float x[kVec] = {};
-    if (cache_slot(p.c, p.request[a.t], p.position[a.t], p.status, page, slot)) {
-        const CacheBlock b = cache_block(p.c.page_size, p.c.D);
-        const uint8_t* blk = cache_page_block(p.c, page, a.h, b.bytes);
-        const int g = a.vec / 4;
-        const uint32_t codes = a.half == 0 ? 0u : b.v_codes;
-        const uint32_t at = a.half == 0 ? b.k_scales + (uint32_t)(slot * groups + g) * 2u
-                                        : b.v_scales + v_scale_at(slot, g, groups);
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + codes + (uint32_t)slot * (p.c.D / 2) + a.vec * 4);
-        const float s = __half2float(*reinterpret_cast<const __half*>(blk + at));
+    __shared__ int2 s_at[kMaxTokens];
+    const uint32_t vecs = p.c.D / kVec, groups = p.c.D / kCacheGroup, each = 2 * p.c.Hkv * vecs;
+    const int first = blockIdx.x * tokens, count = min(tokens, p.T - first);
+    look_up(p, first, count, s_at);
+    const uint32_t n = count * each;
+    const CacheBlock b = cache_block(p.c.page_size, p.c.D);
+    for (uint32_t i = threadIdx.x; i < n; i += kRowsThreads) {
+        const RowAt a = row_at(i, each, p.c.Hkv, vecs);
+        const int2 at = s_at[a.t];
+        float x[kVec] = {};
+        if (at.x >= 0) {
+            const uint8_t* blk = cache_page_block(p.c, at.x, a.h, b.bytes);
+            const int g = a.vec / 4;
+            const uint32_t codes = a.half == 0 ? 0u : b.v_codes;
+            const uint32_t from = a.half == 0 ? b.k_scales + (uint32_t)(at.y * groups + g) * 2u
+                                              : b.v_scales + v_scale_at(at.y, g, groups);
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + codes + (uint32_t)at.y * (p.c.D / 2) + a.vec * 4);
+            const float s = __half2float(*reinterpret_cast<const __half*>(blk + from));
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) x[j] = (float)((int)((word >> (4 * j)) & 15u) - 8) * s;
+            for (int j = 0; j < kVec; ++j) x[j] = (float)((int)((word >> (4 * j)) & 15u) - 8) * s;
+        }
+        T* dst = static_cast<T*>(a.half == 0 ? p.k_out : p.v_out) + ((size_t)(first + a.t) * p.c.Hkv + a.h) * p.c.D + a.vec * kVec;
+        store_vec(dst, x);
     }
-    T* dst = static_cast<T*>(a.half == 0 ? p.k_out : p.v_out) + ((size_t)a.t * p.c.Hkv + a.h) * p.c.D + a.vec * kVec;
-    store_vec(dst, x);
 }
 
 template <typename T>
@@ -173,31 +196,35 @@ bool rows_aligned(const CacheRowsParams& p)
     return base % 16 == 0 && (strides * (int64_t)sizeof(T)) % 16 == 0;
 }
 
-long long rows_grid(const CacheRowsParams& p)
+// Tokens of a CTA: pieces for four rounds of its threads, fewer where that leaves SMs without work
+int rows_tokens(const CacheRowsParams& p)
 {
-    const long long n = (long long)p.T * 2 * p.c.Hkv * (p.c.D / kVec);
-    return (n + kRowsThreads - 1) / kRowsThreads;
+    const int each = 2 * p.c.Hkv * (p.c.D / kVec);
+    int tokens = 4 * kRowsThreads / each;
+    const long long fair = ((long long)p.T + 4ll * num_sms() - 1) / (4ll * num_sms());
+    if (tokens > fair) tokens = (int)fair;
+    return tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s)
 {
-    const dim3 grid((unsigned)rows_grid(p));
+    const int tokens = rows_tokens(p);
+    const dim3 grid(cdiv(p.T, tokens)), block(kRowsThreads);
     const cudaError_t e =
         p.dtype == DSPARK_BF16
-            ? launch_pdl(cache_append_kernel<__nv_bfloat16>, grid, dim3(kRowsThreads), 0, s, p,
-                         (int)rows_aligned<__nv_bfloat16>(p))
-            : launch_pdl(cache_append_kernel<float>, grid, dim3(kRowsThreads), 0, s, p, (int)rows_aligned<float>(p));
+            ? launch_pdl(cache_append_kernel<__nv_bfloat16>, grid, block, 0, s, p, (int)rows_aligned<__nv_bfloat16>(p), tokens)
+            : launch_pdl(cache_append_kernel<float>, grid, block, 0, s, p, (int)rows_aligned<float>(p), tokens);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s)
 {
-    const dim3 grid((unsigned)rows_grid(p));
-    const cudaError_t e = p.dtype == DSPARK_BF16
-                              ? launch_pdl(cache_read_kernel<__nv_bfloat16>, grid, dim3(kRowsThreads), 0, s, p)
-                              : launch_pdl(cache_read_kernel<float>, grid, dim3(kRowsThreads), 0, s, p);
+    const int tokens = rows_tokens(p);
+    const dim3 grid(cdiv(p.T, tokens)), block(kRowsThreads);
+    const cudaError_t e = p.dtype == DSPARK_BF16 ? launch_pdl(cache_read_kernel<__nv_bfloat16>, grid, block, 0, s, p, tokens)
+                                                 : launch_pdl(cache_read_kernel<float>, grid, block, 0, s, p, tokens);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -4,8 +4,12 @@
 //   y = x / sqrt(sum x^2 / D + eps) * gain;  pair i turns by phi_i = 2 pi frac(freq[i] position).
 //
 // The turn per position is a 64-bit fraction, so freq * position modulo 2^64 is the exact fraction of
-// a turn: no angle is ever large, and sincospif sees arguments in [-1, 1). A CTA takes one token: the
-// sines and cosines of its rot / 2 pairs are formed once and serve every head of q and k.
+// a turn: no angle is ever large, and sincospif sees arguments in [-1, 1). The sines and cosines of a
+// token's rot / 2 pairs are formed once for many heads.
+//
+// The bytes bound it: each row read once and written once. rope_vec_kernel keeps 16-byte pieces in registers
+// between the norm's sum and the rotation, with several heads' loads in flight; rope_any_kernel takes the
+// shapes that the pieces do not fit.
 #include "common.cuh"
 #include "internal.h"
 
@@ -96,11 +100,183 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(RopeParams p)
     }
 }
 
+// ------------------------------------------------------------------ 8 channels a lane
+//
+// D a multiple of 8 up to 256, rot of 16 (of 2 when interleaved), 16-byte aligned rows: a head is LPH lanes (D / 8
+// rounded up to a power of two), a warp takes 32 / LPH heads at a time, kUnroll such loads in flight, and `share` warps
+// share a token (one where there are tokens enough: the sines serve all its heads then).
+template <typename T>
+struct Vec {
+    uint32_t u[2 * sizeof(T)];   // 8 elements
+};
+
+template <typename T>
+__device__ __forceinline__ Vec<T> load_row(const T* p, bool on)
+{
+    Vec<T> v = {};
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+            v.u[4 * i] = x.x;
+            v.u[4 * i + 1] = x.y;
+            v.u[4 * i + 2] = x.z;
+            v.u[4 * i + 3] = x.w;
+        }
+    }
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ float element(const Vec<T>& v, int i)
+{
+    if (sizeof(T) == 4) return __uint_as_float(v.u[i % (2 * sizeof(T))]);
+    return __uint_as_float(i % 2 ? v.u[i / 2] & 0xFFFF0000u : v.u[i / 2] << 16);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* p, const float (&y)[8])
+{
+    uint32_t u[2 * sizeof(T)];
+#pragma unroll
+    for (int i = 0; i < 8 / (4 / (int)sizeof(T)); ++i) {
+        if (sizeof(T) == 4) {
+            u[i % (2 * sizeof(T))] = __float_as_uint(y[i]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[(2 * i) % 8], y[(2 * i + 1) % 8]);
+            u[i % (2 * sizeof(T))] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+}
+
+constexpr int kVecWarps = 8;
+
+template <typename T, int LPH>
+__global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, int share)
+{
+    constexpr int kHeads = 32 / LPH;                      // heads of a warp's step
+    constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
+    pdl_enter();
+    __shared__ float2 s_cs[kVecWarps][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * (kVecWarps / share) + warp / share, part = warp % share;
+    if (t >= p.T) return;
+    const int l = lane % LPH, sub = lane / LPH, c0 = l * 8;
+    const bool on = c0 < p.D;
+    long long pos = 0;
+    const bool live = token_position(p, t, pos);
+    const int half = p.rot / 2;
+    if (live)
+        for (int i = lane; i < half; i += 32) s_cs[warp][i] = turn(p.freq[i], pos);
+    __syncwarp();
+    // what each of the lane's channels takes of itself and of its pair's other channel
+    float own[8], other[8];
+    const int step = half / 8;                            // lanes between the channels of a pair
+    const bool turned = c0 < p.rot, second = !p.interleaved && l >= step;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = c0 + i;
+        const bool in = turned && c < p.rot;
+        const float2 cs = in ? s_cs[warp][p.interleaved ? c / 2 : c - (second ? half : 0)] : make_float2(1.f, 0.f);
+        own[i] = cs.x;
+        other[i] = (p.interleaved ? (i & 1) != 0 : second) ? cs.y : -cs.y;
+    }
+    const int mate = p.interleaved || !turned ? lane : lane + (second ? -step : step);
+    const int mate_c0 = (mate % LPH) * 8;
+#pragma unroll 1
+    for (int is_k = 0; is_k < 2; ++is_k) {
+        const int heads = is_k ? p.Hkv : p.Hq;
+        const T* x0 = static_cast<const T*>(is_k ? p.k : p.q) + (int64_t)t * (is_k ? p.k_ts : p.q_ts) + c0;
+        const int64_t hs = is_k ? p.k_hs : p.q_hs;
+        T* y0 = static_cast<T*>(is_k ? p.k_out : p.q_out) + (size_t)t * heads * p.D + c0;
+        const float* gain = is_k ? p.k_gain : p.q_gain;
+        float a[8], b[8];                                 // the factors above times the gains
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = p.interleaved ? i ^ 1 : i;
+            a[i] = own[i] * (gain && on ? gain[c0 + i] : 1.f);
+            b[i] = other[i] * (gain && on ? gain[min(mate_c0 + j, p.D - 1)] : 1.f);
+        }
+#pragma unroll 1
+        for (int h0 = part * kHeads; h0 < heads; h0 += share * kHeads * kUnroll) {
+            Vec<T> v[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int h = h0 + k * share * kHeads + sub;
+                v[k] = load_row<T>(x0 + h * hs, on && live && h < heads);
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int h = h0 + k * share * kHeads + sub;
+                float inv = 1.f;
+                if (p.norm) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum = fmaf(element(v[k], i), element(v[k], i), sum);
+#pragma unroll
+                    for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    inv = 1.f / sqrtf(sum / (float)p.D + p.eps);
+                }
+                Vec<T> w = v[k];
+                if (!p.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 2 * (int)sizeof(T); ++i) w.u[i] = __shfl_sync(0xffffffffu, v[k].u[i], mate);
+                }
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = turned ? fmaf(element(v[k], i) * inv, a[i],
+                                         (p.interleaved ? element(v[k], i ^ 1) : element(w, i)) * inv * b[i])
+                                  : element(v[k], i) * inv * a[i];
+                if (!live) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = 0.f;
+                }
+                if (on && h < heads) store_row<T>(y0 + (size_t)h * p.D, y);
+            }
+        }
+    }
+}
+
+template <typename T>
+bool vec_fits(const RopeParams& p)
+{
+    const uintptr_t base = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
+                           reinterpret_cast<uintptr_t>(p.q_out) | reinterpret_cast<uintptr_t>(p.k_out);
+    const int64_t strides = p.q_ts | p.q_hs | p.k_ts | p.k_hs;
+    return p.D % 8 == 0 && p.D <= 256 && (p.interleaved || p.rot % 16 == 0) && base % 16 == 0 &&
+           (strides * (int64_t)sizeof(T)) % 16 == 0;
+}
+
+template <typename T>
+cudaError_t launch_vec(const RopeParams& p, cudaStream_t s)
+{
+    const int lph = p.D <= 32 ? 4 : p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
+    // warps that share a token: as many as give each SM some 16 warps, and each warp a head
+    int share = 1;
+    while (share < kVecWarps && (long long)p.T * share < 16ll * num_sms() && share * (32 / lph) < p.Hq) share *= 2;
+    const dim3 grid(cdiv(p.T, kVecWarps / share)), block(kVecWarps * 32);
+    switch (lph) {
+    case 4: return launch_pdl(rope_vec_kernel<T, 4>, grid, block, 0, s, p, share);
+    case 8: return launch_pdl(rope_vec_kernel<T, 8>, grid, block, 0, s, p, share);
+    case 16: return launch_pdl(rope_vec_kernel<T, 16>, grid, block, 0, s, p, share);
+    default: return launch_pdl(rope_vec_kernel<T, 32>, grid, block, 0, s, p, share);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s)
 {
-    const cudaError_t e = p.dtype == DSPARK_BF16
+    const bool bf = p.dtype == DSPARK_BF16;
+    if (bf ? vec_fits<__nv_bfloat16>(p) : vec_fits<float>(p)) {
+        const cudaError_t v = bf ? launch_vec<__nv_bfloat16>(p, s) : launch_vec<float>(p, s);
+        return v != cudaSuccess ? v : cudaGetLastError();
+    }
+    const cudaError_t e = bf
                               ? launch_pdl(rope_any_kernel<__nv_bfloat16>, dim3(p.T), dim3(kRopeThreads), 0, s, p)
                               : launch_pdl(rope_any_kernel<float>, dim3(p.T), dim3(kRopeThreads), 0, s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
