@@ -53,14 +53,46 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[kVe
     *reinterpret_cast<uint4*>(p) = v;
 }
 
-// x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8. The remainder x - c s of the
-// guess c is one rounding of an exact difference, so its comparison with s / 2 decides exactly.
-__device__ __forceinline__ uint32_t nearest_code(float x, float s, float inv)
+// x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8.
+//
+// Adding 1.5 2^23 + 8 rounds x / s (|x| held to 7 s) to an integer, whose 4 bits are then the number's lowest. The
+// product with 1 / s may fall on the wrong side of a border. The remainder x - c s is one rounding of an exact difference, so
+// one that is not below s / 2 shows that, or a tie: these rare pieces go through settle_code.
+constexpr float kRound = 12582912.f + 8.f;
+
+__device__ __noinline__ uint32_t settle_code(float x, float s, float inv)
 {
-    float c = rintf(fminf(fmaxf(x * inv, -8.f), 8.f));
+    float c = fmaf(x, inv, kRound) - kRound;
     const float r = fmaf(-c, s, x), off = fabsf(r), h = 0.5f * s;
     if (off > h || (off == h && ((int)c & 1))) c += copysignf(1.f, r);
     return (uint32_t)((int)fminf(fmaxf(c, -7.f), 7.f) + 8);
+}
+
+// The 8 codes of x in a word.
+__device__ __forceinline__ uint32_t code_word(const float (&x)[kVec], float s)
+{
+    const float inv = 1.f / s, most = 7.f * s, h = 0.5f * s;
+    uint32_t word = 0;
+    bool settle = false;
+    float v[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        v[j] = fminf(fmaxf(x[j], -most), most);
+        const float t = fmaf(v[j], inv, kRound);
+        settle |= fabsf(fmaf(kRound - t, s, v[j])) >= h;
+        word |= (__float_as_uint(t) & 15u) << (4 * j);
+    }
+    if (settle) {
+        word = 0;
+#pragma unroll 1
+        for (int j = 0; j < kVec; ++j) {
+            float y = v[0];
+#pragma unroll
+            for (int k = 1; k < kVec; ++k) y = k == j ? v[k] : y;
+            word |= settle_code(y, s, inv) << (4 * j);
+        }
+    }
+    return word;
 }
 
 // A CTA takes `tokens` consecutive tokens. Their pages and slots are looked up once, then thread after thread
@@ -139,13 +171,7 @@ __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsPar
         const float s8 = __bfloat162float(__float2bfloat16_rn(top * (1.f / 7.f)));
         const __half sh = __float2half_rn(fminf(s8, kCacheMaxScale));
         const float s = __half2float(sh);
-        uint32_t word = 0x88888888u;   // the code of 0
-        if (s > 0.f) {
-            const float inv = 1.f / s;
-            word = 0;
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) word |= nearest_code(x[j], s, inv) << (4 * j);
-        }
+        const uint32_t word = s > 0.f ? code_word(x, s) : 0x88888888u;   // the code of 0
         uint8_t* blk = cache_page_block(p.c, at.x, a.h, b.bytes);
         const uint32_t codes = a.half == 0 ? 0u : b.v_codes;
         *reinterpret_cast<uint32_t*>(blk + codes + (uint32_t)at.y * (p.c.D / 2) + a.vec * 4) = word;
@@ -168,6 +194,7 @@ __global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(CacheRowsParam
     look_up(p, first, count, s_at);
     const uint32_t n = count * each;
     const CacheBlock b = cache_block(p.c.page_size, p.c.D);
+#pragma unroll 2
     for (uint32_t i = threadIdx.x; i < n; i += kRowsThreads) {
         const RowAt a = row_at(i, each, p.c.Hkv, vecs);
         const int2 at = s_at[a.t];
@@ -196,11 +223,11 @@ bool rows_aligned(const CacheRowsParams& p)
     return base % 16 == 0 && (strides * (int64_t)sizeof(T)) % 16 == 0;
 }
 
-// Tokens of a CTA: pieces for four rounds of its threads, fewer where that leaves SMs without work
+// Tokens of a CTA: pieces for eight rounds of its threads, fewer where that leaves SMs without work
 int rows_tokens(const CacheRowsParams& p)
 {
     const int each = 2 * p.c.Hkv * (p.c.D / kVec);
-    int tokens = 4 * kRowsThreads / each;
+    int tokens = 8 * kRowsThreads / each;
     const long long fair = ((long long)p.T + 4ll * num_sms() - 1) / (4ll * num_sms());
     if (tokens > fair) tokens = (int)fair;
     return tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;

@@ -127,11 +127,12 @@ __device__ __forceinline__ Vec<T> load_row(const T* p, bool on)
     return v;
 }
 
+// elements 2 i and 2 i + 1
 template <typename T>
-__device__ __forceinline__ float element(const Vec<T>& v, int i)
+__device__ __forceinline__ uint64_t pair(const Vec<T>& v, int i)
 {
-    if (sizeof(T) == 4) return __uint_as_float(v.u[i % (2 * sizeof(T))]);
-    return __uint_as_float(i % 2 ? v.u[i / 2] & 0xFFFF0000u : v.u[i / 2] << 16);
+    if (sizeof(T) == 4) return pack2(__uint_as_float(v.u[(2 * i) % (2 * sizeof(T))]), __uint_as_float(v.u[(2 * i + 1) % (2 * sizeof(T))]));
+    return pack2(__uint_as_float(v.u[i % 4] << 16), __uint_as_float(v.u[i % 4] & 0xFFFF0000u));
 }
 
 template <typename T>
@@ -154,7 +155,7 @@ __device__ __forceinline__ void store_row(T* p, const float (&y)[8])
 
 constexpr int kVecWarps = 8;
 
-template <typename T, int LPH>
+template <typename T, int LPH, bool kInter>
 __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, int share)
 {
     constexpr int kHeads = 32 / LPH;                      // heads of a warp's step
@@ -173,19 +174,19 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
         for (int i = lane; i < half; i += 32) s_cs[warp][i] = turn(p.freq[i], pos);
     __syncwarp();
     // what each of the lane's channels takes of itself and of its pair's other channel
-    float own[8], other[8];
     const int step = half / 8;                            // lanes between the channels of a pair
-    const bool turned = c0 < p.rot, second = !p.interleaved && l >= step;
+    const bool turned = c0 < p.rot, second = !kInter && l >= step;
+    const int mate = kInter || !turned ? lane : lane + (second ? -step : step);
+    const int mate_c0 = (mate % LPH) * 8;
+    float own[8], other[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int c = c0 + i;
-        const bool in = turned && c < p.rot;
-        const float2 cs = in ? s_cs[warp][p.interleaved ? c / 2 : c - (second ? half : 0)] : make_float2(1.f, 0.f);
+        const float2 cs = c < p.rot ? s_cs[warp][kInter ? c / 2 : c - (second ? half : 0)] : make_float2(1.f, 0.f);
         own[i] = cs.x;
-        other[i] = (p.interleaved ? (i & 1) != 0 : second) ? cs.y : -cs.y;
+        other[i] = (kInter ? (i & 1) != 0 : second) ? cs.y : -cs.y;
     }
-    const int mate = p.interleaved || !turned ? lane : lane + (second ? -step : step);
-    const int mate_c0 = (mate % LPH) * 8;
+    const float per = 1.f / (float)p.D;
 #pragma unroll 1
     for (int is_k = 0; is_k < 2; ++is_k) {
         const int heads = is_k ? p.Hkv : p.Hq;
@@ -193,12 +194,18 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
         const int64_t hs = is_k ? p.k_hs : p.q_hs;
         T* y0 = static_cast<T*>(is_k ? p.k_out : p.q_out) + (size_t)t * heads * p.D + c0;
         const float* gain = is_k ? p.k_gain : p.q_gain;
-        float a[8], b[8];                                 // the factors above times the gains
+        uint64_t a[4], b[4];                              // the factors above times the gains
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = p.interleaved ? i ^ 1 : i;
-            a[i] = own[i] * (gain && on ? gain[c0 + i] : 1.f);
-            b[i] = other[i] * (gain && on ? gain[min(mate_c0 + j, p.D - 1)] : 1.f);
+        for (int i = 0; i < 4; ++i) {
+            float u[2], v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = 2 * i + e;
+                u[e] = own[c] * (gain && on ? gain[c0 + c] : 1.f);
+                v[e] = other[c] * (gain && on ? gain[kInter ? c0 + (c ^ 1) : min(mate_c0 + c, p.D - 1)] : 1.f);
+            }
+            a[i] = pack2(u[0], u[1]);
+            b[i] = pack2(v[0], v[1]);
         }
 #pragma unroll 1
         for (int h0 = part * kHeads; h0 < heads; h0 += share * kHeads * kUnroll) {
@@ -211,29 +218,43 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
 #pragma unroll
             for (int k = 0; k < kUnroll; ++k) {
                 const int h = h0 + k * share * kHeads + sub;
+                uint64_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = pair(v[k], i);
                 float inv = 1.f;
                 if (p.norm) {
-                    float sum = 0.f;
+                    uint64_t two = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum = fmaf(element(v[k], i), element(v[k], i), sum);
+                    for (int i = 1; i < 4; ++i) two = fma2(x[i], x[i], two);
+                    float sum, more;
+                    unpack2(two, sum, more);
+                    sum += more;
 #pragma unroll
                     for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    inv = 1.f / sqrtf(sum / (float)p.D + p.eps);
+                    inv = rsqrtf(fmaf(sum, per, p.eps));
                 }
+                if (!live) inv = 0.f;
+                const uint64_t inv2 = pack2(inv, inv);
                 Vec<T> w = v[k];
-                if (!p.interleaved) {
+                if (!kInter) {
 #pragma unroll
                     for (int i = 0; i < 2 * (int)sizeof(T); ++i) w.u[i] = __shfl_sync(0xffffffffu, v[k].u[i], mate);
                 }
                 float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = turned ? fmaf(element(v[k], i) * inv, a[i],
-                                         (p.interleaved ? element(v[k], i ^ 1) : element(w, i)) * inv * b[i])
-                                  : element(v[k], i) * inv * a[i];
-                if (!live) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    uint64_t o;
+                    if (kInter) {
+                        float lo, hi;
+                        unpack2(x[i], lo, hi);
+                        o = pack2(hi, lo);
+                    } else {
+                        o = pair(w, i);
+                    }
+                    // channels that are not turned leave the others' alone: 0 times an infinity would be NaN
+                    uint64_t r = mul2(x[i], a[i]);
+                    if (turned) r = fma2(o, b[i], r);
+                    unpack2(mul2(r, inv2), y[2 * i], y[2 * i + 1]);
                 }
                 if (on && h < heads) store_row<T>(y0 + (size_t)h * p.D, y);
             }
@@ -251,8 +272,8 @@ bool vec_fits(const RopeParams& p)
            (strides * (int64_t)sizeof(T)) % 16 == 0;
 }
 
-template <typename T>
-cudaError_t launch_vec(const RopeParams& p, cudaStream_t s)
+template <typename T, bool kInter>
+cudaError_t launch_lanes(const RopeParams& p, cudaStream_t s)
 {
     const int lph = p.D <= 32 ? 4 : p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
     // warps that share a token: as many as give each SM some 16 warps, and each warp a head
@@ -260,11 +281,17 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t s)
     while (share < kVecWarps && (long long)p.T * share < 16ll * num_sms() && share * (32 / lph) < p.Hq) share *= 2;
     const dim3 grid(cdiv(p.T, kVecWarps / share)), block(kVecWarps * 32);
     switch (lph) {
-    case 4: return launch_pdl(rope_vec_kernel<T, 4>, grid, block, 0, s, p, share);
-    case 8: return launch_pdl(rope_vec_kernel<T, 8>, grid, block, 0, s, p, share);
-    case 16: return launch_pdl(rope_vec_kernel<T, 16>, grid, block, 0, s, p, share);
-    default: return launch_pdl(rope_vec_kernel<T, 32>, grid, block, 0, s, p, share);
+    case 4: return launch_pdl(rope_vec_kernel<T, 4, kInter>, grid, block, 0, s, p, share);
+    case 8: return launch_pdl(rope_vec_kernel<T, 8, kInter>, grid, block, 0, s, p, share);
+    case 16: return launch_pdl(rope_vec_kernel<T, 16, kInter>, grid, block, 0, s, p, share);
+    default: return launch_pdl(rope_vec_kernel<T, 32, kInter>, grid, block, 0, s, p, share);
     }
+}
+
+template <typename T>
+cudaError_t launch_vec(const RopeParams& p, cudaStream_t s)
+{
+    return p.interleaved ? launch_lanes<T, true>(p, s) : launch_lanes<T, false>(p, s);
 }
 
 }  // namespace
