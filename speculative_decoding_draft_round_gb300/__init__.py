@@ -537,20 +537,41 @@ def verify(target, U, E, W, anchor, tokens, draft_lse, draft_logit, keep, temper
 CACHE_GROUP = 32     # channels that share a scale
 
 
-def _strided(t, name, dtype=None, width=None):
-    """Rows [T][heads][D] whose last axis is contiguous; returns (token stride, head stride)."""
+# These calls are made for every layer of a pass, so their checks are quick where all is well: one comparison
+# a property, and the slow, explaining check only where one fails.
+
+def _need(t, name, dtype, shape):
+    """A contiguous CUDA tensor of this type and shape."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype, shape)
+    return _ptr(t)
+
+
+def _strided(t, name, dtype=None, shape=None):
+    """Rows [T][heads][D] whose last axis is contiguous; returns (pointer, token stride, head stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dim() != 3:
         raise ValueError("%s must have shape [tokens][heads][width], got %s" % (name, tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if width is not None and t.shape[2] != width:
-        raise ValueError("%s must have heads of width %d, got %d" % (name, width, t.shape[2]))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     st = t.stride()
     if st[2] != 1 and t.shape[2] > 1:
         raise ValueError("the last axis of %s must be contiguous" % name)
-    return st[0], st[1]
+    return t.data_ptr(), st[0], st[1]
+
+
+def _launch(name, fn, args, workspace, stream):
+    """One call of the C ABI on `stream`, by default the current one of the workspace's device."""
+    if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor of uint8")
+    s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(workspace.device).cuda_stream
+    rc = fn(C.byref(args), workspace.data_ptr(), workspace.numel(), s)
+    if rc != 0:
+        raise DsparkError(name, rc, lib().dspark_last_error().decode() if rc == 4 else "")
 
 
 def _on(stream):
@@ -579,38 +600,33 @@ def rope_frequencies(rot, base=10000.0, *, device="cuda"):
 
 def qk_norm_rope_args(q, k, freq, position, *, request=None, ctx_len=None, q_gain=None, k_gain=None, eps=1e-6,
                       norm=True, interleaved=False, out=None):
+    qp, q_ts, q_hs = _strided(q, "q")
     T, Hq, D = q.shape
-    Hkv = k.shape[1]
     dt = q.dtype
-    a = QkNormRopeArgs()
-    a.q_token_stride, a.q_head_stride = _strided(q, "q")
-    a.k_token_stride, a.k_head_stride = _strided(k, "k", dt, D)
-    if k.shape[0] != T:
-        raise ValueError("q has %d tokens, k %d" % (T, k.shape[0]))
-    rot = 0
+    kp, k_ts, k_hs = _strided(k, "k", dt, (T, k.shape[1], D) if k.dim() == 3 else None)
+    Hkv = k.shape[1]
+    rot, fp = 0, None
     if freq is not None:
-        _dev(freq, "freq", torch.int64)
         rot = 2 * freq.numel()
-    _dev(position, "position", torch.int32, (T,))
-    _dev(request, "request", torch.int32, (T,))
-    _dev(ctx_len, "ctx_len", torch.int32)
-    _dev(q_gain, "q_gain", torch.float32, (D,))
-    _dev(k_gain, "k_gain", torch.float32, (D,))
-    if request is not None and ctx_len is None:
+        fp = _need(freq, "freq", torch.int64, (rot // 2,))
+    i32, f32 = torch.int32, torch.float32
+    pp = _need(position, "position", i32, (T,))
+    rp = None if request is None else _need(request, "request", i32, (T,))
+    R, cp = 0, None
+    if ctx_len is not None:
+        R = ctx_len.numel()
+        cp = _need(ctx_len, "ctx_len", i32, (R,))
+    elif request is not None:
         raise ValueError("request needs ctx_len, whose length is the number of requests")
+    gq = None if q_gain is None else _need(q_gain, "q_gain", f32, (D,))
+    gk = None if k_gain is None else _need(k_gain, "k_gain", f32, (D,))
     if out is None:
         out = {"q": torch.empty((T, Hq, D), dtype=dt, device=q.device),
                "k": torch.empty((T, Hkv, D), dtype=dt, device=q.device)}
-    else:
-        _dev(out["q"], "out q", dt, (T, Hq, D))
-        _dev(out["k"], "out k", dt, (T, Hkv, D))
-    a.struct_size = C.sizeof(QkNormRopeArgs)
-    a.T, a.Hq, a.Hkv, a.D, a.rot, a.dtype = T, Hq, Hkv, D, rot, _dtype_code(q)
-    a.norm, a.interleaved, a.eps = int(bool(norm)), int(bool(interleaved)), float(eps)
-    a.R = 0 if ctx_len is None else ctx_len.numel()
-    a.q, a.k, a.q_gain, a.k_gain, a.freq = _ptr(q), _ptr(k), _ptr(q_gain), _ptr(k_gain), _ptr(freq)
-    a.position, a.request, a.ctx_len = _ptr(position), _ptr(request), _ptr(ctx_len)
-    a.q_out, a.k_out = _ptr(out["q"]), _ptr(out["k"])
+    oq, ok = _need(out["q"], "out q", dt, (T, Hq, D)), _need(out["k"], "out k", dt, (T, Hkv, D))
+    a = QkNormRopeArgs(C.sizeof(QkNormRopeArgs), T, Hq, Hkv, D, rot, _dtype_code(q), 1 if norm else 0,
+                       1 if interleaved else 0, R, eps, 0, qp, kp, q_ts, q_hs, k_ts, k_hs, gq, gk, fp, pp, rp, cp,
+                       oq, ok)
     return a, out
 
 
@@ -620,11 +636,15 @@ def qk_norm_rope(q, k, freq, position, *, request=None, ctx_len=None, q_gain=Non
     head and rotated; returns {"q", "k"}. freq: rope_frequencies(rot), None for no rotation. position: int32
     [T]; with request [T] and ctx_len [R] the tokens of a request follow its ctx_len tokens, and rows with
     request < 0 are written as zeros."""
-    with _on(stream):
+    if out is None and stream is not None:
+        with _on(stream):
+            a, out = qk_norm_rope_args(q, k, freq, position, request=request, ctx_len=ctx_len, q_gain=q_gain,
+                                       k_gain=k_gain, eps=eps, norm=norm, interleaved=interleaved)
+    else:
         a, out = qk_norm_rope_args(q, k, freq, position, request=request, ctx_len=ctx_len, q_gain=q_gain,
                                    k_gain=k_gain, eps=eps, norm=norm, interleaved=interleaved, out=out)
     ws = _status_workspace(workspace, q.device, stream)
-    _call("dspark_qk_norm_rope", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    _launch("dspark_qk_norm_rope", lib().dspark_qk_norm_rope, a, ws, stream)
     out["workspace"] = ws
     return out
 
@@ -644,37 +664,29 @@ def cache_pool(n_pages, Hkv, page_size, D, *, device="cuda"):
 
 def cache_view(pool, table, ctx_len, D):
     """The C struct of a cache: pool (cache_pool), table [R][width] int32, ctx_len [R] int32."""
-    _dev(pool, "pool", torch.uint8)
-    _dev(table, "table", torch.int32)
+    if not isinstance(pool, torch.Tensor) or not isinstance(table, torch.Tensor):
+        raise TypeError("pool and table must be CUDA tensors")
     if pool.dim() != 3 or table.dim() != 2:
         raise ValueError("pool must be [pages][heads][block] and table [requests][pages]")
     R, width = table.shape
-    _dev(ctx_len, "ctx_len", torch.int32, (R,))
     n_pages, Hkv, block = pool.shape
     page_size = block * 8 // (9 * D) if D > 0 else 0
     if page_size * D * 9 != block * 8:
         raise ValueError("pool blocks of %d bytes hold no whole tokens of width %d" % (block, D))
-    c = Cache()
-    c.pages, c.n_pages, c.page_size, c.Hkv, c.D = _ptr(pool), n_pages, page_size, Hkv, D
-    c.R, c.table_width, c.table, c.ctx_len = R, width, _ptr(table), _ptr(ctx_len)
-    return c
+    return Cache(_need(pool, "pool", torch.uint8, (n_pages, Hkv, block)), n_pages, page_size, Hkv, D, R, width, 0,
+                 _need(table, "table", torch.int32, (R, width)), _need(ctx_len, "ctx_len", torch.int32, (R,)))
 
 
 def cache_append_args(k, v, pool, table, request, position, ctx_len):
-    a = CacheAppendArgs()
+    kp, k_ts, k_hs = _strided(k, "k")
     T, Hkv, D = k.shape
-    a.k_token_stride, a.k_head_stride = _strided(k, "k")
-    a.v_token_stride, a.v_head_stride = _strided(v, "v", k.dtype, D)
-    a.cache = cache_view(pool, table, ctx_len, D)
-    if tuple(v.shape) != (T, Hkv, D) or pool.shape[1] != Hkv:
-        raise ValueError("k %s, v %s and the pool's %d heads do not match" % (tuple(k.shape), tuple(v.shape),
-                                                                           pool.shape[1]))
-    _dev(request, "request", torch.int32, (T,))
-    _dev(position, "position", torch.int32, (T,))
-    a.struct_size = C.sizeof(CacheAppendArgs)
-    a.T, a.dtype = T, _dtype_code(k)
-    a.k, a.v, a.request, a.position = _ptr(k), _ptr(v), _ptr(request), _ptr(position)
-    return a
+    vp, v_ts, v_hs = _strided(v, "v", k.dtype, (T, Hkv, D))
+    cache = cache_view(pool, table, ctx_len, D)
+    if pool.shape[1] != Hkv:
+        raise ValueError("k has %d heads, the pool %d" % (Hkv, pool.shape[1]))
+    return CacheAppendArgs(C.sizeof(CacheAppendArgs), T, _dtype_code(k), 0, cache, kp, vp, k_ts, k_hs, v_ts, v_hs,
+                           _need(request, "request", torch.int32, (T,)),
+                           _need(position, "position", torch.int32, (T,)))
 
 
 def cache_append(k, v, pool, table, request, position, ctx_len, *, workspace=None, stream=None):
@@ -682,24 +694,19 @@ def cache_append(k, v, pool, table, request, position, ctx_len, *, workspace=Non
     cache, at position ctx_len[request] + position. Returns {"workspace"}."""
     a = cache_append_args(k, v, pool, table, request, position, ctx_len)
     ws = _status_workspace(workspace, k.device, stream)
-    _call("dspark_cache_append", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    _launch("dspark_cache_append", lib().dspark_cache_append, a, ws, stream)
     return {"workspace": ws}
 
 
 def cache_read_args(pool, table, request, position, ctx_len, *, D, dtype=torch.bfloat16, out=None):
-    a = CacheReadArgs()
-    a.cache = cache_view(pool, table, ctx_len, D)
+    cache = cache_view(pool, table, ctx_len, D)
     T, Hkv = request.numel(), pool.shape[1]
-    _dev(request, "request", torch.int32, (T,))
-    _dev(position, "position", torch.int32, (T,))
     if out is None:
         out = {n: torch.empty((T, Hkv, D), dtype=dtype, device=pool.device) for n in ("k", "v")}
-    else:
-        for n in ("k", "v"):
-            _dev(out[n], "out " + n, dtype, (T, Hkv, D))
-    a.struct_size = C.sizeof(CacheReadArgs)
-    a.T, a.dtype = T, _dtype_code(out["k"])
-    a.request, a.position, a.k_out, a.v_out = _ptr(request), _ptr(position), _ptr(out["k"]), _ptr(out["v"])
+    kp, vp = (_need(out[n], "out " + n, dtype, (T, Hkv, D)) for n in ("k", "v"))
+    a = CacheReadArgs(C.sizeof(CacheReadArgs), T, _dtype_code(out["k"]), 0, cache,
+                      _need(request, "request", torch.int32, (T,)),
+                      _need(position, "position", torch.int32, (T,)), kp, vp)
     return a, out
 
 
@@ -707,34 +714,32 @@ def cache_read(pool, table, request, position, ctx_len, *, D, dtype=torch.bfloat
                stream=None):
     """dspark_cache_read: the cached rows of the tokens (request, position) as values; returns {"k", "v"}
     [T][Hkv][D], zeros where request < 0."""
-    with _on(stream):
+    if out is None and stream is not None:
+        with _on(stream):
+            a, out = cache_read_args(pool, table, request, position, ctx_len, D=D, dtype=dtype)
+    else:
         a, out = cache_read_args(pool, table, request, position, ctx_len, D=D, dtype=dtype, out=out)
     ws = _status_workspace(workspace, pool.device, stream)
-    _call("dspark_cache_read", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    _launch("dspark_cache_read", lib().dspark_cache_read, a, ws, stream)
     out["workspace"] = ws
     return out
 
 
 def cache_attend_args(q, pool, table, offsets, ctx_len, *, scale=None, window=0, sinks=0, max_q=None,
                       path=PATH_AUTO, lse=True, out=None):
-    a = CacheAttendArgs()
+    qp, q_ts, q_hs = _strided(q, "q")
     T, Hq, D = q.shape
-    a.q_token_stride, a.q_head_stride = _strided(q, "q")
-    a.cache = cache_view(pool, table, ctx_len, D)
-    _dev(offsets, "offsets", torch.int32, (table.shape[0] + 1,))
+    cache = cache_view(pool, table, ctx_len, D)
+    fp = _need(offsets, "offsets", torch.int32, (table.shape[0] + 1,))
     if out is None:
         out = {"out": torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)}
         if lse:
             out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    else:
-        _dev(out["out"], "out", q.dtype, (T, Hq, D))
-        _dev(out.get("lse"), "lse", torch.float32, (T, Hq))
-    a.struct_size = C.sizeof(CacheAttendArgs)
-    a.T, a.Hq, a.dtype, a.path = T, Hq, _dtype_code(q), int(path)
-    a.max_q = max(1, T) if max_q is None else int(max_q)
-    a.window, a.sinks = int(window), int(sinks)
-    a.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    a.q, a.offsets, a.out, a.lse = _ptr(q), _ptr(offsets), _ptr(out["out"]), _ptr(out.get("lse"))
+    l = out.get("lse")
+    a = CacheAttendArgs(C.sizeof(CacheAttendArgs), T, Hq, _dtype_code(q), path, max(1, T) if max_q is None else max_q,
+                        window, sinks, 1.0 / math.sqrt(D) if scale is None else scale, 0, cache, qp, q_ts, q_hs, fp,
+                        _need(out["out"], "out", q.dtype, (T, Hq, D)),
+                        None if l is None else _need(l, "lse", torch.float32, (T, Hq)))
     return a, out
 
 
@@ -747,9 +752,10 @@ def cache_attend(q, pool, table, offsets, ctx_len, *, scale=None, window=0, sink
     with _on(stream):
         a, out = cache_attend_args(q, pool, table, offsets, ctx_len, scale=scale, window=window, sinks=sinks,
                                    max_q=max_q, path=path, lse=lse, out=out)
-        ws = _workspace("dspark_cache_attend_workspace_size", a, workspace, q.device)
-    _call("dspark_cache_attend", C.byref(a), _ptr(ws), ws.numel(), _stream(stream))
-    out["workspace"] = ws
+        if workspace is None:
+            workspace = torch.zeros(workspace_bytes("cache_attend", a), dtype=torch.uint8, device=q.device)
+    _launch("dspark_cache_attend", lib().dspark_cache_attend, a, workspace, stream)
+    out["workspace"] = workspace
     return out
 
 
