@@ -57,7 +57,11 @@ __device__ __forceinline__ uint32_t pack(float a, float b) { return as_u32(__flo
 // what its scores take back to log2 units with. Never 0: 0 times a masked score would be NaN.
 __device__ __forceinline__ float row_up(int ex) { return __uint_as_float((uint32_t)min(266 - ex, 254) << 23); }
 
-__device__ __forceinline__ float row_factor(float to_log2, float up) { return fmaxf(to_log2 / up, 1e-37f); }
+__device__ __forceinline__ float row_factor(float to_log2, float up)
+{
+    // 1 / up by its exponent
+    return fmaxf(to_log2 * __uint_as_float((254u << 23) - __float_as_uint(up)), 1e-37f);
+}
 
 // the lowest n bits, all for n >= 32, none for n <= 0
 __device__ __forceinline__ uint32_t below(int n)

@@ -6,15 +6,14 @@
 // An item is 128 rows (query heads of consecutive queries) of one request and key / value head, a tile 128
 // tokens. The items' tiles form one line that is cut into equal runs, one a CTA and SM, whatever the lengths
 // are; a block's tiles are those its own rows reach. Per tile, by warp:
-//   8 - 15  turn codes into fp16 (exact: scales have 8 bits) in shared memory: K by token, V transposed
+//   12 - 19 turn codes into fp16 (exact: scales have 8 bits) in shared memory: K by token, V transposed
 //           by channel, both K-major with the 128-byte swizzle; the next tile's codes are loaded before.
 //           A thread takes 8 tokens of 8 value channels, so the transposition is its choice of registers.
 //   0       issues S = Q K^T (128 x 128 x D, operands in shared memory), a tile ahead.
 //   1       issues O += P V (128 x D x 128, P in tensor memory).
-//   4 - 7   one row a thread: the row's maximum, weights 2^(t - m + 10) as fp16 into the tensor memory that
+//   4 - 11  one row a thread, even and odd items apart, so that one's end is under the other's tiles: the maximum, weights 2^(t - m + 10) as fp16 into the tensor memory that
 //           S had, their sum. m only has to be near the maximum: O is rescaled when a score passes m by 2^5.
-//   2, 3, 16, 17  rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory;
-//           finished rows out of the same buffer.
+//   2, 3, 20, 21  rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory.
 // All waits are bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT and ends the CTA's
 // loops, its MMAs land, and tensor memory is freed.
 #include "attend_convert.cuh"
@@ -30,11 +29,12 @@ namespace {
 
 constexpr int kTile = 128;                     // tokens
 constexpr int kMB = 128;                       // rows of a block
-constexpr int kThreads = 576;
-constexpr int kWarpS = 0, kWarpPv = 1, kWarpSoft = 4, kWarpConv = 8;
-constexpr int kQWarps = 4;   // warps 2, 3, 16, 17
+constexpr int kThreads = 704;
+constexpr int kWarpS = 0, kWarpPv = 1, kWarpSoft = 4, kWarpConv = 12, kWarpQ2 = 20;
+constexpr int kQWarps = 4;   // warps 2, 3 and kWarpQ2 on
 constexpr unsigned long long kDrainNs = 4000000000ull;
-constexpr uint32_t kTmemCols = 512, kTmemO = 256;   // S of even tiles at 0, of odd tiles at 128, O at 256
+// S of even tiles at 0, of odd tiles at 128; O of even items at 256, of odd items at 384
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 // instruction descriptors, kind::f16: D fp32, A and B fp16, both K-major, M = 128
 constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kMB >> 4) << 24);
 template <int D>
@@ -184,25 +184,19 @@ struct Walk {
 
 // ------------------------------------------------------------------ waits
 
-// a try that may sleep some microseconds in the hardware, so that waiting warps leave the issue slots alone
-__device__ __forceinline__ bool try_wait_sleep(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-}
-
+// Waiting warps share the issue slots with the working ones, so a try costs little: the timer and the abort
+// flag are looked at every 16 tries only, and warps that have time (kEasy) sleep between tries.
+template <bool kEasy>
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                        unsigned long long limit_ns)
 {
     const unsigned long long t0 = globaltimer();
-    while (!try_wait_sleep(bar, parity)) {
+    while (true) {
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (kEasy) __nanosleep(100);
+        }
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
@@ -210,7 +204,6 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
             return false;
         }
     }
-    return true;
 }
 
 // Warp-wide: true where every lane saw the phase end.
@@ -220,7 +213,12 @@ struct Waits {
     unsigned long long limit_ns;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
-        const bool ok = mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
+        const bool ok = mbar_try_wait(bar, parity) || wait_slow<false>(bar, parity, abort, status, limit_ns);
+        return __all_sync(0xffffffffu, ok);
+    }
+    __device__ __forceinline__ bool easy(uint32_t bar, uint32_t parity) const
+    {
+        const bool ok = mbar_try_wait(bar, parity) || wait_slow<true>(bar, parity, abort, status, limit_ns);
         return __all_sync(0xffffffffu, ok);
     }
 };
@@ -272,14 +270,14 @@ __device__ __forceinline__ uint4 load_halves(const __nv_bfloat16* src)
 // phase needs an arrival that the waiter, or one that waits for it, makes after it saw the phase before.
 enum Bar {
     kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8,
-    kStaged = 10,   // an item's rows are in q's buffer, or written elsewhere
+    kFree = 10,     // an item's products are done and its rows are out of q's buffer
     kSFull = 12, kPFull = 14,
     kPvDone = 16,   // O += P V of a tile has landed
-    kODone = 18,    // that of an item's last tile in this run
-    kOFree = 19,    // the item's rows are out of O
-    kFin = 20,
-    kCopied = 22,   // the q warps have written out their parts of the staged rows
-    kBars = 24
+    kODone = 18,    // that of an item's last tile in this run; by the item's parity, as the next three
+    kOFree = 20,    // the item's rows are out of O
+    kBegun = 22,    // the item's first S is issued
+    kFin = 24,
+    kBars = 26
 };
 
 // The codes of a tile that one converting thread takes: 64 (32 for D = 64) channels of one key, and 8 tokens
@@ -309,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_scan[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ AttendTodo s_todo[2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar0 = smem_addr(s_bar);
@@ -320,15 +319,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kKEmpty + b), 1);
             mbar_init(bar(kVEmpty + b), 1);
             mbar_init(bar(kQFull + b), kQWarps);
-            mbar_init(bar(kStaged + b), 4);
+            mbar_init(bar(kFree + b), 4);
             mbar_init(bar(kSFull + b), 2);    // its MMAs, and the issuing thread for what it saw (s_valid)
             mbar_init(bar(kPFull + b), 4);
             mbar_init(bar(kPvDone + b), 1);
             mbar_init(bar(kFin + b), 1);
-            mbar_init(bar(kCopied + b), kQWarps);
+            mbar_init(bar(kODone + b), 1);
+            mbar_init(bar(kOFree + b), 4);
+            mbar_init(bar(kBegun + b), 1);
         }
-        mbar_init(bar(kODone), 1);
-        mbar_init(bar(kOFree), 4);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -374,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc5::commit_warp(bar(kSFull + b));
                 tc5::commit_warp(bar(kKEmpty + b));
-                if (lane == 0) mbar_arrive(bar(kSFull + b));
+                if (lane == 0) {
+                    mbar_arrive(bar(kSFull + b));
+                    if (u == 0) mbar_arrive(bar(kBegun + (item & 1)));
+                }
                 __syncwarp();
             }
             at += tiles;
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < tiles && ok; ++u, ++n) {
                 const int b = n & 1;
                 if (!wait(bar(kVFull + b), (n >> 1) & 1u) || !wait(bar(kPFull + b), (n >> 1) & 1u)) ok = false;
-                if (ok && u == 0 && item > 0 && !wait(bar(kOFree), (item - 1) & 1u)) ok = false;
+                if (ok && u == 0 && item >= 2 && !wait(bar(kOFree + (item & 1)), ((item >> 1) - 1) & 1u)) ok = false;
                 if (!ok) break;
                 tc5::fence_after();
                 uint32_t pt = tmem + b * 128, acc = u > 0;
@@ -405,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kTile / 64; ++c) {
                     uint64_t d = vd + c * (D * 128 / 16);
 #pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk, d += 2, pt += 8, acc = 1) tc5::mma_ts_warp(tmem + kTmemO, pt, d, kIdescO<D>, acc);
+                    for (int kk = 0; kk < 4; ++kk, d += 2, pt += 8, acc = 1) tc5::mma_ts_warp(tmem + kTmemO + (item & 1) * 128, pt, d, kIdescO<D>, acc);
                 }
                 tc5::commit_warp(bar(kPvDone + b));
                 tc5::commit_warp(bar(kVEmpty + b));
-                if (u + 1 == tiles) tc5::commit_warp(bar(kODone));
+                if (u + 1 == tiles) tc5::commit_warp(bar(kODone + (item & 1)));
             }
             at += tiles;
             if (at < end) w.advance(p, s_pre);
@@ -417,55 +419,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc5::commit_warp(bar(kFin + 1));
         drain(bar(kFin + 1), 0u);
         __syncwarp();
-    } else if (begin < end && (warp == 2 || warp == 3 || warp >= 16)) {
-        // ---------------- rows of q, one item ahead; finished rows out of the buffer before it is filled again
+    } else if (begin < end && (warp == 2 || warp == 3 || warp >= kWarpQ2)) {
+        // ---------------- rows of q, one item ahead
         Walk w;
         w.start(p, s_pre, begin);
         const float to_log2 = p.scale * kLog2e;
         constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // a row of D channels is D / 8 lanes
-        constexpr int kFlight = 4;                           // loads in flight
-        const int c = lane % kLanes, sub = (warp < 4 ? warp - 2 : warp - 14) * kRows + lane / kLanes;
-        Walk prev[2];            // the items whose rows the two buffers hold
-        bool whole[2] = {false, false};
-        auto put = [&](int b, uint32_t item) {   // the staged rows of item `item` out of buffer b
-            if (!wait(bar(kStaged + b), (item >> 1) & 1u)) return false;
-            if (whole[b]) {
-                const Walk& x = prev[b];
-                const RowMap map(x.b * kMB, p.G, p.g_magic);
-                const int left = min(kMB, x.q.n_rows - x.b * kMB);
-                __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(p.out) + ((size_t)x.q.first * p.Hq + x.h * p.G) * D + c * 8;
-                const uint32_t stage = q_buf + b * kOperand;
-#pragma unroll 4
-                for (int row = sub; row < left; row += kQWarps * kRows) {
-                    int j, g;
-                    map.at(row, j, g);
-                    *reinterpret_cast<uint4*>(o0 + ((size_t)j * p.Hq + g) * D) = load16(stage + row * (D * 2) + ((c ^ (row & 7)) * 16));
-                }
-            }
-            __syncwarp();
-            return true;
-        };
+        constexpr int kFlight = 8;                           // loads in flight
+        const int c = lane % kLanes, sub = (warp < 4 ? warp - 2 : warp - kWarpQ2 + 2) * kRows + lane / kLanes;
         bool ok = true;
-        int item = 0;
-        for (int at = begin; at < end && ok; ++item) {
+        for (int at = begin, item = 0; at < end && ok; ++item) {
             const int tiles = min(w.t.tiles - w.u, end - at), b = item & 1;
-            if (item >= 2) {
-                // the item two before: its products are done when its rows are staged; and all four warps have
-                // read what any of them fills next
-                ok = put(b, item - 2);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive(bar(kCopied + b));
-                ok = wait(bar(kCopied + b), ((item >> 1) - 1) & 1u);
-                if (!ok) break;
-            }
-            prev[b] = w;
-            whole[b] = w.u == 0 && tiles == w.t.tiles;
             const RowMap map(w.b * kMB, p.G, p.g_magic);
             const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)w.q.first * p.q_ts +
                                       (int64_t)w.h * p.G * p.q_hs + c * 8;
             const int left = min(kMB, w.q.n_rows - w.b * kMB);
 #pragma unroll 1
-            for (int r = sub; r < kMB; r += kFlight * kQWarps * kRows) {
+            for (int r = sub; r < kMB && ok; r += kFlight * kQWarps * kRows) {
                 uint4 v[kFlight];
                 if (p.q_aligned) {   // one test for all: a test each would make the loads wait for one another
 #pragma unroll
@@ -487,23 +457,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (k == e) v[k] = y;
                     }
                 }
+                // the buffer is free when the rows of the item two before are out of it; the first loads are under way
+                if (r == sub && item >= 2) ok = wait.easy(bar(kFree + b), ((item >> 1) - 1) & 1u);
+                if (!ok) break;
+                // magnitudes of bf16 order like their bits, two at a time; the rows' shuffles side by side
+                uint32_t two[kFlight];
+#pragma unroll
+                for (int e = 0; e < kFlight; ++e)
+                    two[e] = __vmaxu2(__vmaxu2(v[e].x & 0x7FFF7FFFu, v[e].y & 0x7FFF7FFFu),
+                                      __vmaxu2(v[e].z & 0x7FFF7FFFu, v[e].w & 0x7FFF7FFFu));
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int e = 0; e < kFlight; ++e) two[e] = __vmaxu2(two[e], __shfl_xor_sync(0xffffffffu, two[e], o));
 #pragma unroll
                 for (int e = 0; e < kFlight; ++e) {
                     const int row = r + e * kQWarps * kRows;
                     const uint32_t x[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-                    // magnitudes of bf16 order like their bits, two at a time
-                    uint32_t two = x[0] & 0x7FFF7FFFu;
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) two = __vmaxu2(two, x[k] & 0x7FFF7FFFu);
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
-                    const uint32_t top = max(two & 0xFFFFu, two >> 16);
+                    const uint32_t top = max(two[e] & 0xFFFFu, two[e] >> 16);
                     const bool bad = top >= 0x7F80u;   // an infinity or NaN
-                    if (bad && row < left && c == 0) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
                     const float up = row_up((int)(top >> 7));
-                    // a row that is not finite has the factor NaN and so weights, sum and result; rows past the
-                    // request's repeat its last one and are not written
-                    if (c == 0) s_fac[b][row] = bad ? NAN : row_factor(to_log2, up);
+                    if (c == 0) {
+                        if (bad && row < left) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
+                        // a row that is not finite has the factor NaN and so weights, sum and result; rows past
+                        // the request's repeat its last one and are not written
+                        s_fac[b][row] = bad ? NAN : row_factor(to_log2, up);
+                    }
                     float f[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -515,13 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pack(f[1], f[5]), pack(f[2], f[6]), pack(f[3], f[7]));
                 }
             }
+            if (!ok) break;
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kQFull + b));
             at += tiles;
             if (at < end) w.advance(p, s_pre);
         }
-        for (int x = max(0, item - 2); x < item && ok; ++x) ok = put(x & 1, x);
     } else if (begin < end && warp >= kWarpConv) {
         // ---------------- codes to fp16
         const int cw = warp - kWarpConv;
@@ -659,8 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (begin < end && warp >= kWarpSoft) {
         // ---------------- weights: one row a thread
-        const int row = tid - kWarpSoft * 32;
-        const uint32_t lanes = tmem + ((uint32_t)((warp - kWarpSoft) * 32) << 16);
+        const int grp = (warp - kWarpSoft) >> 2, quarter = (warp - kWarpSoft) & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), o_at = lanes + kTmemO + grp * 128;
         Walk w;
         w.start(p, s_pre, begin);
         bool ok = true;
@@ -668,8 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int at = begin, item = 0; at < end; ++item) {
             const int u0 = w.u, u1 = min(w.t.tiles, u0 + (end - at));
             const int row0 = w.b * kMB, rr = row0 + row;
-            const bool any = row0 + (warp - kWarpSoft) * 32 < w.q.n_rows;   // the warp has rows of the item
-            ok = wait(bar(kQFull + (item & 1)), (item >> 1) & 1u);
+            if ((item & 1) != grp) {   // the other group's
+                n += u1 - u0;
+                at += u1 - u0;
+                if (at < end) w.advance(p, s_pre);
+                continue;
+            }
+            const bool any = row0 + quarter * 32 < w.q.n_rows;   // the warp has rows of the item
+            // the factors are there; and with the item's first S issued the barriers of S are at its tiles
+            ok = wait.easy(bar(kQFull + grp), (item >> 1) & 1u) && wait(bar(kBegun + grp), (item >> 1) & 1u);
             if (!ok) break;
             const float fac = s_fac[item & 1][row];
             const uint64_t fac2 = pack2(fac, fac);
@@ -731,10 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t y[16];
-                            tc5::ld16(lanes + kTmemO + c * 16, y);
+                            tc5::ld16(o_at + c * 16, y);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * keep);
-                            tc5::st16(lanes + kTmemO + c * 16, y);
+                            tc5::st16(o_at + c * 16, y);
                         }
                     }
                     const float base = top == -INFINITY ? 0.f : kShift - top;
@@ -767,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- the item's end in this run
             const bool whole = u0 == 0 && u1 == w.t.tiles;
             const int slot = at == begin ? 0 : 1;   // a run's first item, or its last
-            // warps without rows wait too: their arrival below must not count for the item before
-            ok = wait(bar(kODone), item & 1u);
+            // warps without rows wait too: their arrivals below must not count for the item before
+            ok = wait(bar(kODone + grp), (item >> 1) & 1u);
             if (!ok) break;
             if (any) {
                 tc5::fence_after();
@@ -776,12 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 if (whole) {
                     // rows as bf16 into q's buffer, whose products are done, each row's 16-byte units turned by
-                    // the row; the q warps write them out
-                    const uint32_t stage = q_buf + (item & 1) * kOperand + (uint32_t)(warp - kWarpSoft) * 32 * (D * 2);
+                    // the row, and out from there in whole pieces
+                    const uint32_t stage = q_buf + grp * kOperand + (uint32_t)quarter * 32 * (D * 2);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t x[32];
-                        tc5::ld32(lanes + kTmemO + c * 32, x);
+                        tc5::ld32(o_at + c * 32, x);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t y[4];
@@ -796,7 +783,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc5::fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kOFree));
+                    if (lane == 0) mbar_arrive(bar(kOFree + grp));
+                    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+                    const RowMap map(row0, p.G, p.g_magic);
+                    const int c = lane % kLanes, left = min(32, w.q.n_rows - row0 - quarter * 32);
+                    __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(p.out) + ((size_t)w.q.first * p.Hq + w.h * p.G) * D + c * 8;
+#pragma unroll 4
+                    for (int r = lane / kLanes; r < left; r += kRows) {
+                        int j, g;
+                        map.at(quarter * 32 + r, j, g);
+                        *reinterpret_cast<uint4*>(o0 + ((size_t)j * p.Hq + g) * D) = load16(stage + r * (D * 2) + ((c ^ (r & 7)) * 16));
+                    }
                     if (real && p.lse) {
                         p.lse[(size_t)(w.q.first + rr / p.G) * p.Hq + w.h * p.G + rr % p.G] =
                             sum == 0.f ? -INFINITY : (top + log2f(sum) - kShift) * kLn2;
@@ -807,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t x[32];
-                        tc5::ld32(lanes + kTmemO + c * 32, x);
+                        tc5::ld32(o_at + c * 32, x);
                         if (real) {
                             uint4* o = reinterpret_cast<uint4*>(ws.rows + part * D + c * 32);
 #pragma unroll
@@ -818,12 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (real) ws.ml[part] = make_float2(top, sum);
                     tc5::fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kOFree));
+                    if (lane == 0) mbar_arrive(bar(kOFree + grp));
                 }
             } else if (lane == 0) {
-                mbar_arrive(bar(kOFree));
+                mbar_arrive(bar(kOFree + grp));
             }
-            if (lane == 0) mbar_arrive(bar(kStaged + (item & 1)));
+            if (lane == 0) mbar_arrive(bar(kFree + grp));
             // an item that starts here and goes on: the next kernel joins its parts
             if (u0 == 0 && u1 < w.t.tiles) {
                 todo.parts = (at + w.t.tiles - 1) / per - (int)blockIdx.x + 1;
@@ -838,9 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) todo.parts = 0;
     }
-    if (tid == kWarpSoft * 32) ws.todo[blockIdx.x] = todo;
+    if (warp == kWarpSoft || warp == kWarpSoft + 4) {
+        // the group that had the run's last item has the note
+        if (lane == 0) s_todo[(warp - kWarpSoft) >> 2] = todo;
+    }
     tc5::fence_before();
     __syncthreads();
+    if (tid == 0) ws.todo[blockIdx.x] = s_abort ? AttendTodo{} : s_todo[s_todo[1].parts > 0];
     if (warp == kWarpPv) {
         tc5::fence_after();
         tc5::dealloc(tmem, kTmemCols);
