@@ -11,11 +11,21 @@
 //           A thread takes 8 tokens of 8 value channels, so the transposition is its choice of registers.
 //   0       issues S = Q K^T (128 x 128 x D, operands in shared memory), a tile ahead.
 //   1       issues O += P V (128 x D x 128, P in tensor memory).
-//   4 - 11  one row a thread, even and odd items apart, so that one's end is under the other's tiles: the maximum, weights 2^(t - m + 10) as fp16 into the tensor memory that
-//           S had, their sum. m only has to be near the maximum: O is rescaled when a score passes m by 2^5.
+//   4 - 11  one row a thread, even and odd items apart, so that one's end is under the other's tiles: the maximum,
+//           weights 2^(t - m + 10) as fp16 into the tensor memory that S had, their sum. m only has to be near the
+//           maximum: O is rescaled when a score passes m by 2^5.
 //   2, 3, 20, 21  rows of q of the next item, scaled by a power of two into fp16's range, exactly, into shared memory.
 // All waits are bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT and ends the CTA's
 // loops, its MMAs land, and tensor memory is freed.
+//
+// Bound: prompts need 4 D flops for each row and key, 0.11 ms at the tensor cores' rate for 2 x 2048 rows of 32 heads
+// after up to 4096 tokens, and take 0.22 ms; few rows need the cache's bytes once, 0.053 ms for 128 requests of up to
+// 4096 tokens, and take 0.28 ms. What both wait for is the turning of codes into operands: a tile takes 3600 cycles of
+// the SM for 7500 warp instructions of all roles, half of its issue slots, and as long for 20 rows as for 128. Without
+// the conversion 193 us of 218 are left of the prompts, without conversion, weights and products 116 of 276 us of the
+// 17-row batch. Tried and slower: sixteen converting warps (64 registers a thread), weights formed in one pass
+// from scores kept apart from them, two threads a row; a warp that prefetches codes into the L2 cache gained 4% on few
+// rows and lost 2% on prompts.
 #include "attend_convert.cuh"
 #include "attend_plan.cuh"
 #include "cache.cuh"
@@ -184,19 +194,29 @@ struct Walk {
 
 // ------------------------------------------------------------------ waits
 
-// Waiting warps share the issue slots with the working ones, so a try costs little: the timer and the abort
-// flag are looked at every 16 tries only, and warps that have time (kEasy) sleep between tries.
-template <bool kEasy>
+// A waiting warp is suspended by its try for up to kNap, or the limit if that is less, and then looks at the timer
+// and the abort flag.
+constexpr uint32_t kNapNs = 100000;
+
+__device__ __forceinline__ bool try_for(uint32_t bar, uint32_t parity, uint32_t ns)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                        unsigned long long limit_ns)
 {
     const unsigned long long t0 = globaltimer();
-    while (true) {
-#pragma unroll 1
-        for (int k = 0; k < 16; ++k) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if (kEasy) __nanosleep(100);
-        }
+    const uint32_t nap = limit_ns < kNapNs ? (uint32_t)limit_ns : kNapNs;
+    while (!try_for(bar, parity, nap)) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
@@ -204,6 +224,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
             return false;
         }
     }
+    return true;
 }
 
 // Warp-wide: true where every lane saw the phase end.
@@ -213,12 +234,7 @@ struct Waits {
     unsigned long long limit_ns;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
-        const bool ok = mbar_try_wait(bar, parity) || wait_slow<false>(bar, parity, abort, status, limit_ns);
-        return __all_sync(0xffffffffu, ok);
-    }
-    __device__ __forceinline__ bool easy(uint32_t bar, uint32_t parity) const
-    {
-        const bool ok = mbar_try_wait(bar, parity) || wait_slow<true>(bar, parity, abort, status, limit_ns);
+        const bool ok = mbar_test_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
         return __all_sync(0xffffffffu, ok);
     }
 };
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // the buffer is free when the rows of the item two before are out of it; the first loads are under way
-                if (r == sub && item >= 2) ok = wait.easy(bar(kFree + b), ((item >> 1) - 1) & 1u);
+                if (r == sub && item >= 2) ok = wait(bar(kFree + b), ((item >> 1) - 1) & 1u);
                 if (!ok) break;
                 // magnitudes of bf16 order like their bits, two at a time; the rows' shuffles side by side
                 uint32_t two[kFlight];
@@ -656,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool any = row0 + quarter * 32 < w.q.n_rows;   // the warp has rows of the item
             // the factors are there; and with the item's first S issued the barriers of S are at its tiles
-            ok = wait.easy(bar(kQFull + grp), (item >> 1) & 1u) && wait(bar(kBegun + grp), (item >> 1) & 1u);
+            ok = wait(bar(kQFull + grp), (item >> 1) & 1u) && wait(bar(kBegun + grp), (item >> 1) & 1u);
             if (!ok) break;
             const float fac = s_fac[item & 1][row];
             const uint64_t fac2 = pack2(fac, fac);
@@ -866,8 +882,12 @@ cudaError_t launch_tc(const AttendParams& p, const AttendScratch& ws, cudaStream
 bool attend_tc_supported(const AttendParams& p)
 {
     if (p.dtype != DSPARK_BF16 || (p.c.D != 64 && p.c.D != 128)) return false;
+    // A tile costs the same here for 1 row and for 128; the warp kernel's grows with its blocks of 16. 128 requests of
+    // up to 4096 tokens, 4 query heads a key head: 36 rows 278 us here and 215 there, 48 rows 274 and 251, 64 rows 277
+    // and 299, 128 rows 294 and 494. 32 requests of 2048: 48 rows 60 and 58, 64 rows 63 and 67. A window of 512 keys:
+    // 48 rows 71 and 63, 68 rows 76 and 70, 128 rows 82 and 108.
     const long long rows = (long long)p.max_q * p.G;
-    if (rows <= 16 || rows >= (1ll << 30)) return false;
+    if (rows <= 48 || rows >= (1ll << 30)) return false;
     if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - 2048) return false;
     // tiles are counted in 32 bits
     const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
