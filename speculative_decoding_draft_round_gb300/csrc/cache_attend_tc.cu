@@ -6,9 +6,9 @@
 // An item is 128 rows (query heads of consecutive queries) of one request and key / value head, a tile 128
 // tokens. The items' tiles form one line that is cut into equal runs, one a CTA and SM, whatever the lengths
 // are; a block's tiles are those its own rows reach. Per tile, by warp:
-//   12 - 19 turn codes into fp16 (exact: scales have 8 bits) in shared memory: K by token, V transposed
-//           by channel, both K-major with the 128-byte swizzle; the next tile's codes are loaded before.
-//           A thread takes 8 tokens of 8 value channels, so the transposition is its choice of registers.
+//   12 - 19 turn codes into fp16 (exact: scales have 8 bits) in shared memory, 16 bytes of them at a time, as they lie
+//           in the cache: rows of tokens with the 128-byte swizzle, K-major for the keys and not for the values. The
+//           next tile's codes are loaded before.
 //   0       issues S = Q K^T (128 x 128 x D, operands in shared memory), a tile ahead.
 //   1       issues O += P V (128 x D x 128, P in tensor memory).
 //   4 - 11  one row a thread, even and odd items apart, so that one's end is under the other's tiles: the maximum,
@@ -39,16 +39,18 @@ namespace {
 
 constexpr int kTile = 128;                     // tokens
 constexpr int kMB = 128;                       // rows of a block
-constexpr int kThreads = 704;
-constexpr int kWarpS = 0, kWarpPv = 1, kWarpSoft = 4, kWarpConv = 12, kWarpQ2 = 20;
+constexpr int kThreads = 736;
+constexpr int kWarpS = 0, kWarpPv = 1, kWarpSoft = 4, kWarpConv = 12, kWarpQ2 = 20, kWarpAhead = 22;
+constexpr int kAhead = 4;    // tiles whose codes are under way
 constexpr int kQWarps = 4;   // warps 2, 3 and kWarpQ2 on
 constexpr unsigned long long kDrainNs = 4000000000ull;
 // S of even tiles at 0, of odd tiles at 128; O of even items at 256, of odd items at 384
+// (O's columns in the order of converted codes: channels 0 4 1 5 2 6 3 7 of every 8)
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
-// instruction descriptors, kind::f16: D fp32, A and B fp16, both K-major, M = 128
+// instruction descriptors, kind::f16: D fp32, A and B fp16, M = 128; K-major but for V, whose channels are contiguous
 constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kMB >> 4) << 24);
 template <int D>
-constexpr uint32_t kIdescO = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kMB >> 4) << 24);
+constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kMB >> 4) << 24);
 
 // ------------------------------------------------------------------ the line of tiles
 
@@ -258,6 +260,8 @@ __device__ __forceinline__ uint4 load16(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Query and head in the group of the rows of a block. The quotients by G of numbers below 2048 come by a
 // multiplication: g_magic = ceil(2^32 / G), off by less than G <= 1024, is exact there.
 struct RowMap {
@@ -293,18 +297,22 @@ enum Bar {
     kOFree = 20,    // the item's rows are out of O
     kBegun = 22,    // the item's first S is issued
     kFin = 24,
-    kBars = 26
+    kRun = 26,      // where a tile's codes are is in s_run
+    kBars = 34
 };
 
-// The codes of a tile that one converting thread takes: 64 (32 for D = 64) channels of one key, and 8 tokens
-// of 8 value channels.
+// Where 16 tokens of a tile lie: their first key's codes, from there on to its scale, and how many hold something.
+struct Run {
+    const uint8_t* codes;
+    int scales, left;
+};
+
+// The codes of a tile that one converting thread takes, of keys and of values: 32 channels of one token for every
+// 64 channels of a head, with their scales.
 template <int D>
 struct Raw {
-    uint32_t k[D / 16];
-    uint32_t ks;      // the scales of its one or two groups
-    uint32_t v[8];
-    uint4 vs;         // of the 8 tokens
-    bool valid;       // the value tokens' page is there
+    uint4 k[D / 64], v[D / 64];
+    uint16_t ks[D / 64], vs[D / 64];
 };
 
 template <int D>
@@ -312,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_attend_tc_kernel(AttendParams p, AttendScratch ws, unsigned long long wait_ns)
 {
     constexpr uint32_t kOperand = 128 * D * 2;   // bytes of Q, K or V of a tile
-    constexpr int kVWarps = D == 128 ? 8 : 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t q_buf = smem_addr(smem), k_buf = q_buf + 2 * kOperand, v_buf = q_buf + 4 * kOperand;
@@ -323,6 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_scan[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ __align__(16) Run s_run[8][8];       // of tile n & 7, by converting warp
+    __shared__ int s_done;                           // tiles whose keys the first converting warp is through with
     __shared__ AttendTodo s_todo[2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(kKFull + b), 8);
-            mbar_init(bar(kVFull + b), kVWarps);
+            mbar_init(bar(kVFull + b), 8);
             mbar_init(bar(kKEmpty + b), 1);
             mbar_init(bar(kVEmpty + b), 1);
             mbar_init(bar(kQFull + b), kQWarps);
@@ -345,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kBegun + b), 1);
         }
         s_abort = 0;
+        s_done = 0;
+        for (int b = 0; b < 8; ++b) mbar_init(bar(kRun + b), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
@@ -380,13 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc5::fence_after();
                 // the start address of a descriptor counts 16 bytes: 16 K elements on are 2
                 const uint64_t qd = q_desc + (uint64_t)((item & 1) * (kOperand >> 4)), kd = k_desc + (uint64_t)(b * (kOperand >> 4));
-                uint32_t acc = 0;
-#pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    uint64_t off = c * (16384 / 16);
-#pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk, off += 2, acc = 1) tc5::mma_ss_warp(tmem + b * 128, qd + off, kd + off, kIdescS, acc);
-                }
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tc5::mma_ss4_warp<2, 2>(tmem + b * 128, qd + c * (16384 / 16), kd + c * (16384 / 16), kIdescS, c);
                 tc5::commit_warp(bar(kSFull + b));
                 tc5::commit_warp(bar(kKEmpty + b));
                 if (lane == 0) {
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- O (+)= P V
         Walk w;
         w.start(p, s_pre, begin);
-        const uint64_t v_desc = tc5::desc_sw128(v_buf);
+        const uint64_t v_desc = tc5::desc_sw128_mn(v_buf, 16384);
         bool ok = true;
         int n = 0;
         for (int at = begin, item = 0; at < end && ok; ++item) {
@@ -417,14 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && u == 0 && item >= 2 && !wait(bar(kOFree + (item & 1)), ((item >> 1) - 1) & 1u)) ok = false;
                 if (!ok) break;
                 tc5::fence_after();
-                uint32_t pt = tmem + b * 128, acc = u > 0;
-                const uint64_t vd = v_desc + (uint64_t)(b * (kOperand >> 4));
-#pragma unroll 1
-                for (int c = 0; c < kTile / 64; ++c) {
-                    uint64_t d = vd + c * (D * 128 / 16);
-#pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk, d += 2, pt += 8, acc = 1) tc5::mma_ts_warp(tmem + kTmemO + (item & 1) * 128, pt, d, kIdescO<D>, acc);
-                }
+                const uint64_t vd = v_desc + (uint64_t)(b * (kOperand >> 4));   // 16 tokens on are 16 rows of 128 bytes
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    tc5::mma_ts4_warp<2048 / 16>(tmem + kTmemO + (item & 1) * 128, tmem + b * 128 + c * 32,
+                                                 vd + c * (8192 / 16), kIdescO<D>, c > 0 || u > 0);
                 tc5::commit_warp(bar(kPvDone + b));
                 tc5::commit_warp(bar(kVEmpty + b));
                 if (u + 1 == tiles) tc5::commit_warp(bar(kODone + (item & 1)));
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc5::commit_warp(bar(kFin + 1));
         drain(bar(kFin + 1), 0u);
         __syncwarp();
-    } else if (begin < end && (warp == 2 || warp == 3 || warp >= kWarpQ2)) {
+    } else if (begin < end && (warp == 2 || warp == 3 || warp == kWarpQ2 || warp == kWarpQ2 + 1)) {
         // ---------------- rows of q, one item ahead
         Walk w;
         w.start(p, s_pre, begin);
@@ -517,140 +521,147 @@ __global__ void __launch_bounds__(kThreads, 1)
             at += tiles;
             if (at < end) w.advance(p, s_pre);
         }
-    } else if (begin < end && warp >= kWarpConv) {
-        // ---------------- codes to fp16
-        const int cw = warp - kWarpConv;
-        const int k_tok = (cw & 3) * 32 + lane, k_half = cw >> 2;
-        const bool has_v = cw < kVWarps;
-        const int v_tg = (D == 128 ? cw >> 2 : (cw >> 1) & 1) * 8 + (lane & 7);     // 8 tokens
-        const int v_word = (D == 128 ? cw & 3 : cw & 1) * 4 + (lane >> 3);          // 8 channels
-        const CacheBlock cb = cache_block(p.c.page_size, D);
-        const DequantConst dq = dequant_const();
+    } else if (begin < end && warp == kWarpAhead) {
+        // ---------------- where the codes of the tiles to come are, and they themselves into the L2 cache: what the
+        // converting warps have under way, 18 KB an SM, the memory's latency alone would keep below 2.5 TB/s
         Walk w;
         w.start(p, s_pre, begin);
-        const int magic = p.page_magic, P = p.c.page_size;
-        // What a tile's loads need, found a conversion before them: its first key, its head, the keys there are
-        // and the pages of this thread's tokens.
-        struct Place {
-            int key0, h, keys, k_page, v_page;
+        const CacheBlock cb = cache_block(p.c.page_size, D);
+        const volatile int* done = &s_done;
+        const int slice = lane >> 2, sub = lane & 3;   // 16 tokens, and part of their lines
+        const unsigned long long t0 = globaltimer();
+        const int tiles = end - begin, magic = p.page_magic, P = p.c.page_size;
+        BlockTiles it = w.t;   // in registers: the walk's memory is swept out of the L1 cache by the codes
+        int u = w.u, keys = w.q.keys, h = w.h, key, page;
+        const int32_t* row = p.c.table + (size_t)w.r * p.c.table_width;
+        auto look_up = [&]() {
+            key = it.key0(u) + slice * 16;
+            page = key < keys ? row[page_of(key, magic)] : -1;
         };
-        auto find = [&](int u) {
-            Place x;
-            x.key0 = w.t.key0(u);
-            x.h = w.h;
-            x.keys = w.q.keys;
-            const int32_t* row = p.c.table + (size_t)w.r * p.c.table_width;
-            const int kk = x.key0 + k_tok, vk = x.key0 + v_tg * 8;
-            x.k_page = kk < x.keys ? row[page_of(kk, magic)] : -1;
-            x.v_page = vk < x.keys ? row[page_of(vk, magic)] : -1;
-            return x;
-        };
-        Raw<D> x = {};
-        auto load_k = [&](const Place& a) {
-            const int kk = a.key0 + k_tok;
-            const bool in = kk < a.keys && a.k_page >= 0 && a.k_page < p.c.n_pages;
-            if (kk < a.keys && !in) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
-            x.ks = 0;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) x.k[c] = 0;
-            if (in) {
-                const uint8_t* blk = cache_page_block(p.c, a.k_page, a.h, cb.bytes);
-                const int slot = kk - page_of(kk, magic) * P;
-                const uint4* src = reinterpret_cast<const uint4*>(blk + slot * (D / 2) + k_half * (D / 4));
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint4 y = src[c];
-                    x.k[4 * c] = y.x;
-                    x.k[4 * c + 1] = y.y;
-                    x.k[4 * c + 2] = y.z;
-                    x.k[4 * c + 3] = y.w;
-                }
-                const uint8_t* sc = blk + cb.k_scales + slot * (D / 16);
-                if (D == 128) x.ks = *reinterpret_cast<const uint32_t*>(sc + k_half * 4);
-                else x.ks = *reinterpret_cast<const uint16_t*>(sc + k_half * 2);
-            }
-        };
-        auto load_v = [&](const Place& a) {
-            const int vk = a.key0 + v_tg * 8;
-            const bool in = vk < a.keys && a.v_page >= 0 && a.v_page < p.c.n_pages;
-            x.valid = in;
-            x.vs = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x.v[c] = 0;
-            if (in && has_v) {
-                const uint8_t* blk = cache_page_block(p.c, a.v_page, a.h, cb.bytes);
-                const int slot = vk - page_of(vk, magic) * P;
-                const uint8_t* src = blk + cb.v_codes + slot * (D / 2) + v_word * 4;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) x.v[c] = *reinterpret_cast<const uint32_t*>(src + c * (D / 2));
-                x.vs = *reinterpret_cast<const uint4*>(blk + cb.v_scales + v_scale_at(slot, v_word / 4, D / kCacheGroup));
-                // what no token wrote may be anything: its scale becomes 0
-                const int left = a.keys - vk;
-                if (left < 8) {
-                    x.vs.x &= keep_halves(left);
-                    x.vs.y &= keep_halves(left - 2);
-                    x.vs.z &= keep_halves(left - 4);
-                    x.vs.w &= keep_halves(left - 6);
-                }
-            }
-        };
-        const int tiles = end - begin;
-        int u = w.u;
-        Place place = find(u);
-        load_k(place);
-        load_v(place);
+        look_up();
 #pragma unroll 1
         for (int n = 0; n < tiles; ++n) {
-            // The registers that a conversion frees take the next tile's codes at once: their way is as long as
-            // the other conversion and the waits. (A second set that is copied at the loop's end stops there for
-            // the loads instead.)
-            const int b = n & 1;
-            const bool more = n + 1 < tiles, valid = x.valid;
-            if (more) {
-                if (++u == w.t.tiles) {
+            // An entry is free when tile n - 8 is: the first warp is past the keys of tile n - 5, the others past those
+            // of tile n - 7, or it would have waited for them.
+            bool ok = true;
+            while (ok && n - *done > kAhead) {
+                if (*wait.abort || globaltimer() - t0 > 4 * wait_ns) ok = false;
+                __nanosleep(100);
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+            __threadfence_block();
+            const int left = keys - key, slot = key - page_of(key, magic) * P;
+            const bool in = page >= 0 && page < p.c.n_pages;
+            if (left > 0 && !in && sub == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+            const uint8_t* blk = cache_page_block(p.c, in ? page : 0, h, cb.bytes);
+            if (sub == 0)
+                s_run[n & 7][slice] = Run{blk + slot * (D / 2), (int)cb.k_scales + slot * (D / 16) - slot * (D / 2), in ? left : 0};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kRun + (n & 7)));
+            if (in) {
+                const uint8_t* k = blk + slot * (D / 2) + sub * 128;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    prefetch_l2(k + c * 512);
+                    prefetch_l2(k + cb.v_codes + c * 512);
+                }
+                if (sub < 2) prefetch_l2(blk + (sub ? cb.v_scales : cb.k_scales) + slot * (D / 16));
+            }
+            if (n + 1 < tiles) {
+                if (++u == it.tiles) {
                     w.advance(p, s_pre);
                     u = 0;
+                    it = w.t;
+                    keys = w.q.keys;
+                    h = w.h;
+                    row = p.c.table + (size_t)w.r * p.c.table_width;
                 }
-                place = find(u);
+                look_up();
             }
-            if (n >= 2 && !wait(bar(kKEmpty + b), ((n >> 1) - 1) & 1u)) break;
-            {
-                const uint32_t dst = k_buf + b * kOperand + (D == 128 ? k_half * 16384 : 0) + k_tok * 128;
+        }
+    } else if (begin < end && warp >= kWarpConv) {
+        // ---------------- codes to fp16
+        // A warp has 16 tokens, all in one page; 16 bytes of codes and a scale are 32 channels and become 4 units of
+        // 16 bytes. D = 128: lane / 4 is one of 8 tokens, twice; 64: lane / 2 one of the 16. Loads are contiguous. Of
+        // the 8 lanes that store at a time those of one token have two pairs with the same banks, so that one pair
+        // takes its units in another order (flip), and the two tokens are ones whose orders do not meet either.
+        constexpr int kUnits = D / 64, kQ = D / 32;
+        const int cw = warp - kWarpConv, qc = lane % kQ, l4 = lane / kQ;
+        const int tok = D == 128 ? (l4 & 4) | (0x9C >> (2 * (l4 & 3)) & 3) : l4;   // 0 3 1 2 4 7 5 6
+        const bool flip = D == 128 && qc >= 2;
+        const uint32_t own = (D == 128 ? (qc >> 1) * 16384 : 0) + (cw * 16 + tok) * 128 + (((((qc & 1) * 4) ^ (tok & 7)) * 16) ^ (flip ? 16u : 0u));
+        const CacheBlock cb = cache_block(p.c.page_size, D);
+        const uint32_t to_scale = tok * (D / 16) + qc * 2, to_v_scale = cb.v_scales - cb.k_scales + qc * 32 + tok * 2;
+        const uint32_t to_code = tok * (D / 2) + qc * 16;
+        const DequantConst dq = dequant_const();
+        Raw<D> x;
+        Run run;
+        // Loads without a condition, from page 0 where there is none: what is merged into their registers after them
+        // would wait for them.
+        auto load_k = [&](int n) {
+            run = s_run[n & 7][cw];
+            const uint8_t* from = run.codes + to_code;
+            const uint8_t* scale = run.codes + run.scales + to_scale;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
+            for (int i = 0; i < kUnits; ++i) {
+                x.k[i] = *reinterpret_cast<const uint4*>(from + i * (8 * D / 2));
+                x.ks[i] = *reinterpret_cast<const uint16_t*>(scale + i * (8 * D / 16));
+            }
+        };
+        auto load_v = [&]() {
+            const uint8_t* from = run.codes + cb.v_codes + to_code;
+            const uint8_t* scale = run.codes + run.scales + to_v_scale;
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                x.v[i] = *reinterpret_cast<const uint4*>(from + i * (8 * D / 2));
+                x.vs[i] = *reinterpret_cast<const uint16_t*>(scale + i * 16);
+            }
+        };
+        // what no token wrote may be anything: its scale becomes 0
+        auto put = [&](uint32_t dst, const uint4 (&codes)[D / 64], const uint16_t (&scale)[D / 64], int n_in) {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const uint32_t sc = i * 8 + tok < n_in ? scale[i] : 0u;
+                const __half2 s2 = as_half2(sc | (sc << 16));
+                const uint32_t c4[4] = {flip ? codes[i].y : codes[i].x, flip ? codes[i].x : codes[i].y,
+                                        flip ? codes[i].w : codes[i].z, flip ? codes[i].z : codes[i].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     uint32_t h[4];
-                    const __half2 s = c < 4 ? __low2half2(as_half2(x.ks)) : __high2half2(as_half2(x.ks));
-                    dequant(x.k[c], s, dq, h);
-                    const int unit = D == 128 ? c : k_half * 4 + c;
-                    store16(dst + ((unit ^ (k_tok & 7)) * 16), h[0], h[1], h[2], h[3]);
+                    dequant(c4[c], s2, dq, h);
+                    store16((dst + own + i * 1024) ^ (c * 16), h[0], h[1], h[2], h[3]);
                 }
-                if (has_v && v_word == 0 && (v_tg & 1) == 0) s_valid[n & 3][v_tg >> 1] = valid;
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kKFull + b));
-                if (more) load_k(place);
             }
-            if (has_v) {
-                if (n >= 2 && !wait(bar(kVEmpty + b), ((n >> 1) - 1) & 1u)) break;
-                const uint32_t dst = v_buf + b * kOperand + (v_tg >> 3) * (D * 128) + v_word * 8 * 128;
-                const uint32_t sc[4] = {x.vs.x, x.vs.y, x.vs.z, x.vs.w};
+            fence_proxy_async();
+            __syncwarp();
+        };
+        const int tiles = end - begin;
+        if (wait(bar(kRun), 0u)) {
+            load_k(0);
+            load_v();
 #pragma unroll 1
-                for (int z = 0; z < 2; ++z) {   // channels 4 z .. of the word
-                    uint32_t h[4][4];           // [pair of tokens][channel]
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        dequant(__byte_perm(x.v[2 * m], x.v[2 * m + 1], z == 0 ? 0x5410u : 0x7632u), as_half2(sc[m]), dq, h[m]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int d = z * 4 + c;
-                        store16(dst + d * 128 + (((v_tg & 7) ^ d) * 16), h[0][c], h[1][c], h[2][c], h[3][c]);
+            for (int n = 0; n < tiles; ++n) {
+                // The registers that a conversion frees take the next tile's codes at once: their way is as long as
+                // the other conversion and the waits. (A second set that is copied at the loop's end stops there for
+                // the loads instead.)
+                const int b = n & 1, n_in = run.left, next = min(n + 1, tiles - 1);
+                if (n >= 2 && !wait(bar(kKEmpty + b), ((n >> 1) - 1) & 1u)) break;
+                put(k_buf + b * kOperand, x.k, x.ks, n_in);
+                if (lane == 0) {
+                    s_valid[n & 3][cw] = n_in > 0;
+                    mbar_arrive(bar(kKFull + b));
+                    if (cw == 0) {
+                        __threadfence_block();
+                        *(volatile int*)&s_done = n + 1;
                     }
                 }
-                fence_proxy_async();
-                __syncwarp();
+                if (!wait(bar(kRun + (next & 7)), (next >> 3) & 1u)) break;
+                load_k(next);
+                if (n >= 2 && !wait(bar(kVEmpty + b), ((n >> 1) - 1) & 1u)) break;
+                put(v_buf + b * kOperand, x.v, x.vs, n_in);
                 if (lane == 0) mbar_arrive(bar(kVFull + b));
+                load_v();
             }
-            if (more) load_v(place);
         }
     } else if (begin < end && warp >= kWarpSoft) {
         // ---------------- weights: one row a thread
@@ -684,9 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos_lo = w.q.ctx + row0 / p.G, pos_hi = w.q.ctx + min(row0 + kMB - 1, w.q.n_rows - 1) / p.G;
             const int in_hi = min(pos_lo, w.q.keys - 1) - (kTile - 1);
             const int in_lo = p.window > 0 ? (int)max(0ll, (long long)pos_hi - p.window + 1) : 0;
+            const BlockTiles it = w.t;   // in registers: the walk's memory is swept out of the L1 cache by the codes
             float top = -INFINITY, sum = 0.f;
             for (int u = u0; u < u1; ++u, ++n) {
-                const int b = n & 1, key0 = w.t.key0(u);
+                const int b = n & 1, key0 = it.key0(u);
                 ok = wait(bar(kSFull + b), (n >> 1) & 1u);
                 if (!ok) break;
                 if (any) {
@@ -789,9 +801,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; ++k) {
                             uint32_t y[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]) * inv,
-                                                                               __uint_as_float(x[8 * k + 2 * e + 1]) * inv);
+                            for (int e = 0; e < 4; ++e) {   // channels 2 e and 2 e + 1
+                                const int at = 8 * k + (e & 1) * 4 + (e >> 1);
+                                const __nv_bfloat162 v =
+                                    __floats2bfloat162_rn(__uint_as_float(x[at]) * inv, __uint_as_float(x[at + 2]) * inv);
                                 y[e] = *reinterpret_cast<const uint32_t*>(&v);
                             }
                             store16(stage + lane * (D * 2) + (((c * 4 + k) ^ (lane & 7)) * 16), y[0], y[1], y[2], y[3]);
@@ -824,7 +837,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (real) {
                             uint4* o = reinterpret_cast<uint4*>(ws.rows + part * D + c * 32);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                            for (int k = 0; k < 8; ++k) {
+                                const int at = (k / 2) * 8 + k % 2;
+                                o[k] = make_uint4(x[at], x[at + 2], x[at + 4], x[at + 6]);
+                            }
                         }
                         __syncwarp();
                     }

@@ -38,6 +38,19 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
     return d;
 }
 
+// the same for an operand whose M or N is contiguous: rows of 64 elements of it, one row for each K, atoms of 8 rows
+// 1024 bytes apart and chunks of 64 elements `chunk` bytes apart
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t addr, uint32_t chunk)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(chunk >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
 // D (TMEM, fp32) (+)= A (shared memory) x B (shared memory), kind::f16 with the given instruction
 // descriptor
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
@@ -50,29 +63,42 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
-// The same for a converged warp with warp-uniform operands: one lane, elected inside the instruction
-// sequence, issues. (Issued under a test of the lane the operands, which are uniform registers, cost a loop
-// of some 15 instructions an MMA.)
-__device__ __forceinline__ void mma_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+// Four K steps of 16 for a converged warp with warp-uniform operands: one lane, elected inside the instruction
+// sequence, issues. (Issued under a test of the lane the operands, which are uniform registers, cost a loop of some 15
+// instructions an MMA; elected and stepped on for each MMA it took longer to issue than to run.) kA and kB are the
+// steps of the two descriptors, in 16 bytes.
+template <int kA, int kB>
+__device__ __forceinline__ void mma_ss4_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, 2 * %5;\n\tadd.s64 a3, %1, 3 * %5;\n\t"
+        "add.s64 b1, %2, %6;\n\tadd.s64 b2, %2, 2 * %6;\n\tadd.s64 b3, %2, 3 * %6;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "n"(kA), "n"(kB)
         : "memory");
 }
 
 // A in tensor memory (two 16-bit elements of K a column)
-__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+template <int kB>
+__device__ __forceinline__ void mma_ts4_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, 2 * %5;\n\tadd.s64 b3, %2, 3 * %5;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc), "n"(kB)
         : "memory");
 }
 
