@@ -528,13 +528,26 @@ __global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
 // that no request has.
 constexpr int kMergeMany = 8;   // parts of an item from which on the CTA shares it
 
+template <int E>
+__device__ __forceinline__ void load_part(const float* src, float (&v)[E])
+{
+    static_assert(E == 2 || E == 4, "one load");
+    if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, AttendScratch ws)
 {
     pdl_enter();
     __shared__ float2 s_ml[kWarps];
     __shared__ float s_o[kWarps][D];
-    constexpr int E = D / 32, kAhead = 8;
+    constexpr int E = D / 32, kAhead = kMergeMany;   // parts whose loads are under way
     const int kMB = ws.block_rows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     struct Sum {
@@ -556,22 +569,15 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(AttendParams p, A
             float2 ml[kAhead];
             float v[kAhead][E];
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const int kk = k + x * step;
-                ml[x] = make_float2(-INFINITY, 0.f);
-                if (kk < todo.parts) {
-                    const size_t a = ((size_t)(run + kk) * 2 + (kk == 0 ? todo.slot : 0)) * kMB + row;
-                    ml[x] = ws.ml[a];
-                    const float* src = ws.rows + a * D + lane * E;
-#pragma unroll
-                    for (int c = 0; c < E; ++c) v[x][c] = src[c];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < E; ++c) v[x][c] = 0.f;
-                }
+            for (int x = 0; x < kAhead; ++x) {   // loads without a condition, or each would wait for the one before
+                const int kk = min(k + x * step, todo.parts - 1);
+                const size_t a = ((size_t)(run + kk) * 2 + (kk == 0 ? todo.slot : 0)) * kMB + row;
+                ml[x] = ws.ml[a];
+                load_part<E>(ws.rows + a * D + lane * E, v[x]);
             }
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) combine(s, ml[x].x, ml[x].y, v[x]);
+            for (int x = 0; x < kAhead; ++x)
+                if (k + x * step < todo.parts) combine(s, ml[x].x, ml[x].y, v[x]);
         }
         return s;
     };

@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            ((valid >> (16 * c + 8)) & 1u ? 0xFFFF0000u : 0u);
                         return below(hi + 1 - base) & (~below(lo - base) | below(p.window > 0 ? p.sinks - base : 0)) & v;
                     };
-                    float mx = -INFINITY;
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains
                     uint32_t x[32];
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -729,10 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+                        for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(x[j]));
                     }
                     if (edge) tc5::wait_st();
-                    mx *= fac;
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
                     if (u == u0) {
                         top = mx == mx ? mx : -INFINITY;   // NaN: a row that is not finite
                     } else if (__any_sync(0xffffffffu, mx > top + kSlack)) {
@@ -899,9 +899,9 @@ bool attend_tc_supported(const AttendParams& p)
 {
     if (p.dtype != DSPARK_BF16 || (p.c.D != 64 && p.c.D != 128)) return false;
     // A tile costs the same here for 1 row and for 128; the warp kernel's grows with its blocks of 16. 128 requests of
-    // up to 4096 tokens, 4 query heads a key head: 36 rows 278 us here and 215 there, 48 rows 274 and 251, 64 rows 277
-    // and 299, 128 rows 294 and 494. 32 requests of 2048: 48 rows 60 and 58, 64 rows 63 and 67. A window of 512 keys:
-    // 48 rows 71 and 63, 68 rows 76 and 70, 128 rows 82 and 108.
+    // up to 4096 tokens, 4 query heads a key head: 36 rows 234 us here and 214 there, 44 rows 236 and 237, 48 rows 235
+    // and 251, 68 rows 236 and 306, 128 rows 244 and 491. 32 requests of 2048: 48 rows 59 and 58, 64 rows 62 and 67. A
+    // window of 512 keys: 48 rows 75 and 62, 68 rows 78 and 71, 128 rows 84 and 108.
     const long long rows = (long long)p.max_q * p.G;
     if (rows <= 48 || rows >= (1ll << 30)) return false;
     if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - 2048) return false;
