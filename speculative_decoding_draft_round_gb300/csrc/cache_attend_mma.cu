@@ -44,12 +44,13 @@ struct Tile {
     static constexpr uint32_t bytes = v_scales + kTile * D / 16;
 };
 
-// Variants: CTAs on an SM, and the stages that shared memory then allows.
-template <typename T, int D, int NB>
-struct Variant {
-    static constexpr int ctas = sizeof(T) == 4 ? (NB == 1 ? 3 : 2) : (NB == 1 ? 4 : 3);
-    static constexpr int stages = ctas == 4 && D == 128 ? 2 : 3;
-};
+// Variants: CTAs on an SM. Registers count for more than warps: two column tiles with three CTAs (168 registers, 224
+// bytes of spills) took 58 us for a window of 512 keys and 16 rows a request, with two 47; one column tile of bf16 took
+// 86 us with four for the decode batch (128 x up to 4096 tokens), 84 with three, 92 with two. More stages than three:
+// no gain.
+template <int NB>
+constexpr int kCtas = NB == 1 ? 3 : 2;
+constexpr int kStages = 3;   // tiles a warp has in flight
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -112,12 +113,11 @@ struct Place {
 };
 
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(kThreads, Variant<T, D, NB>::ctas)
+__global__ void __launch_bounds__(kThreads, kCtas<NB>)
     cache_attend_mma_kernel(AttendParams p, AttendScratch ws)
 {
     constexpr bool kSplit = sizeof(T) == 4;   // fp32 rows: two fp16 terms
     constexpr int kMB = 8 * NB;               // rows of a block
-    constexpr int kStages = Variant<T, D, NB>::stages;   // tiles a warp has in flight
     constexpr int KS = D / 16;                // products of 16 channels
     constexpr int MT = D / 16;                // tiles of 16 value channels
     constexpr int CH = D / 4;                 // q's channels of a lane
@@ -628,17 +628,13 @@ int block_rows(const AttendParams& p) { return (long long)p.max_q * p.G <= 8 ? 8
 
 int grid_ctas(const AttendParams& p)
 {
-    const bool bf = p.dtype == DSPARK_BF16, few = block_rows(p) == 8;
-    static_assert(Variant<float, 64, 1>::ctas == Variant<float, 128, 1>::ctas, "independent of the width");
-    const int ctas = bf ? (few ? Variant<__nv_bfloat16, 128, 1>::ctas : Variant<__nv_bfloat16, 128, 2>::ctas)
-                        : (few ? Variant<float, 128, 1>::ctas : Variant<float, 128, 2>::ctas);
-    return num_sms() * ctas;
+    return num_sms() * (block_rows(p) == 8 ? kCtas<1> : kCtas<2>);
 }
 
 template <typename T, int D, int NB>
 cudaError_t launch_rows(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
 {
-    const size_t smem = kWarps * Variant<T, D, NB>::stages * Tile<D>::bytes + sizeof(int) * (p.c.R + 1);
+    const size_t smem = kWarps * kStages * Tile<D>::bytes + sizeof(int) * (p.c.R + 1);
     const cudaError_t e = cudaFuncSetAttribute(cache_attend_mma_kernel<T, D, NB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

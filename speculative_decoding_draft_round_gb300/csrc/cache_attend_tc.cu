@@ -26,6 +26,8 @@
 // 17-row batch. Tried and slower: sixteen converting warps (64 registers a thread), weights formed in one pass
 // from scores kept apart from them, two threads a row; a warp that prefetches codes into the L2 cache gained 4% on few
 // rows and lost 2% on prompts.
+#include <algorithm>
+
 #include "attend_convert.cuh"
 #include "attend_plan.cuh"
 #include "cache.cuh"
@@ -898,12 +900,15 @@ cudaError_t launch_tc(const AttendParams& p, const AttendScratch& ws, cudaStream
 bool attend_tc_supported(const AttendParams& p)
 {
     if (p.dtype != DSPARK_BF16 || (p.c.D != 64 && p.c.D != 128)) return false;
-    // A tile costs the same here for 1 row and for 128; the warp kernel's grows with its blocks of 16. 128 requests of
-    // up to 4096 tokens, 4 query heads a key head: 36 rows 234 us here and 214 there, 44 rows 236 and 237, 48 rows 235
-    // and 251, 68 rows 236 and 306, 128 rows 244 and 491. 32 requests of 2048: 48 rows 59 and 58, 64 rows 62 and 67. A
-    // window of 512 keys: 48 rows 75 and 62, 68 rows 78 and 71, 128 rows 84 and 108.
-    const long long rows = (long long)p.max_q * p.G;
-    if (rows <= 48 || rows >= (1ll << 30)) return false;
+    // A tile costs the same here for 1 row and for 128, and an item as much again as some tiles; the warp kernel's tiles
+    // cost by blocks of 16 rows, its items little. 128 requests of up to 4096 tokens, 4 query heads a key head: 36 rows
+    // 232 us here and 198 there, 48 rows 234 and 231, 64 rows 234 and 283, 128 rows 245 and 469; 8 requests of up to
+    // 8192: 48 rows 47 and 46, 64 rows 48 and 58. Where a row reaches few keys the warp kernel holds out longer: 32
+    // requests of up to 2048 tokens, 48 rows 61 and 52, 68 rows 62 and 58, 128 rows 68 and 85; a window of 512 keys, 48
+    // rows 75 and 50, 68 rows 78 and 59, 128 rows 84 and 94.
+    const long long rows = (long long)p.max_q * p.G, room = (long long)p.c.table_width * p.c.page_size;
+    const long long reach = p.window > 0 ? std::min(room, (long long)p.window + p.sinks) : room;
+    if (rows <= (reach <= 18 * kTile ? 80 : 48) || rows >= (1ll << 30)) return false;
     if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - 2048) return false;
     // tiles are counted in 32 bits
     const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;

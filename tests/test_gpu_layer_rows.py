@@ -110,7 +110,7 @@ def test_bad_pages_and_offsets():
     ctx, each, D, page = [40, 10, 0], [2, 1, 1], 64, 16
     pool, table, keys, values = layer._filled(ctx, each, page, 1, D, 31)
     offsets = [0, 2, 3, 4]
-    q = torch.randn((4, 32, D), device=DEV).bfloat16()
+    q = torch.randn((4, 64, D), device=DEV).bfloat16()
     bad = table.copy()
     bad[0, 1] = pool.shape[0]          # tokens 16 .. 31 of request 0
     bad[1, :] = -1                     # all of request 1
@@ -138,9 +138,9 @@ def test_bad_pages_and_offsets():
 def test_rows_past_max_q_are_not_computed():
     ctx, each = [40, 10], [70, 2]
     q, pool, table, offsets, full = _case(ctx, each, 4, 2, 64, 16, seed=77)
-    out = ds.cache_attend(q, pool, layer._i32(table), layer._i32(offsets), layer._i32(ctx), max_q=30)
+    out = ds.cache_attend(q, pool, layer._i32(table), layer._i32(offsets), layer._i32(ctx), max_q=45)
     assert ds.check(out["workspace"]) == ds.ERR_DEVICE_INPUT
-    rows = np.r_[0:30, 70:72]
+    rows = np.r_[0:45, 70:72]
     for n in ("out", "lse"):
         assert torch.equal(out[n][rows], full[n][rows])
 
