@@ -53,25 +53,17 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[kVe
     *reinterpret_cast<uint4*>(p) = v;
 }
 
-// x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8.
+// The 8 codes of x in a word: x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8.
 //
 // Adding 1.5 2^23 + 8 rounds x / s (|x| held to 7 s) to an integer, whose 4 bits are then the number's lowest. The
-// product with 1 / s may fall on the wrong side of a border. The remainder x - c s is one rounding of an exact difference, so
-// one that is not below s / 2 shows that, or a tie: these rare pieces go through settle_code.
+// product with about 1 / s may fall on the wrong side of a border. The remainder x - c s is one rounding of an exact
+// difference, so one that is not below s / 2 shows that, or a tie: these rare pieces (a tie needs few bits in x) are
+// looked at again.
 constexpr float kRound = 12582912.f + 8.f;
 
-__device__ __noinline__ uint32_t settle_code(float x, float s, float inv)
-{
-    float c = fmaf(x, inv, kRound) - kRound;
-    const float r = fmaf(-c, s, x), off = fabsf(r), h = 0.5f * s;
-    if (off > h || (off == h && ((int)c & 1))) c += copysignf(1.f, r);
-    return (uint32_t)((int)fminf(fmaxf(c, -7.f), 7.f) + 8);
-}
-
-// The 8 codes of x in a word.
 __device__ __forceinline__ uint32_t code_word(const float (&x)[kVec], float s)
 {
-    const float inv = 1.f / s, most = 7.f * s, h = 0.5f * s;
+    const float inv = __fdividef(1.f, s), most = 7.f * s, h = 0.5f * s;
     uint32_t word = 0;
     bool settle = false;
     float v[kVec];
@@ -83,13 +75,11 @@ __device__ __forceinline__ uint32_t code_word(const float (&x)[kVec], float s)
         word |= (__float_as_uint(t) & 15u) << (4 * j);
     }
     if (settle) {
-        word = 0;
-#pragma unroll 1
-        for (int j = 0; j < kVec; ++j) {
-            float y = v[0];
 #pragma unroll
-            for (int k = 1; k < kVec; ++k) y = k == j ? v[k] : y;
-            word |= settle_code(y, s, inv) << (4 * j);
+        for (int j = 0; j < kVec; ++j) {
+            const uint32_t code = (word >> (4 * j)) & 15u;
+            const float r = fmaf(8.f - (float)code, s, v[j]), off = fabsf(r);
+            if (off > h || (off == h && (code & 1u))) word += (r > 0.f ? 1u : ~0u) << (4 * j);
         }
     }
     return word;
@@ -104,13 +94,19 @@ struct RowAt {
     int t, half, h, vec;
 };
 
-__device__ __forceinline__ RowAt row_at(uint32_t i, uint32_t each, int Hkv, uint32_t vecs)
+// Quotients by a multiplication: magic = ceil(2^32 / d), off by less than d in the product, is exact while the number
+// times d stays below 2^32. Pieces of a CTA: fewer than 8 kRowsThreads, or those of one token.
+struct RowMagic {
+    uint32_t each, vecs;
+};
+
+__device__ __forceinline__ RowAt row_at(uint32_t i, uint32_t each, int Hkv, uint32_t vecs, RowMagic magic)
 {
     RowAt a;
-    a.t = (int)(i / each);
-    const uint32_t in = i % each;
-    a.vec = (int)(in % vecs);
-    const int row = (int)(in / vecs);
+    a.t = (int)__umulhi(i, magic.each);
+    const uint32_t in = i - a.t * each;
+    const int row = (int)__umulhi(in, magic.vecs);
+    a.vec = (int)(in - row * vecs);
     a.half = row >= Hkv;
     a.h = row - a.half * Hkv;
     return a;
@@ -128,7 +124,7 @@ __device__ __forceinline__ void look_up(const CacheRowsParams& p, int first, int
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsParams p, int aligned, int tokens)
+__global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsParams p, int aligned, int tokens, RowMagic magic)
 {
     pdl_enter();
     __shared__ int2 s_at[kMaxTokens];
@@ -138,7 +134,7 @@ __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsPar
     const uint32_t n = count * each;   // a multiple of 8: the 4 lanes of a group stay together
     const CacheBlock b = cache_block(p.c.page_size, p.c.D);
     for (uint32_t i = threadIdx.x; i < (n + 31) / 32 * 32; i += kRowsThreads) {
-        const RowAt a = row_at(min(i, n - 1), each, p.c.Hkv, vecs);
+        const RowAt a = row_at(min(i, n - 1), each, p.c.Hkv, vecs, magic);
         const int2 at = s_at[a.t];
         const bool live = i < n && at.x >= 0;
         float x[kVec] = {};
@@ -148,14 +144,11 @@ __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsPar
                                        : static_cast<const T*>(p.v) + t * p.v_ts + a.h * p.v_hs;
             load_vec<T>(src + a.vec * kVec, aligned, x);
         }
-        float top = 0.f;
-        bool odd_input = false;
+        uint32_t most = 0;   // magnitudes order like their bits
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const float m = fabsf(x[j]);
-            odd_input |= !(m <= FLT_MAX);
-            top = fmaxf(top, m);   // NaN does not count
-        }
+        for (int j = 0; j < kVec; ++j) most = max(most, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+        float top = __uint_as_float(most);
+        const bool odd_input = most >= 0x7F800000u;
         if (odd_input) {   // an infinity takes the largest code, NaN the code of 0
             top = 0.f;
 #pragma unroll
@@ -185,7 +178,7 @@ __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsPar
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(CacheRowsParams p, int tokens)
+__global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(CacheRowsParams p, int tokens, RowMagic magic)
 {
     pdl_enter();
     __shared__ int2 s_at[kMaxTokens];
@@ -196,7 +189,7 @@ __global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(CacheRowsParam
     const CacheBlock b = cache_block(p.c.page_size, p.c.D);
 #pragma unroll 2
     for (uint32_t i = threadIdx.x; i < n; i += kRowsThreads) {
-        const RowAt a = row_at(i, each, p.c.Hkv, vecs);
+        const RowAt a = row_at(i, each, p.c.Hkv, vecs, magic);
         const int2 at = s_at[a.t];
         float x[kVec] = {};
         if (at.x >= 0) {
@@ -223,6 +216,13 @@ bool rows_aligned(const CacheRowsParams& p)
     return base % 16 == 0 && (strides * (int64_t)sizeof(T)) % 16 == 0;
 }
 
+RowMagic rows_magic(const CacheRowsParams& p)
+{
+    auto of = [](uint64_t d) { return (uint32_t)(((1ull << 32) + d - 1) / d); };
+    const int vecs = p.c.D / kVec;
+    return RowMagic{of(2ull * p.c.Hkv * vecs), of(vecs)};
+}
+
 // Tokens of a CTA: pieces for eight rounds of its threads, fewer where that leaves SMs without work
 int rows_tokens(const CacheRowsParams& p)
 {
@@ -238,20 +238,22 @@ int rows_tokens(const CacheRowsParams& p)
 cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s)
 {
     const int tokens = rows_tokens(p);
+    const RowMagic magic = rows_magic(p);
     const dim3 grid(cdiv(p.T, tokens)), block(kRowsThreads);
     const cudaError_t e =
         p.dtype == DSPARK_BF16
-            ? launch_pdl(cache_append_kernel<__nv_bfloat16>, grid, block, 0, s, p, (int)rows_aligned<__nv_bfloat16>(p), tokens)
-            : launch_pdl(cache_append_kernel<float>, grid, block, 0, s, p, (int)rows_aligned<float>(p), tokens);
+            ? launch_pdl(cache_append_kernel<__nv_bfloat16>, grid, block, 0, s, p, (int)rows_aligned<__nv_bfloat16>(p), tokens, magic)
+            : launch_pdl(cache_append_kernel<float>, grid, block, 0, s, p, (int)rows_aligned<float>(p), tokens, magic);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s)
 {
     const int tokens = rows_tokens(p);
+    const RowMagic magic = rows_magic(p);
     const dim3 grid(cdiv(p.T, tokens)), block(kRowsThreads);
-    const cudaError_t e = p.dtype == DSPARK_BF16 ? launch_pdl(cache_read_kernel<__nv_bfloat16>, grid, block, 0, s, p, tokens)
-                                                 : launch_pdl(cache_read_kernel<float>, grid, block, 0, s, p, tokens);
+    const cudaError_t e = p.dtype == DSPARK_BF16 ? launch_pdl(cache_read_kernel<__nv_bfloat16>, grid, block, 0, s, p, tokens, magic)
+                                                 : launch_pdl(cache_read_kernel<float>, grid, block, 0, s, p, tokens, magic);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
