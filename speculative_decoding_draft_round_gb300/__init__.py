@@ -564,11 +564,17 @@ def _strided(t, name, dtype=None, shape=None):
     return t.data_ptr(), st[0], st[1]
 
 
+def _raw_stream(device):
+    """The handle of the device's current stream; without the Stream object where torch lets it be had so (2 us)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _launch(name, fn, args, workspace, stream):
     """One call of the C ABI on `stream`, by default the current one of the workspace's device."""
     if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor of uint8")
-    s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(workspace.device).cuda_stream
+    s = stream.cuda_stream if stream is not None else _raw_stream(workspace.get_device())
     rc = fn(C.byref(args), workspace.data_ptr(), workspace.numel(), s)
     if rc != 0:
         raise DsparkError(name, rc, lib().dspark_last_error().decode() if rc == 4 else "")
@@ -749,11 +755,14 @@ def cache_attend(q, pool, table, offsets, ctx_len, *, scale=None, window=0, sink
     already holds their own keys; returns {"out"} [T][Hq][D] and, unless lse=False, {"lse"} [T][Hq]. scale
     defaults to 1 / sqrt(D), max_q (most rows of one request) to T; say it where it is known, the kernels
     are chosen by it."""
-    with _on(stream):
-        a, out = cache_attend_args(q, pool, table, offsets, ctx_len, scale=scale, window=window, sinks=sinks,
-                                   max_q=max_q, path=path, lse=lse, out=out)
-        if workspace is None:
-            workspace = torch.zeros(workspace_bytes("cache_attend", a), dtype=torch.uint8, device=q.device)
+    if stream is not None and (out is None or workspace is None):
+        with _on(stream):
+            return cache_attend(q, pool, table, offsets, ctx_len, scale=scale, window=window, sinks=sinks, max_q=max_q,
+                                path=path, lse=lse, out=out, workspace=workspace)
+    a, out = cache_attend_args(q, pool, table, offsets, ctx_len, scale=scale, window=window, sinks=sinks, max_q=max_q,
+                               path=path, lse=lse, out=out)
+    if workspace is None:
+        workspace = torch.zeros(workspace_bytes("cache_attend", a), dtype=torch.uint8, device=q.device)
     _launch("dspark_cache_attend", lib().dspark_cache_attend, a, workspace, stream)
     out["workspace"] = workspace
     return out
