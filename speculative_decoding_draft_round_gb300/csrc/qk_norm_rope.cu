@@ -111,18 +111,16 @@ struct Vec {
 };
 
 template <typename T>
-__device__ __forceinline__ Vec<T> load_row(const T* p, bool on)
+__device__ __forceinline__ Vec<T> load_row(const T* p)
 {
-    Vec<T> v = {};
-    if (on) {
+    Vec<T> v;
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-            v.u[4 * i] = x.x;
-            v.u[4 * i + 1] = x.y;
-            v.u[4 * i + 2] = x.z;
-            v.u[4 * i + 3] = x.w;
-        }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+        v.u[4 * i] = x.x;
+        v.u[4 * i + 1] = x.y;
+        v.u[4 * i + 2] = x.z;
+        v.u[4 * i + 3] = x.w;
     }
     return v;
 }
@@ -167,11 +165,27 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
     if (t >= p.T) return;
     const int l = lane % LPH, sub = lane / LPH, c0 = l * 8;
     const bool on = c0 < p.D;
+    // Loads without a condition (lanes and heads past the ends repeat the last), the first under way before the position.
+    Vec<T> v[kUnroll];
+    auto load = [&](int is_k, int h0) {
+        const T* x0 = static_cast<const T*>(is_k ? p.k : p.q) + (int64_t)t * (is_k ? p.k_ts : p.q_ts) + (on ? c0 : p.D - 8);
+        const int64_t hs = is_k ? p.k_hs : p.q_hs;
+        const int last = (is_k ? p.Hkv : p.Hq) - 1;
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) v[k] = load_row<T>(x0 + min(h0 + k * share * kHeads + sub, last) * hs);
+    };
+    load(0, part * kHeads);
     long long pos = 0;
-    const bool live = token_position(p, t, pos);
+    if (!token_position(p, t, pos)) {   // padding
+        const float zero[8] = {};
+        for (int h = part * kHeads + sub; h < p.Hq + p.Hkv; h += share * kHeads)
+            if (on)
+                store_row<T>(h < p.Hq ? static_cast<T*>(p.q_out) + ((size_t)t * p.Hq + h) * p.D + c0
+                                      : static_cast<T*>(p.k_out) + ((size_t)t * p.Hkv + h - p.Hq) * p.D + c0, zero);
+        return;
+    }
     const int half = p.rot / 2;
-    if (live)
-        for (int i = lane; i < half; i += 32) s_cs[warp][i] = turn(p.freq[i], pos);
+    for (int i = lane; i < half; i += 32) s_cs[warp][i] = turn(p.freq[i], pos);
     __syncwarp();
     // what each of the lane's channels takes of itself and of its pair's other channel
     const int step = half / 8;                            // lanes between the channels of a pair
@@ -190,8 +204,6 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
 #pragma unroll 1
     for (int is_k = 0; is_k < 2; ++is_k) {
         const int heads = is_k ? p.Hkv : p.Hq;
-        const T* x0 = static_cast<const T*>(is_k ? p.k : p.q) + (int64_t)t * (is_k ? p.k_ts : p.q_ts) + c0;
-        const int64_t hs = is_k ? p.k_hs : p.q_hs;
         T* y0 = static_cast<T*>(is_k ? p.k_out : p.q_out) + (size_t)t * heads * p.D + c0;
         const float* gain = is_k ? p.k_gain : p.q_gain;
         uint64_t a[4], b[4];                              // the factors above times the gains
@@ -209,12 +221,7 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
         }
 #pragma unroll 1
         for (int h0 = part * kHeads; h0 < heads; h0 += share * kHeads * kUnroll) {
-            Vec<T> v[kUnroll];
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int h = h0 + k * share * kHeads + sub;
-                v[k] = load_row<T>(x0 + h * hs, on && live && h < heads);
-            }
+            if (is_k || h0 > part * kHeads) load(is_k, h0);
 #pragma unroll
             for (int k = 0; k < kUnroll; ++k) {
                 const int h = h0 + k * share * kHeads + sub;
@@ -228,12 +235,11 @@ __global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, 
                     for (int i = 1; i < 4; ++i) two = fma2(x[i], x[i], two);
                     float sum, more;
                     unpack2(two, sum, more);
-                    sum += more;
+                    sum = on ? sum + more : 0.f;
 #pragma unroll
                     for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     inv = rsqrtf(fmaf(sum, per, p.eps));
                 }
-                if (!live) inv = 0.f;
                 const uint64_t inv2 = pack2(inv, inv);
                 Vec<T> w = v[k];
                 if (!kInter) {
