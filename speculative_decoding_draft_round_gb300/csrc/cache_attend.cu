@@ -8,6 +8,10 @@
 // end. A CTA takes one flat row and one key / value head: its G query heads, four at a time, share
 // each key's codes. A warp takes 32 keys at a time: a lane forms the products of one key, then the
 // lanes share the channels of the value rows.
+//
+// Instructions bound it (2 D fp32 products a row and key, and the codes turned again for every four heads of a query):
+// 1.1 ms for 128 single rows of 32 heads over up to 4096 tokens (0.05 ms of bytes), 6.7 ms for 17 rows a request. It
+// serves the head widths that the matrix kernels do not, and is what they are checked against.
 #include "cache.cuh"
 #include "internal.h"
 

@@ -22,6 +22,11 @@
 // tile's four parts cost more: their operands are uniform, a divergent loop of about 60 instructions a tile). A run that ends inside an item
 // leaves a part (maximum, sum, unnormalised rows) in the workspace, and a second small kernel joins the
 // parts in order.
+//
+// Measured, with the joining kernel: 128 single rows of 32 heads (8 key heads of 128) over up to 4096 tokens 84 us, of
+// 50 us for the bytes; two rows over up to 131072 tokens 49 of 21 us; 9 rows in a window of 1024 keys after up to 16384
+// 46 of 12 us. The kernel alone issues in 62% of the cycles at 54% of the memory's rate (single rows): what a key costs
+// is its 2 D codes to fp16 and its share of the products' set-up, some 420 instructions for 16 tokens.
 #include "attend_convert.cuh"
 #include "attend_plan.cuh"
 #include "cache.cuh"

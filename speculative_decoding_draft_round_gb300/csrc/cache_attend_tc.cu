@@ -18,14 +18,16 @@
 // All waits are bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT and ends the CTA's
 // loops, its MMAs land, and tensor memory is freed.
 //
-// Bound: prompts need 4 D flops for each row and key, 0.11 ms at the tensor cores' rate for 2 x 2048 rows of 32 heads
-// after up to 4096 tokens, and take 0.22 ms; few rows need the cache's bytes once, 0.053 ms for 128 requests of up to
-// 4096 tokens, and take 0.28 ms. What both wait for is the turning of codes into operands: a tile takes 3600 cycles of
-// the SM for 7500 warp instructions of all roles, half of its issue slots, and as long for 20 rows as for 128. Without
-// the conversion 193 us of 218 are left of the prompts, without conversion, weights and products 116 of 276 us of the
-// 17-row batch. Tried and slower: sixteen converting warps (64 registers a thread), weights formed in one pass
-// from scores kept apart from them, two threads a row; a warp that prefetches codes into the L2 cache gained 4% on few
-// rows and lost 2% on prompts.
+// Bound: prompts need 4 D flops for each row and key, 59 us at the tensor cores' rate for 2 x 2048 rows of 32 heads after
+// 650 tokens on average, and take 212; few rows need the cache's bytes once, 54 us for 128 requests of up to 17 rows
+// and 4096 tokens, and take 232 (28% tensor, 48% of the issue slots). A tile of few rows takes about 2700 cycles, whatever
+// the rows are: one group's weights take 2100 to 2400 of them (four loads of tensor memory for the maximum, four for the
+// weights, 330 cycles each, twice as long for the first because the loop's instructions have to come back), then its
+// products and the next S follow in 300. Items of few tiles add the way of the next item's q rows (7000 cycles after
+// its buffer is free, two buffers). Tried and slower: sixteen converting warps (64 registers a thread), weights in one
+// pass from scores kept apart from them, two threads a row (265 and 242 us: the fixed parts do not halve), prefetches by
+// the converting warps themselves, bulk prefetches (3 ms: they hold up the shared-memory fences), values transposed on
+// their way into shared memory (276 us).
 #include <algorithm>
 
 #include "attend_convert.cuh"

@@ -3,6 +3,10 @@
 //
 // A thread takes 8 channels of a row: one 32-bit word of codes. The 4 threads of a group of 32
 // channels find its largest magnitude with two shuffles. Both kernels move each byte once.
+//
+// Bound: the bytes, 2 us for 2176 tokens of 8 heads of 128 in bf16 and 12.7 us for 16384, but a code costs more than its
+// two bytes: 8.3 and 40 us for the append (65 us while its indices took divisions and a border's codes a loop), 4.9 and
+// 22 us for reading back. 50000 tokens of 4 heads of 64 in fp32: 31 and 31 us of 34 for both.
 #include "cache.cuh"
 #include "internal.h"
 
