@@ -25,8 +25,9 @@
 // weights, 330 cycles each, twice as long for the first because the loop's instructions have to come back), then its
 // products and the next S follow in 300. Items of few tiles add the way of the next item's q rows (7000 cycles after
 // its buffer is free, two buffers). Tried and slower: sixteen converting warps (64 registers a thread), weights in one
-// pass from scores kept apart from them, two threads a row (265 and 242 us: the fixed parts do not halve), prefetches by
-// the converting warps themselves, bulk prefetches (3 ms: they hold up the shared-memory fences), values transposed on
+// pass from scores kept apart from them, two threads a row (265 and 242 us: the fixed parts do not halve), the two groups
+// on alternate tiles of an item (297 and 259 us: with both at work the conversion takes 2800 cycles a tile, and one O has
+// to be read out between items), prefetches by the converting warps themselves, bulk prefetches (3 ms: they hold up the shared-memory fences), values transposed on
 // their way into shared memory (276 us).
 #include <algorithm>
 
