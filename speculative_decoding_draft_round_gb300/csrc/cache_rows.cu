@@ -5,7 +5,7 @@
 // channels find its largest magnitude with two shuffles. Both kernels move each byte once.
 //
 // Bound: the bytes, 2 us for 2176 tokens of 8 heads of 128 in bf16 and 12.7 us for 16384, but a code costs more than its
-// two bytes: 8.3 and 40 us for the append (65 us while its indices took divisions and a border's codes a loop), 4.9 and
+// two bytes: 7.8 and 40 us for the append (65 us while its indices took divisions and a border's codes a loop), 4.9 and
 // 22 us for reading back. 50000 tokens of 4 heads of 64 in fp32: 31 and 31 us of 34 for both.
 #include "cache.cuh"
 #include "internal.h"
@@ -232,7 +232,7 @@ int rows_tokens(const CacheRowsParams& p)
 {
     const int each = 2 * p.c.Hkv * (p.c.D / kVec);
     int tokens = 8 * kRowsThreads / each;
-    const long long fair = ((long long)p.T + 4ll * num_sms() - 1) / (4ll * num_sms());
+    const long long fair = ((long long)p.T + 8ll * num_sms() - 1) / (8ll * num_sms());
     if (tokens > fair) tokens = (int)fair;
     return tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;
 }

@@ -9,9 +9,9 @@
 //
 // The bytes bound it: each row read once and written once. rope_vec_kernel keeps 16-byte pieces in registers
 // between the norm's sum and the rotation, with several heads' loads in flight; rope_any_kernel takes the
-// shapes that the pieces do not fit. Measured: 32749 tokens of 40 heads of 128 in bf16 (671 MB) 117 us, 99 us at the
+// shapes that the pieces do not fit. Measured: 32749 tokens of 40 heads of 128 in bf16 (671 MB) 114 us, 99 us at the
 // copy's rate (148 us while a condition around each load made it wait for the one before); 2176 such tokens 13 us of 6.6,
-// where the chain position, context, sines, rows is what is left; 16384 with half-split pairs 80 us of 49, the
+// where the chain position, context, sines, rows is what is left; 16384 with half-split pairs 67 us of 49, the
 // shuffles that bring a pair's other half.
 #include "common.cuh"
 #include "internal.h"
@@ -154,10 +154,12 @@ __device__ __forceinline__ void store_row(T* p, const float (&y)[8])
         reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
 }
 
-constexpr int kVecWarps = 8;
+// 24 warps an SM in CTAs of four: 16384 tokens with half-split pairs 67 us, 80 with the 16 warps that unbounded registers
+// leave; in CTAs of eight 69
+constexpr int kVecWarps = 4, kVecCtas = 6;
 
 template <typename T, int LPH, bool kInter>
-__global__ void __launch_bounds__(kVecWarps * 32) rope_vec_kernel(RopeParams p, int share)
+__global__ void __launch_bounds__(kVecWarps * 32, kVecCtas) rope_vec_kernel(RopeParams p, int share)
 {
     constexpr int kHeads = 32 / LPH;                      // heads of a warp's step
     constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
@@ -285,7 +287,8 @@ template <typename T, bool kInter>
 cudaError_t launch_lanes(const RopeParams& p, cudaStream_t s)
 {
     const int lph = p.D <= 32 ? 4 : p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    // warps that share a token: as many as give each SM some 16 warps, and each warp a head
+    // Warps that share a token: as many as give each SM some 16 warps, and each warp a head. Each forms the token's sines:
+    // 2176 tokens take 13 us with one or two warps a token, 19 with four.
     int share = 1;
     while (share < kVecWarps && (long long)p.T * share < 16ll * num_sms() && share * (32 / lph) < p.Hq) share *= 2;
     const dim3 grid(cdiv(p.T, kVecWarps / share)), block(kVecWarps * 32);
