@@ -885,6 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+constexpr size_t kStatic = 4096;   // more than the kernel's fixed shared memory
+
 template <int D>
 size_t tc_smem(int R) { return 6 * 128 * D * 2 + sizeof(int) * (R + 1) + 1024; }
 
@@ -912,7 +914,7 @@ bool attend_tc_supported(const AttendParams& p)
     const long long rows = (long long)p.max_q * p.G, room = (long long)p.c.table_width * p.c.page_size;
     const long long reach = p.window > 0 ? std::min(room, (long long)p.window + p.sinks) : room;
     if (rows <= (reach <= 18 * kTile ? 80 : 48) || rows >= (1ll << 30)) return false;
-    if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - 2048) return false;
+    if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - kStatic) return false;
     // tiles are counted in 32 bits
     const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
     return (double)p.c.R * p.c.Hkv * (double)(rows / kMB + 1) * (double)tiles < 2147483647.0;

@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (_launch, _on, assemble, cache_append, cache_append_args, cache_attend, cache_attend_args, cache_pool,
+from . import (_launch, _on, assemble, assemble_args, cache_append, cache_append_args, cache_attend, cache_attend_args, cache_pool,
                check, lib, qk_norm_rope, qk_norm_rope_args, rope_frequencies, workspace_bytes)
 
 
@@ -60,6 +60,9 @@ class VerifyPass:
                 cache_append_args(self.turned["k"], v, *at),
                 cache_attend_args(self.turned["q"], pool, self.table, b["offsets"], self.ctx_len, window=window,
                                   sinks=sinks, max_q=gamma_max + 1, out=self.attended)[0]))
+        size = workspace_bytes("assemble", assemble_args(self.ctx_len, self.ctx_len, torch.zeros((R, gamma_max), **i32),
+                                                         out=self.batch)[0])
+        self.batch["workspace"] = torch.zeros(size, dtype=torch.uint8, device=device)
         self.ws = torch.zeros(max(workspace_bytes("cache_attend", self._calls[0][2]), 256), dtype=torch.uint8,
                               device=device)
 
@@ -71,7 +74,7 @@ class VerifyPass:
     def assemble(self, keep, anchor, tokens, stream=None):
         """The admitted prefixes as this pass's flat batch; returns it (flat_tokens, flat_request, flat_position,
         offsets)."""
-        assemble(keep, anchor, tokens, out=self.batch, workspace=self.batch.get("workspace"), stream=stream)
+        assemble(keep, anchor, tokens, out=self.batch, workspace=self.batch["workspace"], stream=stream)
         return self.batch
 
     def layer(self, l, stream=None):
@@ -107,7 +110,7 @@ class VerifyPass:
 
     def check(self, stream=None) -> int:
         """The first device status recorded since the last check."""
-        codes = [check(w, stream) for w in (self.ws, self.batch.get("workspace")) if w is not None]
+        codes = [check(w, stream) for w in (self.ws, self.batch["workspace"])]
         return next((c for c in codes if c), 0)
 
 

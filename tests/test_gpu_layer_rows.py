@@ -62,6 +62,15 @@ def test_many_requests():
     _case(rng.integers(0, 400, R).tolist(), rng.integers(0, 6, R).tolist(), 4, 1, 64, 16, seed=9)
 
 
+@pytest.mark.parametrize("R", [7679, 7680, 8100, 8192])
+def test_as_many_requests_as_there_can_be(R):
+    """Around the number whose places still fit shared memory, and the most the library takes."""
+    each = np.zeros(R, dtype=int)
+    each[::97] = 1
+    each[R - 1], each[R // 2] = 3, 40
+    _case((np.arange(R) % 23).tolist(), each.tolist(), 2, 1, 128, 16, seed=R)
+
+
 def test_long_keys_of_one_request():
     """One item over every run: its parts are joined by the next kernel."""
     _case([20011, 3], [33, 2], 4, 2, 64, 64, seed=5)
