@@ -540,9 +540,12 @@ CACHE_GROUP = 32     # channels that share a scale
 # These calls are made for every layer of a pass, so their checks are quick where all is well: one comparison
 # a property, and the slow, explaining check only where one fails.
 
+_Tensor, _i32, _u8, _f32 = torch.Tensor, torch.int32, torch.uint8, torch.float32
+
+
 def _need(t, name, dtype, shape):
     """A contiguous CUDA tensor of this type and shape."""
-    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if t.__class__ is _Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
     _dev(t, name, dtype, shape)
     return _ptr(t)
@@ -572,7 +575,7 @@ def _raw_stream(device):
 
 def _launch(name, fn, args, workspace, stream):
     """One call of the C ABI on `stream`, by default the current one of the workspace's device."""
-    if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+    if workspace.dtype is not _u8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor of uint8")
     s = stream.cuda_stream if stream is not None else _raw_stream(workspace.get_device())
     rc = fn(C.byref(args), workspace.data_ptr(), workspace.numel(), s)
@@ -615,7 +618,7 @@ def qk_norm_rope_args(q, k, freq, position, *, request=None, ctx_len=None, q_gai
     if freq is not None:
         rot = 2 * freq.numel()
         fp = _need(freq, "freq", torch.int64, (rot // 2,))
-    i32, f32 = torch.int32, torch.float32
+    i32, f32 = _i32, _f32
     pp = _need(position, "position", i32, (T,))
     rp = None if request is None else _need(request, "request", i32, (T,))
     R, cp = 0, None
@@ -670,17 +673,19 @@ def cache_pool(n_pages, Hkv, page_size, D, *, device="cuda"):
 
 def cache_view(pool, table, ctx_len, D):
     """The C struct of a cache: pool (cache_pool), table [R][width] int32, ctx_len [R] int32."""
-    if not isinstance(pool, torch.Tensor) or not isinstance(table, torch.Tensor):
-        raise TypeError("pool and table must be CUDA tensors")
-    if pool.dim() != 3 or table.dim() != 2:
-        raise ValueError("pool must be [pages][heads][block] and table [requests][pages]")
-    R, width = table.shape
-    n_pages, Hkv, block = pool.shape
+    try:
+        shape, at = pool.shape, table.shape
+        n_pages, Hkv, block = shape
+        R, width = at
+    except AttributeError:
+        raise TypeError("pool and table must be CUDA tensors") from None
+    except ValueError:
+        raise ValueError("pool must be [pages][heads][block] and table [requests][pages]") from None
     page_size = block * 8 // (9 * D) if D > 0 else 0
     if page_size * D * 9 != block * 8:
         raise ValueError("pool blocks of %d bytes hold no whole tokens of width %d" % (block, D))
-    return Cache(_need(pool, "pool", torch.uint8, (n_pages, Hkv, block)), n_pages, page_size, Hkv, D, R, width, 0,
-                 _need(table, "table", torch.int32, (R, width)), _need(ctx_len, "ctx_len", torch.int32, (R,)))
+    return Cache(_need(pool, "pool", _u8, shape), n_pages, page_size, Hkv, D, R, width, 0,
+                 _need(table, "table", _i32, at), _need(ctx_len, "ctx_len", _i32, (R,)))
 
 
 def cache_append_args(k, v, pool, table, request, position, ctx_len):
@@ -691,8 +696,8 @@ def cache_append_args(k, v, pool, table, request, position, ctx_len):
     if pool.shape[1] != Hkv:
         raise ValueError("k has %d heads, the pool %d" % (Hkv, pool.shape[1]))
     return CacheAppendArgs(C.sizeof(CacheAppendArgs), T, _dtype_code(k), 0, cache, kp, vp, k_ts, k_hs, v_ts, v_hs,
-                           _need(request, "request", torch.int32, (T,)),
-                           _need(position, "position", torch.int32, (T,)))
+                           _need(request, "request", _i32, (T,)),
+                           _need(position, "position", _i32, (T,)))
 
 
 def cache_append(k, v, pool, table, request, position, ctx_len, *, workspace=None, stream=None):
@@ -711,8 +716,8 @@ def cache_read_args(pool, table, request, position, ctx_len, *, D, dtype=torch.b
         out = {n: torch.empty((T, Hkv, D), dtype=dtype, device=pool.device) for n in ("k", "v")}
     kp, vp = (_need(out[n], "out " + n, dtype, (T, Hkv, D)) for n in ("k", "v"))
     a = CacheReadArgs(C.sizeof(CacheReadArgs), T, _dtype_code(out["k"]), 0, cache,
-                      _need(request, "request", torch.int32, (T,)),
-                      _need(position, "position", torch.int32, (T,)), kp, vp)
+                      _need(request, "request", _i32, (T,)),
+                      _need(position, "position", _i32, (T,)), kp, vp)
     return a, out
 
 
@@ -736,16 +741,16 @@ def cache_attend_args(q, pool, table, offsets, ctx_len, *, scale=None, window=0,
     qp, q_ts, q_hs = _strided(q, "q")
     T, Hq, D = q.shape
     cache = cache_view(pool, table, ctx_len, D)
-    fp = _need(offsets, "offsets", torch.int32, (table.shape[0] + 1,))
+    fp = _need(offsets, "offsets", _i32, (table.shape[0] + 1,))
     if out is None:
         out = {"out": torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)}
         if lse:
-            out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            out["lse"] = torch.empty((T, Hq), dtype=_f32, device=q.device)
     l = out.get("lse")
     a = CacheAttendArgs(C.sizeof(CacheAttendArgs), T, Hq, _dtype_code(q), path, max(1, T) if max_q is None else max_q,
                         window, sinks, 1.0 / math.sqrt(D) if scale is None else scale, 0, cache, qp, q_ts, q_hs, fp,
                         _need(out["out"], "out", q.dtype, (T, Hq, D)),
-                        None if l is None else _need(l, "lse", torch.float32, (T, Hq)))
+                        None if l is None else _need(l, "lse", _f32, (T, Hq)))
     return a, out
 
 

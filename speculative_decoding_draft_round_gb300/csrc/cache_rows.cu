@@ -5,7 +5,7 @@
 // channels find its largest magnitude with two shuffles. Both kernels move each byte once.
 //
 // Bound: the bytes, 2 us for 2176 tokens of 8 heads of 128 in bf16 and 12.7 us for 16384, but a code costs more than its
-// two bytes: 7.8 and 40 us for the append (65 us while its indices took divisions and a border's codes a loop), 4.9 and
+// two bytes: 7.3 and 37 us for the append (65 us while its indices took divisions and a border's codes a loop), 4.9 and
 // 22 us for reading back. 50000 tokens of 4 heads of 64 in fp32: 31 and 31 us of 34 for both.
 #include "cache.cuh"
 #include "internal.h"
@@ -57,23 +57,22 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[kVe
     *reinterpret_cast<uint4*>(p) = v;
 }
 
-// The 8 codes of x in a word: x / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8.
+// The 8 codes of v in a word: v / s rounded to the nearest integer, ties to even, in -7 .. 7 (s > 0), plus 8.
 //
-// Adding 1.5 2^23 + 8 rounds x / s (|x| held to 7 s) to an integer, whose 4 bits are then the number's lowest. The
+// Adding 1.5 2^23 + 8 rounds v / s to an integer, whose 4 bits are then the number's lowest. The
 // product with about 1 / s may fall on the wrong side of a border. The remainder x - c s is one rounding of an exact
-// difference, so one that is not below s / 2 shows that, or a tie: these rare pieces (a tie needs few bits in x) are
+// difference, so one that is not below s / 2 shows that, or a tie: these rare pieces (a tie needs few bits in v) are
 // looked at again.
 constexpr float kRound = 12582912.f + 8.f;
 
-__device__ __forceinline__ uint32_t code_word(const float (&x)[kVec], float s)
+// v may pass 7 s by less than half a step, unless the scale is one that fp16 holds badly: the caller holds it to 7 s then.
+__device__ __forceinline__ uint32_t code_word(const float (&v)[kVec], float s)
 {
-    const float inv = __fdividef(1.f, s), most = 7.f * s, h = 0.5f * s;
+    const float inv = __fdividef(1.f, s), h = 0.5f * s;
     uint32_t word = 0;
     bool settle = false;
-    float v[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        v[j] = fminf(fmaxf(x[j], -most), most);
         const float t = fmaf(v[j], inv, kRound);
         settle |= fabsf(fmaf(kRound - t, s, v[j])) >= h;
         word |= (__float_as_uint(t) & 15u) << (4 * j);
@@ -168,6 +167,11 @@ __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(CacheRowsPar
         const float s8 = __bfloat162float(__float2bfloat16_rn(top * (1.f / 7.f)));
         const __half sh = __float2half_rn(fminf(s8, kCacheMaxScale));
         const float s = __half2float(sh);
+        if (odd_input || s < 0x1p-13f || s >= kCacheMaxScale) {   // few bits of the scale are left, or it is the largest
+            const float hold = 7.f * s;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) x[j] = fminf(fmaxf(x[j], -hold), hold);
+        }
         const uint32_t word = s > 0.f ? code_word(x, s) : 0x88888888u;   // the code of 0
         uint8_t* blk = cache_page_block(p.c, at.x, a.h, b.bytes);
         const uint32_t codes = a.half == 0 ? 0u : b.v_codes;
