@@ -20,8 +20,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (_launch, _on, assemble, assemble_args, cache_append, cache_append_args, cache_attend, cache_attend_args, cache_pool,
-               check, lib, qk_norm_rope, qk_norm_rope_args, rope_frequencies, workspace_bytes)
+from . import (_launch, _on, assemble, assemble_args, cache_append, cache_append_args, cache_attend_args, cache_pool, check,
+               lib, qk_norm_rope, qk_norm_rope_args, rope_frequencies, workspace_bytes)
 
 
 class VerifyPass:
@@ -65,6 +65,8 @@ class VerifyPass:
         self.batch["workspace"] = torch.zeros(size, dtype=torch.uint8, device=device)
         self.ws = torch.zeros(max(workspace_bytes("cache_attend", self._calls[0][2]), 256), dtype=torch.uint8,
                               device=device)
+        self._prompt_ws = {}                        # of the prompts' attention, by stream and size
+        self._captured = torch.zeros(1, **i32)      # the status of prompts in graphs
 
     def _heads(self, qkv):
         """Views of the projection's rows: q [T][Hq][D], k and v [T][Hkv][D]."""
@@ -95,8 +97,26 @@ class VerifyPass:
                               **self._rope[l])
         cache_append(turned["k"], v, self.pools[l], self.table, request, position, self.ctx_len, workspace=self.ws,
                      stream=stream)
-        return cache_attend(turned["q"], self.pools[l], self.table, offsets, self.ctx_len, window=self.window,
-                            sinks=self.sinks, max_q=max_q, lse=False, stream=stream)["out"]
+        with _on(stream):
+            a, out = cache_attend_args(turned["q"], self.pools[l], self.table, offsets, self.ctx_len, window=self.window,
+                                       sinks=self.sinks, max_q=max_q, lse=False)
+            ws = self._prompt_workspace(a)
+            _launch("dspark_cache_attend", lib().dspark_cache_attend, a, ws, None)
+            if torch.cuda.is_current_stream_capturing():
+                torch.maximum(self._captured, ws[:4].view(torch.int32), out=self._captured)
+        return out["out"]
+
+    def _prompt_workspace(self, args):
+        """The current stream's workspace for a prompt's attention. Its status word has to last until check(), so
+        workspaces stay: one for each size (a kernel has one size, whatever the prompt) and stream (prompts on two
+        streams may run at the same time). A captured call has one of the graph's own, and its status is kept apart."""
+        size, here = max(workspace_bytes("cache_attend", args), 256), torch.cuda.current_stream(self.qkv.device)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(size, dtype=torch.uint8, device=self.qkv.device)
+        ws = self._prompt_ws.get((here, size))
+        if ws is None:
+            ws = self._prompt_ws[here, size] = torch.zeros(size, dtype=torch.uint8, device=self.qkv.device)
+        return ws
 
     def advance_by(self, tokens, stream=None):
         """ctx_len += tokens ([R] int32 on the device)."""
@@ -109,9 +129,11 @@ class VerifyPass:
             self.ctx_len += accepted + 1
 
     def check(self, stream=None) -> int:
-        """The first device status recorded since the last check."""
-        codes = [check(w, stream) for w in (self.ws, self.batch["workspace"])]
-        return next((c for c in codes if c), 0)
+        """The first device status recorded since the last check, the prompts' among them. Waits for `stream`, by
+        default the current one, where graphs with prompts have been replayed, and for the prompts' own streams."""
+        prompts = [check(w, s) for (s, _), w in self._prompt_ws.items()]
+        codes = [check(w, stream) for w in (self.ws, self.batch["workspace"], self._captured)]
+        return next((c for c in codes + prompts if c), 0)
 
 
 class ToyTarget:
