@@ -201,8 +201,8 @@ struct Walk {
 
 // ------------------------------------------------------------------ waits
 
-// A waiting warp is suspended by its try for up to kNap, or the limit if that is less, and then looks at the timer
-// and the abort flag.
+// A waiting warp is suspended by its try for up to kNap and then looks at the timer and the abort flag. The time of a
+// try is a hint that a suspension may pass, so under a limit below kNap tries do not suspend.
 constexpr uint32_t kNapNs = 100000;
 
 __device__ __forceinline__ bool try_for(uint32_t bar, uint32_t parity, uint32_t ns)
@@ -222,8 +222,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
                                        unsigned long long limit_ns)
 {
     const unsigned long long t0 = globaltimer();
-    const uint32_t nap = limit_ns < kNapNs ? (uint32_t)limit_ns : kNapNs;
-    while (!try_for(bar, parity, nap)) {
+    while (!(limit_ns < kNapNs ? mbar_test_wait(bar, parity) : try_for(bar, parity, kNapNs))) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
