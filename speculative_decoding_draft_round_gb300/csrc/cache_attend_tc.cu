@@ -233,6 +233,23 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     return true;
 }
 
+// The same for a count in shared memory that another warp raises to `least`.
+__device__ __noinline__ bool wait_count(const volatile int* count, int least, volatile int* abort, int* status,
+                                        unsigned long long limit_ns)
+{
+    const unsigned long long t0 = globaltimer();
+    while (*count < least) {
+        if (*abort) return false;
+        if (globaltimer() - t0 > limit_ns) {
+            *abort = 1;
+            raise_status(status, DSPARK_ERR_TIMEOUT);
+            return false;
+        }
+        __nanosleep(100);
+    }
+    return true;
+}
+
 // Warp-wide: true where every lane saw the phase end.
 struct Waits {
     volatile int* abort;
@@ -241,6 +258,11 @@ struct Waits {
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
         const bool ok = mbar_test_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
+        return __all_sync(0xffffffffu, ok);
+    }
+    __device__ __forceinline__ bool reaches(const volatile int* count, int least) const
+    {
+        const bool ok = *count >= least || wait_count(count, least, abort, status, limit_ns);
         return __all_sync(0xffffffffu, ok);
     }
 };
@@ -531,9 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk w;
         w.start(p, s_pre, begin);
         const CacheBlock cb = cache_block(p.c.page_size, D);
-        const volatile int* done = &s_done;
         const int slice = lane >> 2, sub = lane & 3;   // 16 tokens, and part of their lines
-        const unsigned long long t0 = globaltimer();
         const int tiles = end - begin, magic = p.page_magic, P = p.c.page_size;
         BlockTiles it = w.t;   // in registers: the walk's memory is swept out of the L1 cache by the codes
         int u = w.u, keys = w.q.keys, h = w.h, key, page;
@@ -547,12 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < tiles; ++n) {
             // An entry is free when tile n - 8 is: the first warp is past the keys of tile n - 5, the others past those
             // of tile n - 7, or it would have waited for them.
-            bool ok = true;
-            while (ok && n - *done > kAhead) {
-                if (*wait.abort || globaltimer() - t0 > 4 * wait_ns) ok = false;
-                __nanosleep(100);
-            }
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!wait.reaches(&s_done, n - kAhead)) break;
             __threadfence_block();
             const int left = keys - key, slot = key - page_of(key, magic) * P;
             const bool in = page >= 0 && page < p.c.n_pages;
