@@ -639,11 +639,11 @@ int grid_ctas(const AttendParams& p)
 template <typename T, int D, int NB>
 cudaError_t launch_rows(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
 {
-    const size_t smem = kWarps * kStages * Tile<D>::bytes + sizeof(int) * (p.c.R + 1);
-    const cudaError_t e = cudaFuncSetAttribute(cache_attend_mma_kernel<T, D, NB>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto smem = [](int R) { return kWarps * kStages * Tile<D>::bytes + sizeof(int) * (R + 1); };
+    static std::atomic<uint64_t> admitted{0};
+    const cudaError_t e = admit_smem(cache_attend_mma_kernel<T, D, NB>, smem(DSPARK_MAX_SLOTS), admitted);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attend_mma_kernel<T, D, NB>, dim3(grid_ctas(p)), dim3(kThreads), smem, s, p, ws);
+    return launch_pdl(cache_attend_mma_kernel<T, D, NB>, dim3(grid_ctas(p)), dim3(kThreads), smem(p.c.R), s, p, ws);
 }
 
 template <typename T, int D>

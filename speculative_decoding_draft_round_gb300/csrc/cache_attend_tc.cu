@@ -900,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr size_t kStatic = 4096;   // more than the kernel's fixed shared memory
+constexpr size_t kMostSmem = 227 * 1024 - kStatic;
 
 template <int D>
 size_t tc_smem(int R) { return 6 * 128 * D * 2 + sizeof(int) * (R + 1) + 1024; }
@@ -907,11 +908,11 @@ size_t tc_smem(int R) { return 6 * 128 * D * 2 + sizeof(int) * (R + 1) + 1024; }
 template <int D>
 cudaError_t launch_tc(const AttendParams& p, const AttendScratch& ws, cudaStream_t s)
 {
-    const size_t smem = tc_smem<D>(p.c.R);
-    const cudaError_t e =
-        cudaFuncSetAttribute(cache_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> admitted{0};
+    const cudaError_t e = admit_smem(cache_attend_tc_kernel<D>, kMostSmem, admitted);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attend_tc_kernel<D>, dim3(ws.runs), dim3(kThreads), smem, s, p, ws, wait_limit_ns());
+    return launch_pdl(cache_attend_tc_kernel<D>, dim3(ws.runs), dim3(kThreads), tc_smem<D>(p.c.R), s, p, ws,
+                      wait_limit_ns());
 }
 
 }  // namespace
@@ -928,7 +929,7 @@ bool attend_tc_supported(const AttendParams& p)
     const long long rows = (long long)p.max_q * p.G, room = (long long)p.c.table_width * p.c.page_size;
     const long long reach = p.window > 0 ? std::min(room, (long long)p.window + p.sinks) : room;
     if (rows <= (reach <= 18 * kTile ? 80 : 48) || rows >= (1ll << 30)) return false;
-    if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > 227 * 1024 - kStatic) return false;
+    if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > kMostSmem) return false;
     // tiles are counted in 32 bits
     const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
     return (double)p.c.R * p.c.Hkv * (double)(rows / kMB + 1) * (double)tiles < 2147483647.0;

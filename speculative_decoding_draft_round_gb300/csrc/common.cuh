@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dspark.h"
 
 namespace dspark {
@@ -110,6 +112,21 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Admit up to `most` bytes of dynamic shared memory for a kernel, once a device. The attribute is the function's, shared
+// by host threads: `most` is the largest any call asks for, so that no call lowers it under another one's launch.
+template <typename... KArgs>
+inline cudaError_t admit_smem(void (*kernel)(KArgs...), size_t most, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // 2^x by the hardware approximation (the SFU's ex2, flushing subnormal results to zero)
