@@ -470,7 +470,8 @@ dspark_status dspark_cache_read(const dspark_cache_read_args* args, void* worksp
  * the row's largest; two fp16 terms for fp32) and the weights exp(z - max) as fp16 (two terms for
  * fp32); elsewhere a CUDA-core kernel in fp32 runs.
  * Decreasing offsets or more than max_q rows of one request are recorded (DSPARK_ERR_DEVICE_INPUT):
- * that request's rows are not computed, or none past max_q.
+ * that request's rows are not computed, or none past max_q; offsets that repeat so many rows that their
+ * blocks' tiles of keys pass 2^31 leave no row computed.
  */
 typedef struct {
     uint32_t struct_size;

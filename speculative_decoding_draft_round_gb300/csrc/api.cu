@@ -323,7 +323,7 @@ AttendParams attend_params(const dspark_cache_attend_args* a)
 
 bool attend_uses_mma(const dspark_cache_attend_args* a, const AttendParams& p)
 {
-    return a->path != DSPARK_PATH_CUDA_CORE && attend_mma_supported(p);
+    return a->path != DSPARK_PATH_CUDA_CORE && (attend_tc_supported(p) || attend_mma_supported(p));
 }
 
 template <typename T>

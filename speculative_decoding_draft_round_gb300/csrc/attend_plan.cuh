@@ -7,6 +7,20 @@
 
 namespace dspark {
 
+// Tiles are counted in 32 bits, with room for what a run looks ahead.
+constexpr long long kMostTiles = (1ll << 31) - 65536;
+
+// Whether they suffice for T rows of which a request has at most max_q, in blocks of MB, and tiles of `tile` tokens: a
+// request's blocks are those of its rows and one more. Offsets that count rows twice may ask for more than this says;
+// the plan looks again.
+inline bool tiles_fit(const AttendParams& p, int MB, int tile)
+{
+    const long long rows = (long long)(p.max_q < p.T ? p.max_q : p.T) * p.G, all = (long long)p.T * p.G / MB + p.c.R;
+    const long long each = p.c.R * (rows / MB + 1), blocks = each < all ? each : all;
+    const long long tiles = ((long long)p.c.table_width * p.c.page_size + tile - 1) / tile + 1;
+    return rows < (1ll << 30) && (double)blocks * p.c.Hkv * (double)tiles < (double)kMostTiles;
+}
+
 // The item that a run starts and does not end: its rows, and how many runs have parts of it (0: none).
 struct __align__(16) AttendTodo {
     int parts, slot;               // and the run's slot that holds the first
@@ -72,41 +86,64 @@ __device__ __forceinline__ RequestSpan<TILE> request_span(const AttendParams& p,
     return s;
 }
 
-// pre[r] = tiles before request r's; returns the total. Called by all NT threads of the CTA, the first
-// `threads` of which do the work. pre has R + 1 entries, scan NT / 32 + 1.
-template <int NT, int TILE>
-__device__ __forceinline__ int plan_line(const AttendParams& p, int MB, int* pre, int* scan, bool report)
+// The sum over all NT threads of `sum` in `total`, and what the threads before this one have of it. scan has NT / 32
+// entries.
+template <int NT>
+__device__ __forceinline__ long long scan_tiles(long long sum, long long* scan, long long& total)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.c.R;
-    const int each = (R + NT - 1) / NT, r0 = min(tid * each, R), r1 = min(r0 + each, R);
-    int sum = 0;
-    for (int r = r0; r < r1; ++r) {
-        const RequestSpan<TILE> s = request_span<TILE>(p, r, MB, report);
-        const int n = s.tiles * s.blocks * p.c.Hkv;
-        pre[r + 1] = n;
-        sum += n;
-    }
-    int inc = sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    int before = inc - sum, total = 0;
-#pragma unroll
+    long long before = inc - sum;
+    total = 0;
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    if (tid == 0) pre[0] = 0;
+    return before;
+}
+
+// pre[r + 1] holds request r's tiles; r0 .. r1 are the thread's own requests, with `sum` tiles; pre[r] becomes the tiles
+// before request r's. Returns the total, 0 where it is more than 32 bits count (offsets that repeat rows): no row is
+// computed then.
+template <int NT>
+__device__ __forceinline__ int sum_line(const AttendParams& p, int r0, int r1, long long sum, int* pre, long long* scan,
+                                        bool report)
+{
+    long long total, before = scan_tiles<NT>(sum, scan, total);
+    if (total > kMostTiles) {
+        if (report && threadIdx.x == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+        total = 0;
+    }
+    if (threadIdx.x == 0) pre[0] = 0;
     for (int r = r0; r < r1; ++r) {
         before += pre[r + 1];
-        pre[r + 1] = before;
+        pre[r + 1] = (int)before;
     }
     __syncthreads();
-    return total;
+    return (int)total;
+}
+
+// pre[r] = tiles before request r's; returns the total. Called by all NT threads of the CTA. pre has R + 1 entries, scan
+// NT / 32.
+template <int NT, int TILE>
+__device__ __forceinline__ int plan_line(const AttendParams& p, int MB, int* pre, long long* scan, bool report)
+{
+    const int R = p.c.R, each = (R + NT - 1) / NT, r0 = min((int)threadIdx.x * each, R), r1 = min(r0 + each, R);
+    long long sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const RequestSpan<TILE> s = request_span<TILE>(p, r, MB, report);
+        const int n = s.tiles * s.blocks * p.c.Hkv;   // one request's: checked on the host
+        pre[r + 1] = n;
+        sum += n;
+    }
+    return sum_line<NT>(p, r0, r1, sum, pre, scan, report);
 }
 
 // The item a tile of the line belongs to: request r, item q (head, row block) and tile u of the item.

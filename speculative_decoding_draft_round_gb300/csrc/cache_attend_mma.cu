@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<NB>)
     using L = Tile<D>;
     extern __shared__ __align__(128) uint8_t smem[];                     // [kWarps][kStages] tiles, [R + 1] ints
     int* s_pre = reinterpret_cast<int*>(smem + kWarps * kStages * L::bytes);
-    __shared__ int s_scan[kWarps + 1];
+    __shared__ long long s_scan[kWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, i = lane & 3;
@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<NB>)
     // ---------------- the line of tiles and this warp's run of it
     const int total = plan_line<kThreads, kTile>(p, kMB, s_pre, s_scan, blockIdx.x == 0);
     const int runs = gridDim.x * kWarps, run_id = blockIdx.x * kWarps + warp;
-    const int per = (total + runs - 1) / runs;
+    const int per = (int)(((long long)total + runs - 1) / runs);
     const int begin = (int)min((long long)run_id * per, (long long)total);
-    const int end = min(begin + per, total);
+    const int end = (int)min((long long)begin + per, (long long)total);
     if (begin >= end) {
         if (lane == 0) ws.todo[run_id].parts = 0;
         return;
@@ -671,10 +671,7 @@ bool q_aligned(const AttendParams& p)
 bool attend_mma_supported(const AttendParams& p)
 {
     if (p.c.D != 64 && p.c.D != 128) return false;
-    // tiles and rows are counted in 32 bits
-    const long long rows = (long long)p.max_q * p.G;
-    const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
-    return rows < (1ll << 30) && (double)p.c.R * p.c.Hkv * (double)(rows / block_rows(p) + 1) * (double)tiles < 2147483647.0;
+    return tiles_fit(p, block_rows(p), kTile);
 }
 
 size_t attend_scratch(const AttendParams& p, AttendScratch* ws, void* base)

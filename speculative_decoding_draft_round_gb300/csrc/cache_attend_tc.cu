@@ -107,7 +107,7 @@ __device__ __forceinline__ int head_tiles(const AttendParams& p, const Request& 
 }
 
 // pre[r] = tiles before request r's; the total is returned. All threads of the CTA.
-__device__ __forceinline__ int plan(const AttendParams& p, int* pre, int* scan, bool report)
+__device__ __forceinline__ int plan(const AttendParams& p, int* pre, long long* scan, bool report)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.c.R;
     if (R <= 64) {   // few requests, perhaps of many blocks: a warp each
@@ -120,28 +120,9 @@ __device__ __forceinline__ int plan(const AttendParams& p, int* pre, int* scan, 
     }
     __syncthreads();
     const int each = (R + kThreads - 1) / kThreads, r0 = min(tid * each, R), r1 = min(r0 + each, R);
-    int sum = 0;
+    long long sum = 0;
     for (int r = r0; r < r1; ++r) sum += pre[r + 1];
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    int before = inc - sum, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    if (tid == 0) pre[0] = 0;
-    for (int r = r0; r < r1; ++r) {
-        before += pre[r + 1];
-        pre[r + 1] = before;
-    }
-    __syncthreads();
-    return total;
+    return sum_line<kThreads>(p, r0, r1, sum, pre, scan, report);
 }
 
 // Items of a run one after the other: request r, head h, block b, from tile u on. Warp-wide; not inlined,
@@ -353,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint64_t s_bar[kBars];
     __shared__ float s_fac[2][kMB];
     __shared__ __align__(8) uint8_t s_valid[4][8];   // of tile n & 3: which runs of 16 tokens hold keys
-    __shared__ int s_scan[kThreads / 32];
+    __shared__ long long s_scan[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ __align__(16) Run s_run[8][8];       // of tile n & 7, by converting warp
@@ -393,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
     const int total = plan(p, s_pre, s_scan, blockIdx.x == 0);
-    const int per = (total + gridDim.x - 1) / gridDim.x;
+    const int per = (int)(((long long)total + gridDim.x - 1) / gridDim.x);
     const int begin = (int)min((long long)blockIdx.x * per, (long long)total);
-    const int end = min(begin + per, total);
+    const int end = (int)min((long long)begin + per, (long long)total);
     const Waits wait{&s_abort, p.status, wait_ns};
     AttendTodo todo = {};
 
@@ -928,11 +909,9 @@ bool attend_tc_supported(const AttendParams& p)
     // rows 75 and 50, 68 rows 78 and 59, 128 rows 84 and 94.
     const long long rows = (long long)p.max_q * p.G, room = (long long)p.c.table_width * p.c.page_size;
     const long long reach = p.window > 0 ? std::min(room, (long long)p.window + p.sinks) : room;
-    if (rows <= (reach <= 18 * kTile ? 80 : 48) || rows >= (1ll << 30)) return false;
+    if (rows <= (reach <= 18 * kTile ? 80 : 48)) return false;
     if ((p.c.D == 64 ? tc_smem<64>(p.c.R) : tc_smem<128>(p.c.R)) > kMostSmem) return false;
-    // tiles are counted in 32 bits
-    const long long tiles = cdiv((long long)p.c.table_width * p.c.page_size, kTile) + 1;
-    return (double)p.c.R * p.c.Hkv * (double)(rows / kMB + 1) * (double)tiles < 2147483647.0;
+    return tiles_fit(p, kMB, kTile);
 }
 
 int attend_tc_block_rows() { return kMB; }
