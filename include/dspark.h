@@ -472,6 +472,7 @@ dspark_status dspark_cache_read(const dspark_cache_read_args* args, void* worksp
  * Decreasing offsets or more than max_q rows of one request are recorded (DSPARK_ERR_DEVICE_INPUT):
  * that request's rows are not computed, or none past max_q; offsets that repeat so many rows that their
  * blocks' tiles of keys pass 2^31 leave no row computed.
+ * A workspace of more than 256 bytes has to be 16-byte aligned.
  */
 typedef struct {
     uint32_t struct_size;

@@ -297,6 +297,13 @@ dspark_status check_attend(const dspark_cache_attend_args* a)
     return DSPARK_OK;
 }
 
+// The status word and, with `align`, the parts of a workspace that kernels read and write in pieces of 16 bytes
+dspark_status check_workspace(const void* ws, size_t bytes, size_t need, size_t align)
+{
+    if (!ws || bytes < need) return DSPARK_ERR_WORKSPACE;
+    return reinterpret_cast<uintptr_t>(ws) % align ? DSPARK_ERR_INVALID_ARGUMENT : DSPARK_OK;
+}
+
 AttendParams attend_params(const dspark_cache_attend_args* a)
 {
     AttendParams p;
@@ -635,7 +642,8 @@ dspark_status dspark_qk_norm_rope(const dspark_qk_norm_rope_args* a, void* ws, s
     clear_stale_error();
     const dspark_status st = check_rope(a);
     if (st != DSPARK_OK) return st;
-    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
     if (a->T == 0) return DSPARK_OK;
     RopeParams p;
     p.T = a->T;
@@ -681,7 +689,8 @@ dspark_status dspark_cache_append(const dspark_cache_append_args* a, void* ws, s
     clear_stale_error();
     const dspark_status st = check_append(a);
     if (st != DSPARK_OK) return st;
-    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
     if (a->T == 0) return DSPARK_OK;
     CacheRowsParams p;
     memset(&p, 0, sizeof p);
@@ -715,7 +724,8 @@ dspark_status dspark_cache_read(const dspark_cache_read_args* a, void* ws, size_
     clear_stale_error();
     const dspark_status st = check_read(a);
     if (st != DSPARK_OK) return st;
-    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
     if (a->T == 0) return DSPARK_OK;
     CacheRowsParams p;
     memset(&p, 0, sizeof p);
@@ -748,16 +758,19 @@ dspark_status dspark_cache_attend(const dspark_cache_attend_args* a, void* ws, s
     if (st != DSPARK_OK) return st;
     AttendParams p = attend_params(a);
     if (a->path == DSPARK_PATH_TENSOR_CORE && !attend_uses_mma(a, p)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
-    if (!ws || ws_bytes < kStatusBytes) return DSPARK_ERR_WORKSPACE;
+    const bool mma = attend_uses_mma(a, p);
+    const size_t need = kStatusBytes + (mma ? attend_scratch(p, nullptr, nullptr) : 0);
+    const dspark_status sw = check_workspace(ws, ws_bytes, need, mma ? 16 : alignof(int));
+    if (sw != DSPARK_OK) return sw;
     p.status = at<int>(ws, 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!attend_uses_mma(a, p)) {
+    if (!mma) {
         if (a->T == 0) return DSPARK_OK;
         return cuda_status(launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend_simt(p, s); }));
     }
-    AttendScratch scratch;
-    if (ws_bytes < kStatusBytes + attend_scratch(p, &scratch, at<char>(ws, kStatusBytes))) return DSPARK_ERR_WORKSPACE;
     if (a->T == 0) return DSPARK_OK;
+    AttendScratch scratch;
+    attend_scratch(p, &scratch, at<char>(ws, kStatusBytes));
     cudaError_t e = launch(DSPARK_KERNEL_CACHE_ATTEND, s, [&] { return launch_cache_attend(p, scratch, s); });
     if (e == cudaSuccess) e = launch(DSPARK_KERNEL_CACHE_MERGE, s, [&] { return launch_cache_merge(p, scratch, s); });
     return cuda_status(e);

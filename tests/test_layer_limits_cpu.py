@@ -47,3 +47,33 @@ def test_blocks_of_128_rows_are_counted_as_such(run):
     """More blocks of 16 rows than can be counted, but not of 128."""
     assert run(1 << 18, 1, 1 << 18, 32, 8, (1 << 18) // 64, ds.F32) == UNSUPPORTED
     assert run(1 << 18, 1, 1 << 18, 32, 8, (1 << 18) // 64, ds.BF16) == WORKSPACE
+
+
+@pytest.mark.parametrize("D", [128, 96])   # the matrix kernels' workspace, and a status word alone
+def test_workspaces_off_their_boundaries_are_refused(run, D):
+    a = ds.CacheAttendArgs()
+    a.struct_size, a.T, a.Hq, a.max_q, a.scale, a.dtype = C.sizeof(a), 0, 8, 4, 0.1, ds.BF16
+    c = a.cache
+    c.pages = c.table = c.ctx_len = FAKE
+    c.n_pages, c.page_size, c.Hkv, c.D, c.R, c.table_width = 1, 16, 2, D, 3, 4
+    n = C.c_size_t(0)
+    assert ds.lib().dspark_cache_attend_workspace_size(C.byref(a), C.byref(n)) == 0 and (n.value > 256) == (D == 128)
+    for off in range(17):
+        ok = off % (16 if D == 128 else 4) == 0
+        assert ds.lib().dspark_cache_attend(C.byref(a), FAKE + off, n.value, None) == (0 if ok else 1), off
+    assert ds.lib().dspark_cache_attend(C.byref(a), FAKE, n.value - 1, None) == WORKSPACE
+
+
+@pytest.mark.parametrize("call,args", [("qk_norm_rope", ds.QkNormRopeArgs), ("cache_append", ds.CacheAppendArgs),
+                                       ("cache_read", ds.CacheReadArgs)])
+def test_status_words_off_their_boundaries_are_refused(run, call, args):
+    a = args()
+    a.struct_size = C.sizeof(a)
+    if call == "qk_norm_rope":
+        a.Hq, a.Hkv, a.D = 2, 1, 64
+    else:
+        c = a.cache
+        c.pages = c.table = c.ctx_len = FAKE
+        c.n_pages, c.page_size, c.Hkv, c.D, c.R, c.table_width = 1, 16, 2, 64, 3, 4
+    for off in range(9):
+        assert getattr(ds.lib(), "dspark_" + call)(C.byref(a), FAKE + off, 256, None) == (1 if off % 4 else 0), off
