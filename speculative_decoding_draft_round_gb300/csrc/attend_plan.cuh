@@ -21,6 +21,9 @@ inline bool tiles_fit(const AttendParams& p, int MB, int tile)
     return rows < (1ll << 30) && (double)blocks * p.c.Hkv * (double)tiles < (double)kMostTiles;
 }
 
+// Tiles of `keys` tokens, which may be as many as an int counts
+__device__ __forceinline__ int tiles_of(int keys, int tile) { return (int)(((uint32_t)keys + tile - 1) / tile); }
+
 // The item that a run starts and does not end: its rows, and how many runs have parts of it (0: none).
 struct __align__(16) AttendTodo {
     int parts, slot;               // and the run's slot that holds the first
@@ -69,7 +72,7 @@ __device__ __forceinline__ RequestSpan<TILE> request_span(const AttendParams& p,
     }
     if (odd && report) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
     s.keys = s.n_q > 0 ? (int)keys : 0;
-    const int all = (s.keys + TILE - 1) / TILE;
+    const int all = tiles_of(s.keys, TILE);
     s.sink_tiles = s.lo_tile = 0;
     s.tiles = all;
     if (p.window > 0 && s.n_q > 0) {

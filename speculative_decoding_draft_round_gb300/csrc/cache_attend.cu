@@ -88,13 +88,13 @@ __global__ void __launch_bounds__(kWarps * 32) cache_attend_simt_kernel(AttendPa
 #pragma unroll
             for (int e = 0; e < kMaxE; ++e) o[row][e] = 0.f;
         }
-        for (int u0 = warp * 32; u0 < span; u0 += kWarps * 32) {
+        for (uint32_t u0 = warp * 32; u0 < (uint32_t)span; u0 += kWarps * 32) {   // may pass what an int holds
             // products of key u0 + lane
-            const int u = u0 + lane;
+            const uint32_t u = u0 + lane;
             const uint8_t* blk = nullptr;
             int slot = 0;
-            if (u < span) {
-                const int key = u < sinks ? u : from + u - sinks;
+            if (u < (uint32_t)span) {
+                const int key = (int)u < sinks ? (int)u : from + (int)u - sinks;
                 const int page = p.c.table[(size_t)r * p.c.table_width + key / P];
                 slot = key % P;
                 if (page >= 0 && page < p.c.n_pages) blk = cache_page_block(p.c, page, kvh, cb.bytes);

@@ -81,7 +81,7 @@ __device__ __forceinline__ BlockTiles block_tiles(const AttendParams& p, const R
     const int j0 = b * kMB / p.G, j1 = min((b + 1) * kMB - 1, q.n_rows - 1) / p.G;
     const int keys = (int)min((long long)q.keys, (long long)q.ctx + j1 + 1);
     BlockTiles t;
-    const int all = (keys + kTile - 1) / kTile;
+    const int all = tiles_of(keys, kTile);
     t.sink_tiles = t.lo_tile = 0;
     t.tiles = all;
     if (p.window > 0) {
