@@ -158,9 +158,14 @@ __device__ __forceinline__ void store_row(T* p, const float (&y)[8])
 // leave; in CTAs of eight 69
 constexpr int kVecWarps = 4, kVecCtas = 6;
 
-template <typename T, int LPH, bool kInter>
+// Which channels pair: half-split, neighbours, and neighbours with a rot that is no multiple of 8, so that a lane holds
+// pairs that are turned and pairs that are not. (With that test for all neighbours 32749 tokens took 1 us more.)
+enum Pairs { kHalves, kNeighbours, kMixed };
+
+template <typename T, int LPH, Pairs kPairs>
 __global__ void __launch_bounds__(kVecWarps * 32, kVecCtas) rope_vec_kernel(RopeParams p, int share)
 {
+    constexpr bool kInter = kPairs != kHalves;
     constexpr int kHeads = 32 / LPH;                      // heads of a warp's step
     constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
     pdl_enter();
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, kVecCtas) rope_vec_kernel(Rope
                     }
                     // channels that are not turned leave the others' alone: 0 times an infinity would be NaN
                     uint64_t r = mul2(x[i], a[i]);
-                    if (turned) r = fma2(o, b[i], r);
+                    if (kPairs == kMixed ? c0 + 2 * i < p.rot : turned) r = fma2(o, b[i], r);
                     unpack2(mul2(r, inv2), y[2 * i], y[2 * i + 1]);
                 }
                 if (on && h < heads) store_row<T>(y0 + (size_t)h * p.D, y);
@@ -283,7 +288,7 @@ bool vec_fits(const RopeParams& p)
            (strides * (int64_t)sizeof(T)) % 16 == 0;
 }
 
-template <typename T, bool kInter>
+template <typename T, Pairs kPairs>
 cudaError_t launch_lanes(const RopeParams& p, cudaStream_t s)
 {
     const int lph = p.D <= 32 ? 4 : p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
@@ -293,17 +298,18 @@ cudaError_t launch_lanes(const RopeParams& p, cudaStream_t s)
     while (share < kVecWarps && (long long)p.T * share < 16ll * num_sms() && share * (32 / lph) < p.Hq) share *= 2;
     const dim3 grid(cdiv(p.T, kVecWarps / share)), block(kVecWarps * 32);
     switch (lph) {
-    case 4: return launch_pdl(rope_vec_kernel<T, 4, kInter>, grid, block, 0, s, p, share);
-    case 8: return launch_pdl(rope_vec_kernel<T, 8, kInter>, grid, block, 0, s, p, share);
-    case 16: return launch_pdl(rope_vec_kernel<T, 16, kInter>, grid, block, 0, s, p, share);
-    default: return launch_pdl(rope_vec_kernel<T, 32, kInter>, grid, block, 0, s, p, share);
+    case 4: return launch_pdl(rope_vec_kernel<T, 4, kPairs>, grid, block, 0, s, p, share);
+    case 8: return launch_pdl(rope_vec_kernel<T, 8, kPairs>, grid, block, 0, s, p, share);
+    case 16: return launch_pdl(rope_vec_kernel<T, 16, kPairs>, grid, block, 0, s, p, share);
+    default: return launch_pdl(rope_vec_kernel<T, 32, kPairs>, grid, block, 0, s, p, share);
     }
 }
 
 template <typename T>
 cudaError_t launch_vec(const RopeParams& p, cudaStream_t s)
 {
-    return p.interleaved ? launch_lanes<T, true>(p, s) : launch_lanes<T, false>(p, s);
+    if (!p.interleaved) return launch_lanes<T, kHalves>(p, s);
+    return p.rot % 8 == 0 ? launch_lanes<T, kNeighbours>(p, s) : launch_lanes<T, kMixed>(p, s);
 }
 
 }  // namespace
