@@ -379,12 +379,13 @@ size_t dspark_cache_block_bytes(int32_t page_size, int32_t D);
 
 /*
  * dspark_qk_norm_rope -- for every token and every head of q and k (width D, fp32 statistics):
- *   y = x / sqrt(sum(x^2) / D + eps) * gain          (norm = 1; y = x for norm = 0)
+ *   y = x / sqrt(sum(x^2) / D + eps) * gain          (norm = 1; y = x * gain for norm = 0)
  *   with the angle phi_i = 2 pi * freq[i] * 2^-64 * position, for the pairs i < rot / 2
  *   (y_a, y_b) -> (y_a cos phi_i - y_b sin phi_i, y_a sin phi_i + y_b cos phi_i),
  *   (a, b) = (i, i + rot / 2), or (2i, 2i + 1) when interleaved; channels from rot on are not turned.
  * freq[i] is the turn of pair i per position as a 64-bit fraction of a whole turn, so that far
- * positions lose nothing: whole turns leave the product by integer arithmetic.
+ * positions lose nothing: whole turns leave the product by integer arithmetic. The sum is fp32: a
+ * head whose squares pass its range is not normed rightly.
  */
 typedef struct {
     uint32_t struct_size;
@@ -469,8 +470,9 @@ dspark_status dspark_cache_read(const dspark_cache_read_args* args, void* worksp
  * products as fp16 after a scaling by a power of two (exact for bf16 unless an element is 2^-25 of
  * the row's largest; two fp16 terms for fp32) and the weights exp(z - max) as fp16 (two terms for
  * fp32); elsewhere a CUDA-core kernel in fp32 runs.
- * Decreasing offsets or more than max_q rows of one request are recorded (DSPARK_ERR_DEVICE_INPUT):
- * that request's rows are not computed, or none past max_q; offsets that repeat so many rows that their
+ * Decreasing offsets, a negative context or more than max_q rows of one request are recorded
+ * (DSPARK_ERR_DEVICE_INPUT): that request's rows, or those past max_q, are not computed (they are zeros
+ * from the CUDA-core kernel and what they were from the others); offsets that repeat so many rows that their
  * blocks' tiles of keys pass 2^31 leave no row computed.
  * A workspace of more than 256 bytes has to be 16-byte aligned.
  */

@@ -23,7 +23,10 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t or_bits)
     return r;
 }
 
-// Constants of the conversion, kept in registers for a whole item: 1024 in both halves, 1032, 1/16, -72
+// Codes to fp16 by the old way of turning small integers into floating point: or them into the lowest bits of a power of
+// two whose last place is 1, and subtract it. fp16 has that at 1024, and a code 4 bits up in the word counts 16 there:
+//   (1024 + u) - (1024 + 8) = u - 8,   (1024 + 16 u) / 16 - (64 + 8) = u - 8,   exactly.
+// The constants, kept in registers for a whole item: 1024 in both halves, 1032, 1/16, -72.
 struct DequantConst {
     uint32_t magic, off, sixteenth, m72;
 };
@@ -68,8 +71,5 @@ __device__ __forceinline__ uint32_t below(int n)
 {
     return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
-
-// mask of a word's first n halves
-__device__ __forceinline__ uint32_t keep_halves(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u; }
 
 }  // namespace dspark

@@ -12,6 +12,7 @@
 // Instructions bound it (2 D fp32 products a row and key, and the codes turned again for every four heads of a query):
 // 1.1 ms for 128 single rows of 32 heads over up to 4096 tokens (0.05 ms of bytes), 6.7 ms for 17 rows a request. It
 // serves the head widths that the matrix kernels do not, and is what they are checked against.
+#include "attend_plan.cuh"
 #include "cache.cuh"
 #include "internal.h"
 
@@ -22,13 +23,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRows = 4;      // query heads that share a pass over the keys
 constexpr int kMaxE = 8;      // channels of a value row a lane holds (D <= 256)
-
-template <typename T>
-__device__ __forceinline__ void store_out(T* p, float x);
-template <>
-__device__ __forceinline__ void store_out<float>(float* p, float x) { *p = x; }
-template <>
-__device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) cache_attend_simt_kernel(AttendParams p)
@@ -181,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_attend_simt_kernel(AttendPa
             const bool none = top == -INFINITY;
             const float bad = s_bad[row] ? NAN : 0.f;
             const size_t at = (size_t)t * p.Hq + kvh * p.G + g0 + row;
-            store_out(static_cast<T*>(p.out) + at * D + c, (none ? 0.f : acc / sum) + bad);
+            store1(static_cast<T*>(p.out) + at * D + c, (none ? 0.f : acc / sum) + bad);
             if (c == 0 && p.lse) p.lse[at] = (none ? -INFINITY : (top + log2f(sum)) * kLn2) + bad;
             if (c == 0 && s_bad[row]) raise_status(p.status, DSPARK_ERR_NONFINITE_INPUT);
         }

@@ -19,16 +19,16 @@
 // loops, its MMAs land, and tensor memory is freed.
 //
 // Bound: prompts need 4 D flops for each row and key, 59 us at the tensor cores' rate for 2 x 2048 rows of 32 heads after
-// 650 tokens on average, and take 212; few rows need the cache's bytes once, 54 us for 128 requests of up to 17 rows
-// and 4096 tokens, and take 232 (28% tensor, 48% of the issue slots). A tile of few rows takes about 2700 cycles, whatever
-// the rows are: one group's weights take 2100 to 2400 of them (four loads of tensor memory for the maximum, four for the
-// weights, 330 cycles each, twice as long for the first because the loop's instructions have to come back), then its
-// products and the next S follow in 300. Items of few tiles add the way of the next item's q rows (7000 cycles after
-// its buffer is free, two buffers). Tried and slower: sixteen converting warps (64 registers a thread), weights in one
-// pass from scores kept apart from them, two threads a row (265 and 242 us: the fixed parts do not halve), the two groups
-// on alternate tiles of an item (297 and 259 us: with both at work the conversion takes 2800 cycles a tile, and one O has
-// to be read out between items), prefetches by the converting warps themselves, bulk prefetches (3 ms: they hold up the shared-memory fences), values transposed on
-// their way into shared memory (276 us).
+// 650 tokens on average, and take 212; after 2000 tokens 108, and take 270 to 300. Few rows need the cache's bytes once,
+// 54 us for 128 requests of up to 17 rows and 4096 tokens, and take 231 (28% tensor, 48% of the issue slots). A tile of
+// few rows takes about 2700 cycles, whatever the rows are: one group's weights take 2100 to 2400 of them (four loads of
+// tensor memory for the maximum, four for the weights, 330 cycles each, twice as long for the first because the loop's
+// instructions have to come back), then its products and the next S follow in 300. Items of few tiles add the way of the
+// next item's q rows (7000 cycles after its buffer is free, two buffers). Tried and slower: sixteen converting warps (64
+// registers a thread), weights in one pass from scores kept apart from them, two threads a row (265 and 242 us: the fixed
+// parts do not halve), the two groups on alternate tiles of an item (297 and 259 us: with both at work the conversion takes
+// 2800 cycles a tile, and one O has to be read out between items), prefetches by the converting warps themselves, bulk
+// prefetches (3 ms: they hold up the shared-memory fences), values transposed on their way into shared memory (276 us).
 #include <algorithm>
 
 #include "attend_convert.cuh"
@@ -906,7 +906,8 @@ bool attend_tc_supported(const AttendParams& p)
     // 232 us here and 198 there, 48 rows 234 and 231, 64 rows 234 and 283, 128 rows 245 and 469; 8 requests of up to
     // 8192: 48 rows 47 and 46, 64 rows 48 and 58. Where a row reaches few keys the warp kernel holds out longer: 32
     // requests of up to 2048 tokens, 48 rows 61 and 52, 68 rows 62 and 58, 128 rows 68 and 85; a window of 512 keys, 48
-    // rows 75 and 50, 68 rows 78 and 59, 128 rows 84 and 94.
+    // rows 75 and 50, 68 rows 78 and 59, 128 rows 84 and 94. The lengths are on the device, so what a row can reach goes by
+    // the table's width: requests far shorter than their tables take this kernel where the other would be quicker.
     const long long rows = (long long)p.max_q * p.G, room = (long long)p.c.table_width * p.c.page_size;
     const long long reach = p.window > 0 ? std::min(room, (long long)p.window + p.sinks) : room;
     if (rows <= (reach <= 18 * kTile ? 80 : 48)) return false;

@@ -9,10 +9,11 @@
 //
 // The bytes bound it: each row read once and written once. rope_vec_kernel keeps 16-byte pieces in registers
 // between the norm's sum and the rotation, with several heads' loads in flight; rope_any_kernel takes the
-// shapes that the pieces do not fit. Measured: 32749 tokens of 40 heads of 128 in bf16 (671 MB) 114 us, 99 us at the
-// copy's rate (148 us while a condition around each load made it wait for the one before); 2176 such tokens 13 us of 6.6,
-// where the chain position, context, sines, rows is what is left; 16384 with half-split pairs 67 us of 49, the
-// shuffles that bring a pair's other half.
+// shapes that the pieces do not fit. The first takes rsqrtf (2 units in the last place: listed fp32 rows are off by
+// 7.8e-8 of their size against 64 bits, by 7.0e-8 in plain fp32), the second divides by a root. Measured: 32749 tokens
+// of 40 heads of 128 in bf16 (671 MB) 114 us, 99 us at the copy's rate (148 us while a condition around each load made
+// it wait for the one before); 2176 such tokens 13 us of 6.6, where the chain position, context, sines, rows is what is
+// left; 16384 with half-split pairs 67 us of 49, the shuffles that bring a pair's other half.
 #include "common.cuh"
 #include "internal.h"
 
