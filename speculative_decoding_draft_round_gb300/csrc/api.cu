@@ -236,8 +236,8 @@ dspark_status check_rope(const dspark_qk_norm_rope_args* a)
     if ((a->norm | 1) != 1 || (a->interleaved | 1) != 1 || a->reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
     if (!(a->eps >= 0.f) || a->eps > FLT_MAX) return DSPARK_ERR_INVALID_ARGUMENT;
     if (a->request && a->R < 1) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T == 0) return DSPARK_OK;   // an empty tensor may have no address
     if (a->ctx_len && !a->request) return DSPARK_ERR_INVALID_ARGUMENT;
-    if (a->T == 0) return DSPARK_OK;
     if (!a->q || !a->k || !a->q_out || !a->k_out || !a->position || (a->rot > 0 && !a->freq))
         return DSPARK_ERR_INVALID_ARGUMENT;
     return DSPARK_OK;

@@ -90,8 +90,8 @@ class VerifyPass:
 
     def prompt(self, l, qkv, request, position, offsets, max_q, stream=None):
         """The same for the rows of prompts: qkv [T][(Hq + 2 Hkv) D] of any T, laid out as request, position [T] and
-        offsets [R + 1] (int32, on the device), at most max_q rows a request. A prompt that comes in pieces is
-        moved on with advance_by between them."""
+        offsets [R + 1] (int32, on the device), at most max_q rows a request (0 where none has a row). A prompt that
+        comes in pieces is moved on with advance_by between them."""
         q, k, v = self._heads(qkv)
         turned = qk_norm_rope(q, k, position=position, request=request, workspace=self.ws, stream=stream,
                               **self._rope[l])
@@ -99,7 +99,7 @@ class VerifyPass:
                      stream=stream)
         with _on(stream):
             a, out = cache_attend_args(turned["q"], self.pools[l], self.table, offsets, self.ctx_len, window=self.window,
-                                       sinks=self.sinks, max_q=max_q, lse=False)
+                                       sinks=self.sinks, max_q=max(1, max_q), lse=False)
             ws = self._prompt_workspace(a)
             _launch("dspark_cache_attend", lib().dspark_cache_attend, a, ws, None)
             if torch.cuda.is_current_stream_capturing():

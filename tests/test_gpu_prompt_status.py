@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 
 import speculative_decoding_draft_round_gb300 as ds
 import test_gpu_layer as layer
-from speculative_decoding_draft_round_gb300.verify_pass import VerifyPass
+from speculative_decoding_draft_round_gb300.verify_pass import ToyTarget, VerifyPass
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -86,3 +86,14 @@ def test_status_of_a_captured_prompt():
     rows = np.r_[100:109]                            # of the request whose rows are as they were
     for o in out:
         assert torch.equal(o[rows], want[rows])
+
+
+def test_a_prompt_of_no_rows():
+    """Requests that start with nothing: no row a request, alone or as a model's prompt."""
+    vp, qkv, _ = _prompt([3, 1])
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out = vp.prompt(0, qkv[:0], none, none, torch.zeros(3, dtype=torch.int32, device=DEV), 0)
+    assert out.shape == (0, 8, 64) and vp.check() == 0
+    target = ToyTarget(vp, 50, 32)
+    target.prompt(none, [0, 0])
+    assert vp.check() == 0 and vp.ctx_len.tolist() == [0, 0]

@@ -77,3 +77,11 @@ def test_status_words_off_their_boundaries_are_refused(run, call, args):
         c.n_pages, c.page_size, c.Hkv, c.D, c.R, c.table_width = 1, 16, 2, 64, 3, 4
     for off in range(9):
         assert getattr(ds.lib(), "dspark_" + call)(C.byref(a), FAKE + off, 256, None) == (1 if off % 4 else 0), off
+
+
+def test_empty_batches_need_no_pointers(run):
+    """An empty tensor's address is 0."""
+    a = ds.QkNormRopeArgs()
+    a.struct_size = C.sizeof(a)
+    a.Hq, a.Hkv, a.D, a.rot, a.R, a.ctx_len, a.freq = 2, 1, 64, 64, 3, FAKE, FAKE
+    assert ds.lib().dspark_qk_norm_rope(C.byref(a), FAKE, 256, None) == 0
