@@ -500,6 +500,154 @@ dspark_status dspark_cache_attend(const dspark_cache_attend_args* args, void* wo
                                   void* stream);
 
 /*
+ * The rest of the target's pass (no counterpart in the paper, which takes the target's logits as given): the norms and
+ * 8-bit projections around the attention, and what stands between the target's logits and dspark_verify.
+ *
+ * dspark_add_norm_quant -- for every row t of x [T][N]:
+ *   s = x + residual, rounded to the rows' type (s = x without a residual; written to sum where given)
+ *   p = s * gain;   y = p / sqrt(sum(s^2) / N + eps)   (norm = 1; y = p for norm = 0)
+ *   scale = max|y| / 127;   code = 127 p / max|p| rounded to nearest, ties to even
+ * codes and scale, y, or both are written. A code does not depend on the norm's rounding: it is the nearest one of the
+ * exact quotient (formed in 64 bits where fp32 leaves it open). Sums are fp32, and 64 bits for rows whose squares or
+ * products leave its range. A row of zeros has scale 0 and codes 0. A row whose p holds a NaN or an infinity has scale
+ * NaN and codes 0, y as the formula gives it, and DSPARK_ERR_NONFINITE_INPUT is recorded; other rows are not touched by it.
+ * norm = 0 without gain and residual quantises plain rows, weights [N][K] for dspark_linear_i8 among them.
+ * sum and y may be x's or the residual's own rows (same address and stride), but not the same rows as each other.
+ * n_rows (NULL: T), on the device: only the first *n_rows rows are computed, the others of every output stay as they
+ * were (offsets + R of dspark_assemble); outside 0 .. T it is clamped and DSPARK_ERR_DEVICE_INPUT recorded.
+ */
+typedef struct {
+    uint32_t struct_size;
+    int32_t T;                 /* rows, >= 0 */
+    int32_t N;                 /* row width, 1 .. 32768 */
+    int32_t dtype;             /* element type of x, residual, sum and y */
+    int32_t norm;              /* 1: root-mean-square norm, 0: none */
+    float eps;                 /* >= 0 */
+    const void* x;             /* [T][N], the last axis contiguous */
+    const void* residual;      /* [T][N] or NULL */
+    int64_t x_stride, residual_stride, sum_stride, y_stride, codes_stride;   /* of rows, in elements */
+    const float* gain;         /* [N] or NULL = 1 */
+    const int32_t* n_rows;     /* [1] or NULL */
+    void* sum;                 /* out [T][N] or NULL (needs residual) */
+    void* y;                   /* out [T][N] or NULL */
+    int8_t* codes;             /* out [T][N] or NULL; with scale */
+    float* scale;              /* out [T] */
+} dspark_add_norm_quant_args;
+
+dspark_status dspark_add_norm_quant_workspace_size(const dspark_add_norm_quant_args* args, size_t* bytes);
+dspark_status dspark_add_norm_quant(const dspark_add_norm_quant_args* args, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * dspark_linear_i8 -- rows of 8-bit codes times weights in 8 bits, with a scale for each row and each channel:
+ *   out[out_row[t]][n] = (sum_k x[t][k] w[n][k]) * x_scale[t] * w_scale[n] + bias[n]
+ * The sum is formed from whole numbers in fp32 (32-bit integers on the CUDA-core path): exact while the partial sums
+ * stay below 2^24 in magnitude, and off by at most 2^-23 of the largest of them for each 16 further products.
+ * out_row (NULL: row t) scatters the rows, for instance a verify batch's into [R][gamma_max + 1][V]; rows with
+ * out_row < 0 are not written, and neither are those with out_row >= out_rows (DSPARK_ERR_DEVICE_INPUT recorded). Two
+ * rows must not share a place. n_rows as in dspark_add_norm_quant.
+ * Weights off 16-byte boundaries (address or row stride) are laid out anew in the workspace by every call.
+ * A workspace of more than 256 bytes has to be 16-byte aligned.
+ */
+typedef struct {
+    uint32_t struct_size;
+    int32_t T;                 /* rows of x, >= 0 */
+    int32_t K;                 /* 1 .. 131071 */
+    int32_t N;                 /* output channels, 1 .. 2^24 */
+    int32_t dtype;             /* element type of out */
+    int32_t path;              /* DSPARK_PATH_AUTO, _CUDA_CORE or _TENSOR_CORE */
+    int32_t out_rows;          /* rows of out; >= T without out_row */
+    int32_t reserved;          /* 0 */
+    const int8_t* x;           /* [T][K], the last axis contiguous */
+    const float* x_scale;      /* [T] */
+    const int8_t* w;           /* [N][K], the last axis contiguous */
+    const float* w_scale;      /* [N] */
+    const float* bias;         /* [N] or NULL */
+    const int32_t* out_row;    /* [T] or NULL */
+    const int32_t* n_rows;     /* [1] or NULL */
+    void* out;                 /* out [out_rows][N], the last axis contiguous */
+    int64_t x_stride, w_stride, out_stride;   /* of rows, in elements */
+} dspark_linear_i8_args;
+
+dspark_status dspark_linear_i8_workspace_size(const dspark_linear_i8_args* args, size_t* bytes);
+dspark_status dspark_linear_i8(const dspark_linear_i8_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dspark_seen_add -- the table of tokens that the requests have seen, which the penalties of dspark_adjust_logits read:
+ * seen [R][seen_stride], one 16-bit word for each token id: bit 15 set for a token of the prompt, the low 15 bits the
+ * number of times it has been put out (32767 at most). For every request r, rows of zeros first where fresh[r] != 0, the
+ * tokens tokens[r][0 .. n[r] - 1] and extra[r] are added: to the counts, or with prompt = 1 by setting bit 15. After
+ * dspark_verify: tokens with n = accepted and extra = next_token. A token outside 0 .. V-1 or n[r] outside 0 .. W is
+ * recorded (DSPARK_ERR_DEVICE_INPUT) and skipped, or clamped. Words from V to seen_stride are zeroed with a fresh row and
+ * otherwise left as they are.
+ */
+typedef struct {
+    uint32_t struct_size;
+    int32_t R;                 /* requests, 1 .. DSPARK_MAX_SLOTS */
+    int32_t W;                 /* tokens a row, >= 0 */
+    int32_t V;                 /* vocabulary, 1 .. 2^24 */
+    int32_t prompt;            /* 1: tokens of the prompt, 0: tokens put out */
+    int32_t reserved;          /* 0 */
+    int64_t seen_stride;       /* of rows, in words: a multiple of 8, >= V */
+    int64_t tokens_stride;     /* of rows, in elements */
+    int16_t* seen;             /* in and out, 16-byte aligned */
+    const int32_t* tokens;     /* [R][W] (NULL with W = 0) */
+    const int32_t* n;          /* [R] or NULL: W */
+    const int32_t* extra;      /* [R] or NULL */
+    const uint8_t* fresh;      /* [R] or NULL: none */
+} dspark_seen_add_args;
+
+dspark_status dspark_seen_add_workspace_size(const dspark_seen_add_args* args, size_t* bytes);
+dspark_status dspark_seen_add(const dspark_seen_add_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dspark_adjust_logits -- penalties, biases and grammar masks on the logits of rows (r, j), j < S: the target's rows
+ * before dspark_verify (S = gamma_max + 1; row j follows the drafted tokens tokens[r][0 .. j-1], which count as put out),
+ * or the backbone's U before dspark_sample_block (S = gamma_max, no tokens). In fp32, rounded once:
+ *   n = count of v in seen[r] and in tokens[r][0 .. j-1]
+ *   z = z > 0 ? z / repetition[r] : z * repetition[r]    where n > 0 or v is in the prompt
+ *   z = z - frequency[r] n - presence[r] [n > 0] + the biases of v
+ *   z = -infinity                                        where v's bit of the row's mask is 0
+ * Biases: entries bias_offsets[r] .. bias_offsets[r+1]-1 of bias_token and bias_value; entries of one token add up in
+ * their order. Mask rows: mask_row[r][j] < 0 allows all. Bit v % 32 of word v / 32 allows token v. What a mask hides is
+ * never looked at; other infinities and NaN pass through. Rows j > keep[r] are not read, and stay as they were in out.
+ * out may be logits (in place: what does not change is not written) but must not overlap it otherwise.
+ * Recorded (DSPARK_ERR_DEVICE_INPUT): a repetition that is not above zero and finite (1 is taken), a penalty that is
+ * not finite (0 is taken), keep outside 0 .. S-1 (clamped), bias offsets that decrease or pass n_bias (no biases), a
+ * token id not below V or a bias' token outside 0 .. V-1 (skipped; tokens < 0 are skipped silently), mask_row >= n_masks
+ * (all allowed).
+ */
+typedef struct {
+    uint32_t struct_size;
+    int32_t R;                 /* requests, 1 .. DSPARK_MAX_SLOTS */
+    int32_t S;                 /* rows a request, 1 .. DSPARK_MAX_GAMMA + 1 */
+    int32_t V;                 /* vocabulary, 1 .. 2^24 */
+    int32_t dtype;             /* element type of logits and out */
+    int32_t n_masks;           /* rows of mask */
+    int32_t n_bias;            /* entries of bias_token and bias_value */
+    int32_t reserved;          /* 0 */
+    const void* logits;        /* [R][S][V] */
+    void* out;                 /* out [R][S][V] */
+    const int16_t* seen;       /* [R][seen_stride] of dspark_seen_add, 16-byte aligned, or NULL: nothing seen */
+    int64_t seen_stride;       /* a multiple of 8, >= V */
+    const float* repetition;   /* [R] or NULL = 1 */
+    const float* presence;     /* [R] or NULL = 0 */
+    const float* frequency;    /* [R] or NULL = 0 */
+    const int32_t* tokens;     /* [R][S - 1] or NULL */
+    const int32_t* bias_offsets;   /* [R + 1] or NULL */
+    const int32_t* bias_token;     /* [n_bias] */
+    const float* bias_value;       /* [n_bias] */
+    const uint32_t* mask;      /* [n_masks][mask_stride] or NULL */
+    int64_t mask_stride;       /* words, >= ceil(V / 32) */
+    const int32_t* mask_row;   /* [R][S]; NULL with a mask: row r * S + j (n_masks >= R * S) */
+    const int32_t* keep;       /* [R] or NULL = S - 1 */
+} dspark_adjust_logits_args;
+
+dspark_status dspark_adjust_logits_workspace_size(const dspark_adjust_logits_args* args, size_t* bytes);
+dspark_status dspark_adjust_logits(const dspark_adjust_logits_args* args, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
  * Launch accounting and timing (measurement support, not part of the method).
  *
  * dspark_launch_count: number of kernels this library has launched in this
@@ -530,7 +678,12 @@ enum {
     DSPARK_KERNEL_CACHE_APPEND = 13,
     DSPARK_KERNEL_CACHE_READ = 14,
     DSPARK_KERNEL_CACHE_ATTEND = 15,
-    DSPARK_KERNEL_CACHE_MERGE = 16   /* joins the parts of rows whose keys were split over CTAs */
+    DSPARK_KERNEL_CACHE_MERGE = 16,  /* joins the parts of rows whose keys were split over CTAs */
+    DSPARK_KERNEL_ADD_NORM_QUANT = 17,
+    DSPARK_KERNEL_LINEAR_LAYOUT = 18,  /* codes to 16 bits (and weights to 16-byte rows) for the tensor cores */
+    DSPARK_KERNEL_LINEAR_I8 = 19,
+    DSPARK_KERNEL_SEEN_ADD = 20,
+    DSPARK_KERNEL_ADJUST_LOGITS = 21
 };
 
 typedef struct {

@@ -16,6 +16,10 @@ and, for the target layers that stream runs through (verify_pass.py puts them to
   cache_append  key and value rows into a paged cache of 4-bit codes
   cache_read    cached rows back as values
   cache_attend  attention over that cache, with an optional sliding window and first tokens
+  add_norm_quant  residual sum, root-mean-square norm and 8-bit codes of rows
+  linear_i8     8-bit rows times 8-bit weights, a scale for each row and channel
+  seen_add      the table of tokens the requests have seen
+  adjust_logits penalties for those, biases and grammar masks on logits
 """
 from __future__ import annotations
 
@@ -134,6 +138,43 @@ class CacheAttendArgs(C.Structure):
     ]
 
 
+class AddNormQuantArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("T", C.c_int32), ("N", C.c_int32), ("dtype", C.c_int32), ("norm", C.c_int32),
+        ("eps", C.c_float), ("x", _vp), ("residual", _vp),
+        ("x_stride", C.c_int64), ("residual_stride", C.c_int64), ("sum_stride", C.c_int64), ("y_stride", C.c_int64),
+        ("codes_stride", C.c_int64), ("gain", _vp), ("n_rows", _vp), ("sum", _vp), ("y", _vp), ("codes", _vp),
+        ("scale", _vp),
+    ]
+
+
+class LinearI8Args(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("T", C.c_int32), ("K", C.c_int32), ("N", C.c_int32), ("dtype", C.c_int32),
+        ("path", C.c_int32), ("out_rows", C.c_int32), ("reserved", C.c_int32), ("x", _vp), ("x_scale", _vp),
+        ("w", _vp), ("w_scale", _vp), ("bias", _vp), ("out_row", _vp), ("n_rows", _vp), ("out", _vp),
+        ("x_stride", C.c_int64), ("w_stride", C.c_int64), ("out_stride", C.c_int64),
+    ]
+
+
+class SeenAddArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("R", C.c_int32), ("W", C.c_int32), ("V", C.c_int32), ("prompt", C.c_int32),
+        ("reserved", C.c_int32), ("seen_stride", C.c_int64), ("tokens_stride", C.c_int64), ("seen", _vp),
+        ("tokens", _vp), ("n", _vp), ("extra", _vp), ("fresh", _vp),
+    ]
+
+
+class AdjustLogitsArgs(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("R", C.c_int32), ("S", C.c_int32), ("V", C.c_int32), ("dtype", C.c_int32),
+        ("n_masks", C.c_int32), ("n_bias", C.c_int32), ("reserved", C.c_int32), ("logits", _vp), ("out", _vp),
+        ("seen", _vp), ("seen_stride", C.c_int64), ("repetition", _vp), ("presence", _vp), ("frequency", _vp),
+        ("tokens", _vp), ("bias_offsets", _vp), ("bias_token", _vp), ("bias_value", _vp), ("mask", _vp),
+        ("mask_stride", C.c_int64), ("mask_row", _vp), ("keep", _vp),
+    ]
+
+
 EXPORTS = ("dspark_sample_workspace_size", "dspark_sample_block", "dspark_schedule_workspace_size",
            "dspark_schedule", "dspark_verify_workspace_size", "dspark_verify", "dspark_check",
            "dspark_status_string", "dspark_abi_version", "dspark_launch_count", "dspark_time_kernel",
@@ -143,12 +184,17 @@ EXPORTS = ("dspark_sample_workspace_size", "dspark_sample_block", "dspark_schedu
            "dspark_qk_norm_rope_workspace_size", "dspark_qk_norm_rope",
            "dspark_cache_append_workspace_size", "dspark_cache_append",
            "dspark_cache_read_workspace_size", "dspark_cache_read",
-           "dspark_cache_attend_workspace_size", "dspark_cache_attend")
+           "dspark_cache_attend_workspace_size", "dspark_cache_attend",
+           "dspark_add_norm_quant_workspace_size", "dspark_add_norm_quant",
+           "dspark_linear_i8_workspace_size", "dspark_linear_i8",
+           "dspark_seen_add_workspace_size", "dspark_seen_add",
+           "dspark_adjust_logits_workspace_size", "dspark_adjust_logits")
 
 KERNELS = {"draft_setup": 0, "draft_stats": 1, "draft_commit": 2, "schedule": 3, "verify_rows": 4,
            "verify_decide": 5, "residual_stats": 6, "residual_pick": 7, "assemble": 8, "rnn_step": 9,
            "rnn_hidden": 10, "draft_loop": 11, "qk_norm_rope": 12, "cache_append": 13, "cache_read": 14,
-           "cache_attend": 15, "cache_merge": 16}
+           "cache_attend": 15, "cache_merge": 16, "add_norm_quant": 17, "linear_layout": 18, "linear_i8": 19,
+           "seen_add": 20, "adjust_logits": 21}
 
 
 class EventPair(C.Structure):
@@ -192,6 +238,16 @@ def lib():
                            ("dspark_cache_attend_workspace_size",
                             [C.POINTER(CacheAttendArgs), C.POINTER(C.c_size_t)]),
                            ("dspark_cache_attend", [C.POINTER(CacheAttendArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_add_norm_quant_workspace_size",
+                            [C.POINTER(AddNormQuantArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_add_norm_quant", [C.POINTER(AddNormQuantArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_linear_i8_workspace_size", [C.POINTER(LinearI8Args), C.POINTER(C.c_size_t)]),
+                           ("dspark_linear_i8", [C.POINTER(LinearI8Args), _vp, C.c_size_t, _vp]),
+                           ("dspark_seen_add_workspace_size", [C.POINTER(SeenAddArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_seen_add", [C.POINTER(SeenAddArgs), _vp, C.c_size_t, _vp]),
+                           ("dspark_adjust_logits_workspace_size",
+                            [C.POINTER(AdjustLogitsArgs), C.POINTER(C.c_size_t)]),
+                           ("dspark_adjust_logits", [C.POINTER(AdjustLogitsArgs), _vp, C.c_size_t, _vp]),
                            ("dspark_check", [_vp, _vp])):
             f = getattr(L, name)
             f.argtypes = argt
@@ -770,6 +826,221 @@ def cache_attend(q, pool, table, offsets, ctx_len, *, scale=None, window=0, sink
         workspace = torch.zeros(workspace_bytes("cache_attend", a), dtype=torch.uint8, device=q.device)
     _launch("dspark_cache_attend", lib().dspark_cache_attend, a, workspace, stream)
     out["workspace"] = workspace
+    return out
+
+
+# ----------------------------------------------------------------- the rest of the target's pass
+
+_i8 = torch.int8
+
+
+def _rows2(t, name, dtype, shape):
+    """Rows [T][N] whose last axis is contiguous; returns (pointer, row stride)."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    st = t.stride()
+    if st[1] != 1 and shape[1] > 1:
+        raise ValueError("the last axis of %s must be contiguous" % name)
+    return t.data_ptr(), st[0]
+
+
+def add_norm_quant_args(x, *, residual=None, gain=None, eps=1e-6, norm=True, codes=True, values=False, n_rows=None,
+                        out=None):
+    if not isinstance(x, _Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError("x must have shape [rows][width], got %s" % (tuple(x.shape),))
+    shape, dt, dev = x.shape, x.dtype, x.device
+    T, N = shape
+    xp, x_rs = _rows2(x, "x", dt, shape)
+    rp, r_rs = (None, 0) if residual is None else _rows2(residual, "residual", dt, shape)
+    if out is None:
+        out = {}
+        if codes:
+            out["codes"] = torch.empty(shape, dtype=_i8, device=dev)
+            out["scale"] = torch.empty(T, dtype=_f32, device=dev)
+        if values:
+            out["y"] = torch.empty(shape, dtype=dt, device=dev)
+        if residual is not None:
+            out["sum"] = torch.empty(shape, dtype=dt, device=dev)
+    if codes and ("codes" not in out or "scale" not in out) or values and "y" not in out:
+        raise ValueError("out must hold what is asked for: codes and scale, or y")
+    cp, c_rs = _rows2(out["codes"], "out codes", _i8, shape) if codes else (None, 0)
+    yp, y_rs = _rows2(out["y"], "out y", dt, shape) if values else (None, 0)
+    s = out.get("sum")
+    sp, s_rs = (None, 0) if s is None else _rows2(s, "out sum", dt, shape)
+    a = AddNormQuantArgs(C.sizeof(AddNormQuantArgs), T, N, _dtype_code(x), 1 if norm else 0, eps, xp, rp, x_rs, r_rs,
+                         s_rs, y_rs, c_rs, None if gain is None else _need(gain, "gain", _f32, (N,)),
+                         None if n_rows is None else _need(n_rows, "n_rows", _i32, (1,)), sp, yp, cp,
+                         _need(out["scale"], "out scale", _f32, (T,)) if codes else None)
+    return a, out
+
+
+def add_norm_quant(x, *, residual=None, gain=None, eps=1e-6, norm=True, codes=True, values=False, n_rows=None, out=None,
+                   workspace=None, stream=None):
+    """dspark_add_norm_quant: rows x [T][N] (the last axis contiguous), a residual added, normed and quantised;
+    returns {"codes" int8 [T][N], "scale" fp32 [T]} with codes, {"y"} in x's type with values, and the rounded {"sum"}
+    with a residual (out may give the residual itself for it, or leave it out). n_rows: int32 [1] on the device, the
+    rows that are computed. norm=False without gain quantises plain rows, weights for linear_i8 among them."""
+    if out is None and stream is not None:
+        with _on(stream):
+            a, out = add_norm_quant_args(x, residual=residual, gain=gain, eps=eps, norm=norm, codes=codes, values=values,
+                                         n_rows=n_rows)
+    else:
+        a, out = add_norm_quant_args(x, residual=residual, gain=gain, eps=eps, norm=norm, codes=codes, values=values,
+                                     n_rows=n_rows, out=out)
+    ws = _status_workspace(workspace, x.device, stream)
+    _launch("dspark_add_norm_quant", lib().dspark_add_norm_quant, a, ws, stream)
+    out["workspace"] = ws
+    return out
+
+
+def linear_i8_args(x, x_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, out_row=None, n_rows=None, path=PATH_AUTO,
+                   out=None):
+    for t, name in ((x, "x"), (w, "w")):
+        if not isinstance(t, _Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.dim() != 2:
+            raise ValueError("%s must have shape [rows][width], got %s" % (name, tuple(t.shape)))
+    T, K = x.shape
+    N = w.shape[0]
+    xp, x_rs = _rows2(x, "x", _i8, (T, K))
+    wp, w_rs = _rows2(w, "w", _i8, (N, K))
+    if out is None:
+        if out_row is not None:
+            raise ValueError("out_row needs out, whose rows it names")
+        out = {"out": torch.empty((T, N), dtype=dtype, device=x.device)}
+    o = out["out"]
+    if isinstance(o, _Tensor) and o.dim() > 2:
+        _dev(o, "out")
+        o = o.view(-1, o.shape[-1])
+    if not isinstance(o, _Tensor) or o.dim() != 2 or out_row is None and o.shape[0] != T:
+        raise ValueError("out must be a tensor of rows of %d channels, one for each row of x without out_row" % N)
+    op, o_rs = _rows2(o, "out", o.dtype, (o.shape[0], N))
+    a = LinearI8Args(C.sizeof(LinearI8Args), T, K, N, _dtype_code(o), path, o.shape[0], 0, xp,
+                     _need(x_scale, "x_scale", _f32, (T,)), wp, _need(w_scale, "w_scale", _f32, (N,)),
+                     None if bias is None else _need(bias, "bias", _f32, (N,)),
+                     None if out_row is None else _need(out_row, "out_row", _i32, (T,)),
+                     None if n_rows is None else _need(n_rows, "n_rows", _i32, (1,)), op, x_rs, w_rs, o_rs)
+    return a, out
+
+
+def linear_i8(x, x_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, out_row=None, n_rows=None, path=PATH_AUTO,
+              out=None, workspace=None, stream=None):
+    """dspark_linear_i8: codes x [T][K] with x_scale [T] times weights w [N][K] with w_scale [N] (add_norm_quant makes
+    both); returns {"out"} [T][N] of dtype. out gives another place: {"out": rows of N channels, their last axis
+    contiguous, or a contiguous tensor of more axes}, its own type counts then; with out_row [T] (int32) row t goes to its
+    row out_row[t], nowhere where that is negative. n_rows: int32 [1] on the device, the rows that are computed."""
+    if stream is not None and (out is None or workspace is None):
+        with _on(stream):
+            return linear_i8(x, x_scale, w, w_scale, bias=bias, dtype=dtype, out_row=out_row, n_rows=n_rows, path=path,
+                             out=out, workspace=workspace)
+    a, out = linear_i8_args(x, x_scale, w, w_scale, bias=bias, dtype=dtype, out_row=out_row, n_rows=n_rows, path=path,
+                            out=out)
+    if workspace is None:
+        # only its status word has to start at zero
+        workspace = torch.empty(workspace_bytes("linear_i8", a), dtype=_u8, device=x.device)
+        workspace[:256].zero_()
+    _launch("dspark_linear_i8", lib().dspark_linear_i8, a, workspace, stream)
+    out["workspace"] = workspace
+    return out
+
+
+def seen_table(R, V, *, device="cuda"):
+    """The table of what R requests have seen of V tokens: int16 [R][V rounded up to 8], bit 15 for the prompt's tokens,
+    the low 15 bits the times a token has been put out."""
+    return torch.zeros((R, -(-V // 8) * 8), dtype=torch.int16, device=device)
+
+
+def seen_add_args(seen, tokens, *, V, n=None, extra=None, fresh=None, prompt=False):
+    if not isinstance(seen, _Tensor) or seen.dim() != 2:
+        raise TypeError("seen must be a CUDA tensor [requests][words]")
+    R = seen.shape[0]
+    sp, s_rs = _rows2(seen, "seen", torch.int16, seen.shape)
+    if not 0 < V <= seen.shape[1]:
+        raise ValueError("V is %d, seen has %d words a request" % (V, seen.shape[1]))
+    W, tp, t_rs = 0, None, 0
+    if tokens is not None:
+        W = tokens.shape[1] if tokens.dim() == 2 else 0
+        tp, t_rs = _rows2(tokens, "tokens", _i32, (R, W))
+    return SeenAddArgs(C.sizeof(SeenAddArgs), R, W, V, 1 if prompt else 0, 0, s_rs, t_rs, sp, tp,
+                       None if n is None else _need(n, "n", _i32, (R,)),
+                       None if extra is None else _need(extra, "extra", _i32, (R,)),
+                       None if fresh is None else _need(fresh, "fresh", _u8, (R,)))
+
+
+def seen_add(seen, tokens, *, V, n=None, extra=None, fresh=None, prompt=False, workspace=None, stream=None):
+    """dspark_seen_add: the first n[r] (int32 [R], all without it) of tokens[r] ([R][W] int32 or None) and extra[r] (int32
+    [R]) into the rows of seen (seen_table), as put out or as the prompt's; rows with fresh[r] (uint8 [R]) are cleared
+    first. After verify: seen_add(seen, tokens, V=V, n=accepted, extra=next_token). Returns {"workspace"}."""
+    a = seen_add_args(seen, tokens, V=V, n=n, extra=extra, fresh=fresh, prompt=prompt)
+    ws = _status_workspace(workspace, seen.device, stream)
+    _launch("dspark_seen_add", lib().dspark_seen_add, a, ws, stream)
+    return {"workspace": ws}
+
+
+def adjust_logits_args(logits, *, seen=None, repetition=None, presence=None, frequency=None, tokens=None,
+                       bias_offsets=None, bias_token=None, bias_value=None, mask=None, mask_row=None, keep=None, out=None):
+    _dev(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must have shape [requests][rows][vocabulary], got %s" % (tuple(logits.shape),))
+    shape = R, S, V = logits.shape
+    if out is None:
+        out = {"out": torch.empty_like(logits)}
+    one = lambda t, name, dtype: None if t is None else _need(t, name, dtype, (R,))
+    sp, s_rs = (None, 0)
+    if seen is not None:
+        sp, s_rs = _rows2(seen, "seen", torch.int16, (R, seen.shape[1] if seen.dim() == 2 else 0))
+        if seen.shape[1] < V:
+            raise ValueError("seen has %d words a request, the logits %d" % (seen.shape[1], V))
+    n_bias = 0
+    if bias_offsets is not None:
+        if bias_token is None or bias_value is None:
+            raise ValueError("bias_offsets needs bias_token and bias_value")
+        n_bias = bias_token.numel()
+    mp, m_rs, n_masks = None, 0, 0
+    if mask is not None:
+        if not isinstance(mask, _Tensor) or mask.dim() != 2:
+            raise ValueError("mask must have shape [masks][words]")
+        mp, m_rs = _rows2(mask, "mask", _i32, mask.shape)
+        n_masks = mask.shape[0]
+        if mask.shape[1] < -(-V // 32):
+            raise ValueError("mask has %d words a row, %d tokens need %d" % (mask.shape[1], V, -(-V // 32)))
+        m_rs = mask.shape[1] if n_masks == 1 else m_rs
+    elif mask_row is not None:
+        raise ValueError("mask_row needs mask")
+    a = AdjustLogitsArgs(C.sizeof(AdjustLogitsArgs), R, S, V, _dtype_code(logits), n_masks, n_bias, 0, _ptr(logits),
+                         _need(out["out"], "out", logits.dtype, shape), sp, s_rs, one(repetition, "repetition", _f32),
+                         one(presence, "presence", _f32), one(frequency, "frequency", _f32),
+                         None if tokens is None else _need(tokens, "tokens", _i32, (R, S - 1)),
+                         None if bias_offsets is None else _need(bias_offsets, "bias_offsets", _i32, (R + 1,)),
+                         None if bias_offsets is None else _need(bias_token, "bias_token", _i32, (n_bias,)),
+                         None if bias_offsets is None else _need(bias_value, "bias_value", _f32, (n_bias,)), mp, m_rs,
+                         None if mask_row is None else _need(mask_row, "mask_row", _i32, (R, S)),
+                         one(keep, "keep", _i32))
+    return a, out
+
+
+def adjust_logits(logits, *, seen=None, repetition=None, presence=None, frequency=None, tokens=None, bias_offsets=None,
+                  bias_token=None, bias_value=None, mask=None, mask_row=None, keep=None, out=None, workspace=None,
+                  stream=None):
+    """dspark_adjust_logits: logits [R][S][V] with penalties (fp32 [R] each) for what seen (seen_table) and the drafted
+    tokens [R][S - 1] before each row hold, biases (bias_token and bias_value from bias_offsets[r] to bias_offsets[r + 1])
+    and grammar masks (int32 words [masks][V / 32], mask_row [R][S], negative: none). Rows past keep[r] are left alone.
+    Returns {"out"}; out={"out": logits} works in place."""
+    if out is None and stream is not None:
+        with _on(stream):
+            out = {"out": torch.empty_like(logits)}
+    a, out = adjust_logits_args(logits, seen=seen, repetition=repetition, presence=presence, frequency=frequency,
+                                tokens=tokens, bias_offsets=bias_offsets, bias_token=bias_token, bias_value=bias_value,
+                                mask=mask, mask_row=mask_row, keep=keep, out=out)
+    ws = _status_workspace(workspace, logits.device, stream)
+    _launch("dspark_adjust_logits", lib().dspark_adjust_logits, a, ws, stream)
+    out["workspace"] = ws
     return out
 
 

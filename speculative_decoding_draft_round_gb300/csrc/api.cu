@@ -37,8 +37,9 @@ const char* kernel_name(int kernel)
     static const char* names[] = {"draft_setup", "draft_stats", "draft_commit", "schedule",
                                   "verify_rows", "verify_decide", "residual_stats", "residual_pick",
                                   "assemble", "rnn_step", "rnn_hidden", "draft_loop",
-                                  "qk_norm_rope", "cache_append", "cache_read", "cache_attend", "cache_merge"};
-    return kernel >= 0 && kernel <= DSPARK_KERNEL_CACHE_MERGE ? names[kernel] : "?";
+                                  "qk_norm_rope", "cache_append", "cache_read", "cache_attend", "cache_merge",
+                                  "add_norm_quant", "linear_layout", "linear_i8", "seen_add", "adjust_logits"};
+    return kernel >= 0 && kernel <= DSPARK_KERNEL_ADJUST_LOGITS ? names[kernel] : "?";
 }
 
 thread_local char g_last_error[256] = "no error";
@@ -331,6 +332,93 @@ AttendParams attend_params(const dspark_cache_attend_args* a)
 bool attend_uses_mma(const dspark_cache_attend_args* a, const AttendParams& p)
 {
     return a->path != DSPARK_PATH_CUDA_CORE && (attend_tc_supported(p) || attend_mma_supported(p));
+}
+
+// ------------------------------------------------------------ the rest of the target's pass
+
+dspark_status check_norm(const dspark_add_norm_quant_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_add_norm_quant_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T < 0 || a->N < 1 || (a->norm | 1) != 1) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (!(a->eps >= 0.f) || a->eps > FLT_MAX) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->N > 32768) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (a->T == 0) return DSPARK_OK;   // an empty tensor may have no address
+    if (!a->x || (a->sum && !a->residual) || (!a->codes && !a->y) || !a->codes != !a->scale)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->sum && a->sum == a->y) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->x_stride < 0 || a->residual_stride < 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    // rows of an output do not overlap
+    if (a->T > 1 && ((a->sum && a->sum_stride < a->N) || (a->y && a->y_stride < a->N) || (a->codes && a->codes_stride < a->N)))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+dspark_status check_linear(const dspark_linear_i8_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_linear_i8_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->T < 0 || a->K < 1 || a->N < 1 || a->reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->path < DSPARK_PATH_AUTO || a->path > DSPARK_PATH_TENSOR_CORE) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->out_rows < 0 || (!a->out_row && a->out_rows < a->T)) return DSPARK_ERR_INVALID_ARGUMENT;
+    // sums of K products of at most 2^14 stay below 2^31
+    if (a->K > 131071 || a->N > (1 << 24)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (a->T == 0) return DSPARK_OK;
+    if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->x_stride < 0 || a->w_stride < 0 || (a->out_rows > 1 && a->out_stride < a->N))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+LinearParams linear_params(const dspark_linear_i8_args* a)
+{
+    LinearParams p;
+    memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.K = a->K;
+    p.N = a->N;
+    p.dtype = a->dtype;
+    p.out_rows = a->out_rows;
+    p.x = a->x;
+    p.x_scale = a->x_scale;
+    p.w = a->w;
+    p.w_scale = a->w_scale;
+    p.bias = a->bias;
+    p.out_row = a->out_row;
+    p.n_rows = a->n_rows;
+    p.out = a->out;
+    p.x_rs = a->x_stride;
+    p.w_rs = a->w_stride;
+    p.o_rs = a->out_stride;
+    return p;
+}
+
+dspark_status check_seen(const dspark_seen_add_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_seen_add_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->R < 1 || a->W < 0 || a->V < 1 || (a->prompt | 1) != 1 || a->reserved != 0) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->R > DSPARK_MAX_SLOTS || a->V > (1 << 24)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (!a->seen || reinterpret_cast<uintptr_t>(a->seen) % 16 || a->seen_stride % 8 || a->seen_stride < a->V)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->W > 0 && (!a->tokens || a->tokens_stride < 0)) return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
+}
+
+dspark_status check_adjust(const dspark_adjust_logits_args* a)
+{
+    if (!a || a->struct_size != sizeof(dspark_adjust_logits_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->R < 1 || a->S < 1 || a->V < 1 || a->n_masks < 0 || a->n_bias < 0 || a->reserved != 0)
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->R > DSPARK_MAX_SLOTS || a->S > DSPARK_MAX_GAMMA + 1 || a->V > (1 << 24)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    if (!a->logits || !a->out) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->seen && (reinterpret_cast<uintptr_t>(a->seen) % 16 || a->seen_stride % 8 || a->seen_stride < a->V))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->bias_offsets && a->n_bias > 0 && (!a->bias_token || !a->bias_value)) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->mask && a->mask_stride < (a->V + 31) / 32) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->mask_row && !a->mask) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->mask && !a->mask_row && a->n_masks < (long long)a->R * a->S) return DSPARK_ERR_INVALID_ARGUMENT;
+    return DSPARK_OK;
 }
 
 template <typename T>
@@ -776,6 +864,146 @@ dspark_status dspark_cache_attend(const dspark_cache_attend_args* a, void* ws, s
     return cuda_status(e);
 }
 
+dspark_status dspark_add_norm_quant_workspace_size(const dspark_add_norm_quant_args* a, size_t* bytes)
+{
+    const dspark_status st = check_norm(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_add_norm_quant(const dspark_add_norm_quant_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_norm(a);
+    if (st != DSPARK_OK) return st;
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
+    if (a->T == 0) return DSPARK_OK;
+    NormParams p;
+    p.T = a->T;
+    p.N = a->N;
+    p.dtype = a->dtype;
+    p.norm = a->norm;
+    p.eps = a->eps;
+    p.x = a->x;
+    p.residual = a->residual;
+    p.x_rs = a->x_stride;
+    p.r_rs = a->residual_stride;
+    p.s_rs = a->sum_stride;
+    p.y_rs = a->y_stride;
+    p.c_rs = a->codes_stride;
+    p.gain = a->gain;
+    p.n_rows = a->n_rows;
+    p.sum = a->sum;
+    p.y = a->y;
+    p.codes = a->codes;
+    p.scale = a->scale;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_ADD_NORM_QUANT, s, [&] { return launch_add_norm_quant(p, s); }));
+}
+
+dspark_status dspark_linear_i8_workspace_size(const dspark_linear_i8_args* a, size_t* bytes)
+{
+    const dspark_status st = check_linear(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_linear_i8(const dspark_linear_i8_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_linear(a);
+    if (st != DSPARK_OK) return st;
+    LinearParams p = linear_params(a);
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
+    if (a->T == 0) return DSPARK_OK;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_LINEAR_I8, s, [&] { return launch_linear_simt(p, s); }));
+}
+
+dspark_status dspark_seen_add_workspace_size(const dspark_seen_add_args* a, size_t* bytes)
+{
+    const dspark_status st = check_seen(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_seen_add(const dspark_seen_add_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_seen(a);
+    if (st != DSPARK_OK) return st;
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
+    SeenParams p;
+    p.R = a->R;
+    p.W = a->W;
+    p.V = a->V;
+    p.prompt = a->prompt;
+    p.seen_rs = a->seen_stride;
+    p.tokens_rs = a->tokens_stride;
+    p.seen = a->seen;
+    p.tokens = a->tokens;
+    p.n = a->n;
+    p.extra = a->extra;
+    p.fresh = a->fresh;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_SEEN_ADD, s, [&] { return launch_seen_add(p, s); }));
+}
+
+dspark_status dspark_adjust_logits_workspace_size(const dspark_adjust_logits_args* a, size_t* bytes)
+{
+    const dspark_status st = check_adjust(a);
+    if (st != DSPARK_OK) return st;
+    if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
+    *bytes = kStatusBytes;
+    return DSPARK_OK;
+}
+
+dspark_status dspark_adjust_logits(const dspark_adjust_logits_args* a, void* ws, size_t ws_bytes, void* stream)
+{
+    clear_stale_error();
+    const dspark_status st = check_adjust(a);
+    if (st != DSPARK_OK) return st;
+    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    if (sw != DSPARK_OK) return sw;
+    AdjustParams p;
+    p.R = a->R;
+    p.S = a->S;
+    p.V = a->V;
+    p.dtype = a->dtype;
+    p.n_masks = a->n_masks;
+    p.n_bias = a->n_bias;
+    p.logits = a->logits;
+    p.out = a->out;
+    p.seen = a->seen;
+    p.seen_rs = a->seen_stride;
+    p.repetition = a->repetition;
+    p.presence = a->presence;
+    p.frequency = a->frequency;
+    p.tokens = a->S > 1 ? a->tokens : nullptr;
+    p.bias_offsets = a->n_bias > 0 ? a->bias_offsets : nullptr;
+    p.bias_token = a->bias_token;
+    p.bias_value = a->bias_value;
+    p.mask = a->mask;
+    p.mask_rs = a->mask_stride;
+    p.mask_row = a->mask_row;
+    p.keep = a->keep;
+    p.status = at<int>(ws, 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch(DSPARK_KERNEL_ADJUST_LOGITS, s, [&] { return launch_adjust_logits(p, s); }));
+}
+
 const char* dspark_last_error(void) { return g_last_error; }
 
 uint64_t dspark_set_wait_limit(uint64_t ns)
@@ -791,7 +1019,7 @@ dspark_status dspark_time_kernel(int32_t kernel, dspark_event_pair* events, int3
         g_timer = KernelTimer();
         return DSPARK_OK;
     }
-    if (kernel > DSPARK_KERNEL_CACHE_MERGE || !events || capacity < 0 || !count) return DSPARK_ERR_INVALID_ARGUMENT;
+    if (kernel > DSPARK_KERNEL_ADJUST_LOGITS || !events || capacity < 0 || !count) return DSPARK_ERR_INVALID_ARGUMENT;
     g_timer.kernel = kernel;
     g_timer.events = events;
     g_timer.capacity = capacity;

@@ -165,6 +165,69 @@ struct AttendParams {
     int* status;
 };
 
+// Rows normed and quantised (dspark_add_norm_quant).
+struct NormParams {
+    int T, N, dtype, norm;
+    float eps;
+    const void* x;
+    const void* residual;
+    int64_t x_rs, r_rs, s_rs, y_rs, c_rs;   // row strides
+    const float* gain;
+    const int32_t* n_rows;
+    void* sum;
+    void* y;
+    int8_t* codes;
+    float* scale;
+    int* status;
+};
+
+// Products of 8-bit rows and weights (dspark_linear_i8).
+struct LinearParams {
+    int T, K, N, dtype, out_rows;
+    const int8_t* x;
+    const float* x_scale;
+    const int8_t* w;
+    const float* w_scale;
+    const float* bias;
+    const int32_t* out_row;
+    const int32_t* n_rows;
+    void* out;
+    int64_t x_rs, w_rs, o_rs;   // row strides
+    int* status;
+};
+
+// Tokens into the table of what requests have seen (dspark_seen_add), and the logits that it bears on.
+struct SeenParams {
+    int R, W, V, prompt;
+    int64_t seen_rs, tokens_rs;
+    int16_t* seen;
+    const int32_t* tokens;
+    const int32_t* n;
+    const int32_t* extra;
+    const uint8_t* fresh;
+    int* status;
+};
+
+struct AdjustParams {
+    int R, S, V, dtype, n_masks, n_bias;
+    const void* logits;
+    void* out;
+    const int16_t* seen;
+    int64_t seen_rs;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int32_t* tokens;
+    const int32_t* bias_offsets;
+    const int32_t* bias_token;
+    const float* bias_value;
+    const uint32_t* mask;
+    int64_t mask_rs;
+    const int32_t* mask_row;
+    const int32_t* keep;
+    int* status;
+};
+
 // sample.cu
 cudaError_t launch_draft_setup(const DraftStep& p, cudaStream_t s);
 cudaError_t launch_draft_stats_simt(const DraftStep& p, cudaStream_t s);
@@ -230,6 +293,16 @@ cudaError_t launch_cache_merge(const AttendParams& p, const AttendScratch& ws, c
 bool attend_tc_supported(const AttendParams& p);
 int attend_tc_block_rows();
 cudaError_t launch_cache_attend_tc(const AttendParams& p, const AttendScratch& ws, cudaStream_t s);
+
+// add_norm_quant.cu
+cudaError_t launch_add_norm_quant(const NormParams& p, cudaStream_t s);
+
+// linear_i8.cu
+cudaError_t launch_linear_simt(const LinearParams& p, cudaStream_t s);
+
+// logits.cu
+cudaError_t launch_seen_add(const SeenParams& p, cudaStream_t s);
+cudaError_t launch_adjust_logits(const AdjustParams& p, cudaStream_t s);
 
 // rnn.cu (RNN head)
 cudaError_t launch_rnn_hidden(const DraftStep& p, cudaStream_t s);   // rnn_hidden.cu: yh = W_rnn[:, 2r:] h, every position

@@ -1,0 +1,399 @@
+// logits.cu -- penalties for tokens seen, biases and grammar masks on rows of logits (dspark_adjust_logits), and the
+// table of what each request has seen (dspark_seen_add).
+//
+// A request's rows share its row of the table and its biases: a CTA takes a stretch of the vocabulary of one request,
+// keeps both for its ids in registers, and runs through the rows, counting a drafted token when it has passed its row.
+// The bytes bound it: a row is read and written once; in place, only 16-byte pieces that change are written, pieces that
+// nothing bears on are not read, and pieces that a mask hides whole are written without being read.
+#include <float.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dspark {
+
+namespace {
+
+// ------------------------------------------------------------------ the table
+
+constexpr int kSeenThreads = 256;
+constexpr int kSeenStretch = 8192;       // ids whose new counts a CTA holds: 32 KB
+
+__device__ __forceinline__ int seen_tokens(const SeenParams& p, int r, bool report)
+{
+    if (!p.n) return p.W;
+    const int n = p.n[r];
+    if (n >= 0 && n <= p.W) return n;
+    if (report) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+    return n < 0 ? 0 : p.W;
+}
+
+// one more token, at most 32767 counted
+__device__ __forceinline__ void count_one(int16_t* at)
+{
+    unsigned short* w = reinterpret_cast<unsigned short*>(at);
+    unsigned short old = *reinterpret_cast<volatile unsigned short*>(w);
+    while ((old & 0x7FFF) != 0x7FFF) {   // a try fails only where another token got through
+        const unsigned short was = atomicCAS(w, old, (unsigned short)(old + 1));
+        if (was == old) return;
+        old = was;
+    }
+}
+
+__device__ __forceinline__ void mark_one(int16_t* at)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
+    atomicOr(reinterpret_cast<unsigned*>(a & ~uintptr_t(3)), a & 2 ? 0x80000000u : 0x8000u);
+}
+
+// grid (stretches of the vocabulary, requests). A fresh row is written whole, each CTA the stretch whose tokens it has
+// counted in shared memory; otherwise the CTAs of a request share its tokens, and each goes into the row by an atomic.
+__global__ void __launch_bounds__(kSeenThreads) seen_add_kernel(SeenParams p)
+{
+    __shared__ int s_new[kSeenStretch];
+    pdl_enter();
+    const int r = blockIdx.y, tid = threadIdx.x;
+    const int n = seen_tokens(p, r, blockIdx.x == 0 && tid == 0);
+    const int32_t* tokens = p.tokens + r * p.tokens_rs;
+    int16_t* row = p.seen + r * p.seen_rs;
+    const int all = n + (p.extra ? 1 : 0);
+    auto token = [&](int i) { return i < n ? tokens[i] : p.extra[r]; };
+    if (!p.fresh || !p.fresh[r]) {
+        for (int i = blockIdx.x * kSeenThreads + tid; i < all; i += gridDim.x * kSeenThreads) {
+            const int v = token(i);
+            if (v < 0 || v >= p.V) {
+                raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+                continue;
+            }
+            if (p.prompt) mark_one(row + v);
+            else count_one(row + v);
+        }
+        return;
+    }
+    const int v0 = blockIdx.x * kSeenStretch;
+    for (int i = tid; i < kSeenStretch; i += kSeenThreads) s_new[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < all; i += kSeenThreads) {
+        const int v = token(i);
+        if ((unsigned)(v - v0) < (unsigned)kSeenStretch && v < p.V) {
+            if (p.prompt) s_new[v - v0] = 1;
+            else atomicAdd(&s_new[v - v0], 1);
+        } else if (blockIdx.x == 0 && (unsigned)v >= (unsigned)p.V) {
+            raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+        }
+    }
+    __syncthreads();
+    const int words = (int)min((long long)kSeenStretch, (long long)p.seen_rs - v0);
+    for (int i = tid * 8; i < words; i += kSeenThreads * 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int a = s_new[i + 2 * j], b = s_new[i + 2 * j + 1];
+            w[j] = p.prompt ? (a ? 0x8000u : 0u) | (b ? 0x80000000u : 0u) : (uint32_t)min(a, 32767) | (uint32_t)min(b, 32767) << 16;
+        }
+        *reinterpret_cast<uint4*>(row + v0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ------------------------------------------------------------------ the logits
+
+constexpr int kAdjThreads = 256;
+constexpr int kAdjEach = 8;                              // ids a thread
+constexpr int kAdjStretch = kAdjThreads * kAdjEach;      // ids a CTA
+constexpr int kAdjRows = 4;                              // rows whose loads are in flight together
+constexpr int kAdjMaxS = DSPARK_MAX_GAMMA + 1;
+
+template <typename T>
+struct Logits8 {
+    uint32_t u[2 * sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ float logit(const Logits8<T>& x, int e);
+template <>
+__device__ __forceinline__ float logit<float>(const Logits8<float>& x, int e) { return __uint_as_float(x.u[e]); }
+template <>
+__device__ __forceinline__ float logit<__nv_bfloat16>(const Logits8<__nv_bfloat16>& x, int e)
+{
+    return __uint_as_float(e & 1 ? x.u[e / 2] & 0xFFFF0000u : x.u[e / 2] << 16);
+}
+template <typename T>
+__device__ __forceinline__ void set_logit(Logits8<T>& x, int e, float z);
+template <>
+__device__ __forceinline__ void set_logit<float>(Logits8<float>& x, int e, float z) { x.u[e] = __float_as_uint(z); }
+template <>
+__device__ __forceinline__ void set_logit<__nv_bfloat16>(Logits8<__nv_bfloat16>& x, int e, float z)
+{
+    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+    x.u[e / 2] = e & 1 ? (x.u[e / 2] & 0xFFFFu) | h << 16 : (x.u[e / 2] & 0xFFFF0000u) | h;
+}
+
+// kVec: a thread's ids are 8 neighbours, loaded 16 bytes at a time; else every 256th, one at a time.
+template <typename T, bool kVec>
+__device__ __forceinline__ int id_of(int v0, int e)
+{
+    return kVec ? v0 + threadIdx.x * kAdjEach + e : v0 + e * kAdjThreads + threadIdx.x;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_logits(Logits8<T>& x, const T* row, int v0, int V)
+{
+    if constexpr (kVec) {
+        const uint4* src = reinterpret_cast<const uint4*>(row + v0 + threadIdx.x * kAdjEach);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 q = src[i];
+            x.u[4 * i] = q.x;
+            x.u[4 * i + 1] = q.y;
+            x.u[4 * i + 2] = q.z;
+            x.u[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kAdjEach; ++e) {
+            const int v = id_of<T, kVec>(v0, e);
+            set_logit<T>(x, e, v < V ? to_f32<T>(row[v]) : 0.f);
+        }
+    }
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_logits(const Logits8<T>& x, T* row, int v0, int V)
+{
+    if constexpr (kVec) {
+        uint4* dst = reinterpret_cast<uint4*>(row + v0 + threadIdx.x * kAdjEach);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            dst[i] = make_uint4(x.u[4 * i], x.u[4 * i + 1], x.u[4 * i + 2], x.u[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kAdjEach; ++e) {
+            const int v = id_of<T, kVec>(v0, e);
+            if (v >= V) continue;
+            if constexpr (sizeof(T) == 4) row[v] = __uint_as_float(x.u[e]);
+            else row[v] = __ushort_as_bfloat16((unsigned short)(x.u[e / 2] >> (16 * (e & 1))));
+        }
+    }
+}
+
+// grid (stretches, requests)
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
+{
+    __shared__ int s_token[kAdjMaxS];        // what row j has before it, one more each row; -1: none
+    __shared__ int s_mask[kAdjMaxS];
+    __shared__ int s_bias_id[kAdjThreads];
+    __shared__ float s_bias[kAdjThreads];
+    __shared__ int s_base[kAdjThreads / 32 + 1];
+    pdl_enter();
+    const int r = blockIdx.y, tid = threadIdx.x, v0 = blockIdx.x * kAdjStretch;
+    const bool first = blockIdx.x == 0;
+    int keep = p.keep ? p.keep[r] : p.S - 1;
+    if (keep < 0 || keep >= p.S) {
+        if (first && tid == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+        keep = keep < 0 ? 0 : p.S - 1;
+    }
+    const int rows = keep + 1;
+    if (tid < rows) {
+        int v = -1, m = -1;
+        if (p.tokens && tid > 0) {
+            v = p.tokens[(size_t)r * (p.S - 1) + tid - 1];
+            if (v >= p.V) {
+                if (first) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+                v = -1;
+            }
+        }
+        if (p.mask) {
+            m = p.mask_row ? p.mask_row[(size_t)r * p.S + tid] : r * p.S + tid;
+            if (m >= p.n_masks) {
+                if (first) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+                m = -1;
+            }
+        }
+        s_token[tid] = v;
+        s_mask[tid] = m;
+    }
+    auto factor = [&](const float* f, float none, bool above) {
+        if (!f) return none;
+        const float x = f[r];
+        if (fabsf(x) <= FLT_MAX && (!above || x > 0.f)) return x;
+        if (first && tid == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+        return none;
+    };
+    const float rep = factor(p.repetition, 1.f, true), pres = factor(p.presence, 0.f, false),
+                freq = factor(p.frequency, 0.f, false);
+    const bool penal = rep != 1.f || pres != 0.f || freq != 0.f;
+    // what this thread's ids have been, and what they are given
+    int count[kAdjEach];
+    float bias[kAdjEach] = {};
+    unsigned prompt = 0u, known = 0u, biased = 0u;       // bits by id
+#pragma unroll
+    for (int e = 0; e < kAdjEach; ++e) count[e] = 0;
+    if (p.seen && penal) {
+        const int16_t* row = p.seen + r * p.seen_rs;
+        if constexpr (kVec) {
+            const int v = v0 + tid * kAdjEach;
+            if (v < p.V) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + v));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < kAdjEach; ++e) {
+                    const uint32_t c = (w[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
+                    count[e] = c & 0x7FFF;
+                    prompt |= (c >> 15) << e;
+                    known |= (c != 0u ? 1u : 0u) << e;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kAdjEach; ++e) {
+                const int v = id_of<T, kVec>(v0, e);
+                const uint32_t c = v < p.V ? (uint16_t)__ldg(row + v) : 0u;
+                count[e] = c & 0x7FFF;
+                prompt |= (c >> 15) << e;
+                known |= (c != 0u ? 1u : 0u) << e;
+            }
+        }
+    }
+    if (p.bias_offsets) {
+        const int b0 = p.bias_offsets[r], b1 = p.bias_offsets[r + 1];
+        if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
+            if (first && tid == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+        } else {
+            // this stretch's entries, 256 looked at a time, in their order
+            for (int b = b0; b < b1; b += kAdjThreads) {
+                const int i = b + tid;
+                const int v = i < b1 ? p.bias_token[i] : -1;
+                if (first && i < b1 && (v < 0 || v >= p.V)) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+                const bool here = i < b1 && (unsigned)(v - v0) < (unsigned)kAdjStretch && v < p.V && v >= 0;
+                const unsigned vote = __ballot_sync(0xffffffffu, here);
+                __syncthreads();
+                if ((tid & 31) == 0) s_base[tid >> 5] = __popc(vote);
+                __syncthreads();
+                int at = __popc(vote & ((1u << (tid & 31)) - 1u)), total = 0;
+#pragma unroll
+                for (int w = 0; w < kAdjThreads / 32; ++w) {
+                    if (w < (tid >> 5)) at += s_base[w];
+                    total += s_base[w];
+                }
+                if (here) {
+                    s_bias_id[at] = v - v0;
+                    s_bias[at] = p.bias_value[i];
+                }
+                __syncthreads();
+                for (int k = 0; k < total; ++k) {
+                    const int d = s_bias_id[k];
+                    const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
+                    if (owner == tid) {
+                        const float x = s_bias[k];
+#pragma unroll
+                        for (int e = 0; e < kAdjEach; ++e)
+                            if (e == slot) bias[e] += x;
+                        biased |= 1u << slot;
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const bool inside = kVec ? v0 + tid * kAdjEach < p.V : v0 + tid < p.V;
+    if (!inside) return;
+    const bool in_place = p.out == p.logits;
+    const size_t base = (size_t)r * p.S * p.V;
+    const T* src = static_cast<const T*>(p.logits) + base;
+    T* dst = static_cast<T*>(p.out) + base;
+    for (int j0 = 0; j0 < rows; j0 += kAdjRows) {
+        Logits8<T> x[kAdjRows];
+        unsigned allowed[kAdjRows], near[kAdjRows];
+        unsigned touch = known | biased;
+#pragma unroll
+        for (int u = 0; u < kAdjRows; ++u) {
+            const int j = j0 + u;
+            allowed[u] = 0xFFu;
+            near[u] = 0u;
+            if (j >= rows) continue;
+            const int m = s_mask[j];
+            if (m >= 0) {
+                const uint32_t* bits = p.mask + m * p.mask_rs;
+                if constexpr (kVec) {
+                    allowed[u] = __ldg(reinterpret_cast<const uint8_t*>(bits) + (v0 + tid * kAdjEach) / 8);
+                } else {
+                    allowed[u] = 0u;
+#pragma unroll
+                    for (int e = 0; e < kAdjEach; ++e) {
+                        const int v = id_of<T, kVec>(v0, e);
+                        if (v < p.V) allowed[u] |= ((__ldg(bits + v / 32) >> (v % 32)) & 1u) << e;
+                    }
+                }
+            }
+            const int d = s_token[j] - v0;
+            if (penal && s_token[j] >= 0 && (unsigned)d < (unsigned)kAdjStretch) {
+                const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
+                if (owner == tid) near[u] = 1u << slot;
+            }
+            touch |= near[u];
+            if (allowed[u] != 0u && (!in_place || touch != 0u || allowed[u] != 0xFFu))
+                load_logits<T, kVec>(x[u], src + (size_t)j * p.V, v0, p.V);
+        }
+        touch = known | biased;
+#pragma unroll
+        for (int u = 0; u < kAdjRows; ++u) {
+            const int j = j0 + u;
+            if (j >= rows) continue;
+            if (near[u]) {
+                known |= near[u];
+                touch |= near[u];
+#pragma unroll
+                for (int e = 0; e < kAdjEach; ++e) count[e] += (near[u] >> e) & 1u;
+            }
+            if (touch == 0u && allowed[u] == 0xFFu) {
+                if (!in_place) store_logits<T, kVec>(x[u], dst + (size_t)j * p.V, v0, p.V);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < kAdjEach; ++e) {
+                if (!((allowed[u] >> e) & 1u)) {
+                    set_logit<T>(x[u], e, -INFINITY);
+                } else if ((touch >> e) & 1u) {
+                    float z = logit<T>(x[u], e);
+                    if ((known >> e) & 1u) {
+                        z = z > 0.f ? __fdiv_rn(z, rep) : z * rep;
+                        z = fmaf(-freq, (float)count[e], z);
+                        if (count[e] > 0) z -= pres;
+                    }
+                    if ((biased >> e) & 1u) z += bias[e];
+                    set_logit<T>(x[u], e, z);
+                }
+            }
+            store_logits<T, kVec>(x[u], dst + (size_t)j * p.V, v0, p.V);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_adjust(const AdjustParams& p, cudaStream_t s)
+{
+    const dim3 grid(cdiv(p.V, kAdjStretch), p.R);
+    const uintptr_t where = reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(p.out);
+    // rows of whole 16-byte pieces
+    if (p.V % 8 == 0 && where % 16 == 0) return launch_pdl(adjust_kernel<T, true>, grid, dim3(kAdjThreads), 0, s, p);
+    return launch_pdl(adjust_kernel<T, false>, grid, dim3(kAdjThreads), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_seen_add(const SeenParams& p, cudaStream_t s)
+{
+    const dim3 grid(cdiv(p.seen_rs, kSeenStretch), p.R);
+    const cudaError_t e = launch_pdl(seen_add_kernel, grid, dim3(kSeenThreads), 0, s, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_adjust_logits(const AdjustParams& p, cudaStream_t s)
+{
+    const cudaError_t e = p.dtype == DSPARK_BF16 ? launch_adjust<__nv_bfloat16>(p, s) : launch_adjust<float>(p, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace dspark
