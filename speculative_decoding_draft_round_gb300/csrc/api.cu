@@ -393,6 +393,11 @@ LinearParams linear_params(const dspark_linear_i8_args* a)
     return p;
 }
 
+bool linear_uses_tc(const dspark_linear_i8_args* a, const LinearParams& p)
+{
+    return a->path != DSPARK_PATH_CUDA_CORE && a->T > 0 && linear_tc_supported(p);
+}
+
 dspark_status check_seen(const dspark_seen_add_args* a)
 {
     if (!a || a->struct_size != sizeof(dspark_seen_add_args)) return DSPARK_ERR_INVALID_ARGUMENT;
@@ -910,7 +915,8 @@ dspark_status dspark_linear_i8_workspace_size(const dspark_linear_i8_args* a, si
     const dspark_status st = check_linear(a);
     if (st != DSPARK_OK) return st;
     if (!bytes) return DSPARK_ERR_INVALID_ARGUMENT;
-    *bytes = kStatusBytes;
+    const LinearParams p = linear_params(a);
+    *bytes = kStatusBytes + (linear_uses_tc(a, p) ? linear_tc_scratch(p) : 0);
     return DSPARK_OK;
 }
 
@@ -920,11 +926,20 @@ dspark_status dspark_linear_i8(const dspark_linear_i8_args* a, void* ws, size_t 
     const dspark_status st = check_linear(a);
     if (st != DSPARK_OK) return st;
     LinearParams p = linear_params(a);
-    const dspark_status sw = check_workspace(ws, ws_bytes, kStatusBytes, alignof(int));
+    const bool tc = linear_uses_tc(a, p);
+    if (a->path == DSPARK_PATH_TENSOR_CORE && !tc && a->T > 0) return DSPARK_ERR_UNSUPPORTED_SHAPE;
+    const size_t need = kStatusBytes + (tc ? linear_tc_scratch(p) : 0);
+    const dspark_status sw = check_workspace(ws, ws_bytes, need, need > kStatusBytes ? 16 : alignof(int));
     if (sw != DSPARK_OK) return sw;
     if (a->T == 0) return DSPARK_OK;
     p.status = at<int>(ws, 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tc) {
+        void* scratch = at<char>(ws, kStatusBytes);
+        cudaError_t e = launch(DSPARK_KERNEL_LINEAR_LAYOUT, s, [&] { return launch_linear_layout(p, scratch, s); });
+        if (e == cudaSuccess) e = launch(DSPARK_KERNEL_LINEAR_I8, s, [&] { return launch_linear_tc(p, scratch, s); });
+        return cuda_status(e);
+    }
     return cuda_status(launch(DSPARK_KERNEL_LINEAR_I8, s, [&] { return launch_linear_simt(p, s); }));
 }
 

@@ -299,6 +299,11 @@ cudaError_t launch_add_norm_quant(const NormParams& p, cudaStream_t s);
 
 // linear_i8.cu
 cudaError_t launch_linear_simt(const LinearParams& p, cudaStream_t s);
+// linear_i8_tc.cu; ws: linear_tc_scratch bytes
+bool linear_tc_supported(const LinearParams& p);
+size_t linear_tc_scratch(const LinearParams& p);
+cudaError_t launch_linear_layout(const LinearParams& p, void* ws, cudaStream_t s);
+cudaError_t launch_linear_tc(const LinearParams& p, void* ws, cudaStream_t s);
 
 // logits.cu
 cudaError_t launch_seen_add(const SeenParams& p, cudaStream_t s);
