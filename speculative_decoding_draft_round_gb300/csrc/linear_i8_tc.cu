@@ -16,6 +16,8 @@
 // lanes and half of the step each, into one of two slots), 10-13 take finished sums out (one of two accumulators).
 // Tiles that would leave SMs idle are split along K over the pairs of a cluster, which add up their sums through
 // distributed shared memory in a fixed order.
+// The kernel is launched without programmatic dependence: with it, calls that fill every SM with pairs, made back to back
+// by the thousand, came to a stop (none did in 4000 without).
 // Every wait is bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT, the CTAs stop issuing, let
 // copies and MMAs land, free their tensor memory and return.
 #include <cudaTypedefs.h>
@@ -344,8 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc5::fence_after();
     const uint32_t tmem = *s_tmem;
-    pdl_wait();
-    pdl_trigger();
 
     const Waits wait{s_abort, p.status, g.wait_ns};
     const Tiles tiles(p, g, linear_rows(p, false));
@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) pair_commit(bar(kSumFull + b), both);
             }
-            // every MMA issued is done before the tensor memory is freed (also after an abort)
-            pair_commit(bar(kFin), (uint16_t)(1u << rank));
-            drain(bar(kFin), 0u);
+            pair_commit(bar(kFin), both);
         }
+        // every MMA issued is done, and its arrivals here have been made, before the CTAs leave (also after an abort)
+        drain(bar(kFin), 0u);
     } else if (warp < kFirstOut) {
         // ---------------- widening: lane 32 (warp % 4) + lane, half `part` of the step
         const int part = (warp - kFirstWidener) >> 2;
@@ -588,10 +588,8 @@ cudaError_t configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int pa
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * pairs;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     return cudaSuccess;
 }
 
@@ -607,9 +605,8 @@ cudaError_t clusters_held(int pairs, int* n)
     *n = dev < 64 ? h.load(std::memory_order_acquire) : 0;
     if (*n > 0) return cudaSuccess;
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     e = configure<T>(cfg, attr, pairs, 1, nullptr);
-    cfg.numAttrs = 1;
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(n, linear_tc_kernel<T>, &cfg);
     if (e == cudaSuccess && *n < 1) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess && dev < 64) h.store(*n, std::memory_order_release);
@@ -652,7 +649,7 @@ cudaError_t launch_tc(const LinearParams& p, void* ws, cudaStream_t s)
         !encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, p.K, p.T, (uint64_t)g.x_pitch * 2, 64, g.rows / 2))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     e = configure<T>(cfg, attr, g.split, clusters, s);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, linear_tc_kernel<T>, p, g, wmap, xmap);
     return e;
