@@ -143,9 +143,11 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
     return a;
 }
 
+// What the arrival tells of is in tensor memory and ordered by the tcgen05 fences (or is a copy's, which the copy engine's
+// barrier ordered): it needs no release of this thread's other writes to the cluster.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -153,38 +155,11 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The phase's end as arrivals of both CTAs of a pair made it; does not wait
-__device__ __forceinline__ bool pair_test_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ bool pair_try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                        unsigned long long limit_ns)
 {
     const unsigned long long t0 = globaltimer();
-    while (!pair_try_wait(bar, parity)) {
+    while (!mbar_try_wait(bar, parity)) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
@@ -201,7 +176,7 @@ struct Waits {
     unsigned long long limit_ns;
     __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const
     {
-        return pair_test_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
+        return mbar_test_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
     }
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const
     {
@@ -212,7 +187,7 @@ struct Waits {
 __device__ __noinline__ void drain(uint32_t bar, uint32_t parity)
 {
     const unsigned long long t0 = globaltimer();
-    while (!pair_try_wait(bar, parity) && globaltimer() - t0 < kDrainNs) {
+    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < kDrainNs) {
     }
 }
 
