@@ -5,7 +5,7 @@
 //   scale = max|y| / 127,  code = rint(127 p / max|p|): the norm cancels from the code.
 //
 // Codes are exact. In fp32 the quotient 127 p / max|p| carries four roundings, 127 * 4 * 2^-24 < 2^-14 in all, so its
-// nearest whole number is the exact one's unless it lies within 2^-14 of a half. Those few are formed again in 64 bits,
+// nearest whole number is the exact one's unless it lies within 2^-14 of a half. Those few are settled
 // from the exact products s * gain (48 bits) and the exact largest of them (fp32 head and remainder). Rows whose
 // products or squares leave fp32's range, and those with a NaN or an infinity, are done in 64 bits altogether.
 //
@@ -20,7 +20,6 @@ namespace dspark {
 namespace {
 
 constexpr int kNormMaxN = 32768;
-constexpr int kVecMax = 4;               // pieces of 8 elements a thread
 constexpr float kNearHalf = 0.5f - 0x1.0p-14f;
 
 template <typename T>
@@ -118,6 +117,13 @@ __device__ __forceinline__ int ordered(float x)
 }
 __device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b >= 0 ? b : b ^ 0x7FFFFFFF); }
 
+// What the product s * g leaves beyond its fp32 rounding, where that is the row's largest
+__device__ __forceinline__ int remainder_at(float s, float g, uint32_t m, int lo)
+{
+    const float h = s * g, rest = fmaf(s, g, -h);
+    return (__float_as_uint(h) & 0x7FFFFFFFu) == m ? max(lo, ordered(h < 0.f ? -rest : rest)) : lo;
+}
+
 // The rows' threads: a warp, or a whole CTA of NT. Every reduction takes fresh words of shared memory, so that one
 // barrier is enough for each; they come in this order.
 template <int NT>
@@ -125,7 +131,7 @@ struct Team {
     static constexpr int kWarps = NT / 32;
     float* sums;       // [kWarps]
     uint32_t* tops;    // [kWarps]
-    int* los;          // [kWarps]
+    int* lo;           // [1]
     double* wide;      // [2][kWarps]
 
     __device__ __forceinline__ RowStats stats(float sum, uint32_t m) const
@@ -137,6 +143,7 @@ struct Team {
             if (lane == 0) {
                 sums[warp] = sum;
                 tops[warp] = m;
+                if (warp == 0) *lo = INT32_MIN;
             }
             __syncthreads();
             sum = 0.f;
@@ -149,17 +156,17 @@ struct Team {
         }
         return RowStats{sum, m};
     }
-    __device__ __forceinline__ int largest(int x) const
+    // the largest of what the threads that hold the row's largest product found
+    __device__ __forceinline__ float largest(bool holds, int x) const
     {
-        x = __reduce_max_sync(0xffffffffu, x);
-        if constexpr (kWarps > 1) {
-            if ((threadIdx.x & 31) == 0) los[threadIdx.x >> 5] = x;
+        if constexpr (kWarps == 1) {
+            x = __reduce_max_sync(0xffffffffu, holds ? x : INT32_MIN);
+        } else {
+            if (holds) atomicMax(lo, x);
             __syncthreads();
-            x = los[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) x = max(x, los[w]);
+            x = *lo;
         }
-        return x;
+        return from_ordered(x);
     }
     // sum of a, largest of b
     __device__ __noinline__ void in_64(double& a, double& b) const
@@ -208,8 +215,22 @@ __device__ __forceinline__ bool in_range(const RowStats& st, int N)
 // What the row's elements are turned with.
 struct RowScales {
     float inv, scale, per;   // y = p * inv, the codes' scale, code = p * per
-    double top;              // max|p|
+    float m, lo;             // max|p|: its fp32 rounding and what that leaves (rows whose statistics are in range)
+    double top;              // max|p| (the others)
 };
+
+// The code of a quotient f near a half, k + 1/2: the sign of 254 |p| - (2 k + 1) max|p|, whose heads are near enough to
+// leave each other exactly and whose remainders are exact. 64 bits only where that is next to nothing: on this chip a
+// division in 64 bits by a warp takes as long as its whole row (2176 rows of 4096 29 us with one for every such code).
+__device__ __noinline__ int settled(float s, float g, float f, const RowScales& r)
+{
+    const float h = s * g, rest = fmaf(s, g, -h), k = floorf(fabsf(f)), o = 2.f * k + 1.f;
+    const float a = 254.f * fabsf(h), b = o * r.m;
+    const float d = (a - b) + ((fmaf(254.f, fabsf(h), -a) - fmaf(o, r.m, -b)) + (254.f * (h < 0.f ? -rest : rest) - o * r.lo));
+    if (fabsf(d) <= 0x1.0p-34f * r.m) return code_in_64(s, g, (double)r.m + (double)r.lo);
+    const int q = (int)k + (d > 0.f ? 1 : 0);
+    return f < 0.f ? -q : q;
+}
 
 template <int NT>
 __device__ __forceinline__ void finish(const NormParams& p, const RowStats& st, RowScales& k)
@@ -218,6 +239,8 @@ __device__ __forceinline__ void finish(const NormParams& p, const RowStats& st, 
     k.inv = p.norm ? 1.f / sqrtf(st.sum / (float)p.N + p.eps) : 1.f;
     k.scale = m * k.inv / 127.f;
     k.per = 127.f / m;
+    k.m = m;
+    k.lo = 0.f;
 }
 
 // N a multiple of 8, rows and outputs on 16-byte (codes on 8-byte) boundaries: V pieces of 8 elements a thread, kept in
@@ -228,9 +251,9 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_vec_kernel(NormParam
     constexpr int kRows = NT == 32 ? 8 : 1, kWarps = NT / 32;
     __shared__ float s_sums[kWarps];
     __shared__ uint32_t s_tops[kWarps];
-    __shared__ int s_los[kWarps];
+    __shared__ int s_lo;
     __shared__ double s_wide[2 * kWarps];
-    const Team<NT> team{s_sums, s_tops, s_los, s_wide};
+    const Team<NT> team{s_sums, s_tops, &s_lo, s_wide};
     pdl_enter();
     const int t = blockIdx.x * kRows + (kRows > 1 ? (int)(threadIdx.x >> 5) : 0);
     const int tid = kRows > 1 ? threadIdx.x & 31 : threadIdx.x;
@@ -267,8 +290,7 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_vec_kernel(NormParam
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 sum = fmaf(s[i][e], s[i][e], sum);
-                const float h = p.gain ? s[i][e] * g[e] : s[i][e];
-                m = max(m, __float_as_uint(h) & 0x7FFFFFFFu);
+                m = max(m, __float_as_uint(p.gain ? s[i][e] * g[e] : s[i][e]) & 0x7FFFFFFFu);
             }
         }
     }
@@ -277,26 +299,18 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_vec_kernel(NormParam
     bool wide = !in_range(st, p.N), bad = false;
     if (!wide) {
         finish<NT>(p, st, k);
-        k.top = (double)__uint_as_float(st.m);
         if (p.codes && p.gain) {
-            // the remainder of the largest product
             int lo = INT32_MIN;
+            if (m == st.m) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = i * NT + tid;
-                if (c >= pieces) continue;
-                float g[8];
-                load8(p.gain + c * 8, g);
+                for (int i = 0; i < V; ++i) {
+                    const int c = i * NT + tid;
+                    if (c >= pieces) continue;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float h = s[i][e] * g[e];
-                    if ((__float_as_uint(h) & 0x7FFFFFFFu) == st.m) {
-                        const float rest = fmaf(s[i][e], g[e], -h);
-                        lo = max(lo, ordered(h < 0.f ? -rest : rest));
-                    }
+                    for (int e = 0; e < 8; ++e) lo = remainder_at(s[i][e], p.gain[c * 8 + e], st.m, lo);
                 }
             }
-            k.top += (double)from_ordered(team.largest(lo));
+            k.lo = team.largest(m == st.m, lo);
         }
     } else {
         double ss = 0.0, top = 0.0;
@@ -347,11 +361,20 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_vec_kernel(NormParam
         if (p.codes) {
             int q[8];
             if (!wide) {
+                // 1.5 * 2^23 added: the sum's low bits are the nearest whole number
+                float f[8], off = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float f = (p.gain ? s[i][e] * g[e] : s[i][e]) * k.per, n = rintf(f);
-                    q[e] = (int)n;
-                    if (fabsf(f - n) > kNearHalf) q[e] = code_in_64(s[i][e], p.gain ? g[e] : 1.f, k.top);
+                    f[e] = (p.gain ? s[i][e] * g[e] : s[i][e]) * k.per;
+                    const float n = f[e] + 12582912.f;
+                    q[e] = __float_as_int(n);
+                    off = fmaxf(off, fabsf(f[e] - (n - 12582912.f)));
+                }
+                if (off > kNearHalf) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (fabsf(f[e] - ((f[e] + 12582912.f) - 12582912.f)) > kNearHalf)
+                            q[e] = settled(s[i][e], p.gain ? g[e] : 1.f, f[e], k);
                 }
             } else {
 #pragma unroll
@@ -375,9 +398,9 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormParams p)
     extern __shared__ float row[];
     __shared__ float s_sums[kWarps];
     __shared__ uint32_t s_tops[kWarps];
-    __shared__ int s_los[kWarps];
+    __shared__ int s_lo;
     __shared__ double s_wide[2 * kWarps];
-    const Team<NT> team{s_sums, s_tops, s_los, s_wide};
+    const Team<NT> team{s_sums, s_tops, &s_lo, s_wide};
     pdl_enter();
     const int t = blockIdx.x, tid = threadIdx.x;
     if (t >= live_rows(p.n_rows, p.T, p.status, t == 0 && tid == 0)) return;
@@ -402,24 +425,18 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(NormParams p)
     bool wide = !in_range(st, p.N), bad = false;
     if (!wide) {
         finish<NT>(p, st, k);
-        k.top = (double)__uint_as_float(st.m);
         if (p.codes && p.gain) {
             int lo = INT32_MIN;
-            for (int c = tid; c < p.N; c += NT) {
-                const float g = gain(c), h = row[c] * g;
-                if ((__float_as_uint(h) & 0x7FFFFFFFu) == st.m) {
-                    const float rest = fmaf(row[c], g, -h);
-                    lo = max(lo, ordered(h < 0.f ? -rest : rest));
-                }
-            }
-            k.top += (double)from_ordered(team.largest(lo));
+            if (m == st.m)
+                for (int c = tid; c < p.N; c += NT) lo = remainder_at(row[c], gain(c), st.m, lo);
+            k.lo = team.largest(m == st.m, lo);
         }
         for (int c = tid; c < p.N; c += NT) {
             const float g = gain(c), h = row[c] * g;
             if (p.y) static_cast<T*>(p.y)[t * p.y_rs + c] = narrowed<T>(h * k.inv);
             if (p.codes) {
                 const float f = h * k.per, n = rintf(f);
-                p.codes[t * p.c_rs + c] = (int8_t)(fabsf(f - n) > kNearHalf ? code_in_64(row[c], g, k.top) : (int)n);
+                p.codes[t * p.c_rs + c] = (int8_t)(fabsf(f - n) > kNearHalf ? settled(row[c], g, f, k) : (int)n);
             }
         }
     } else {
@@ -456,31 +473,26 @@ bool vec_rows(const NormParams& p)
            (!p.codes || on(p.codes, p.c_rs, 8)) && on(p.gain, 0, 16);
 }
 
-// kFrom: the fewest pieces a thread that the widths left to NT threads need
-template <typename T, int NT, int kFrom>
+// kFrom .. kTo: the pieces a thread that the widths left to NT threads need
+template <typename T, int NT, int kFrom, int kTo>
 cudaError_t launch_vec(const NormParams& p, cudaStream_t s)
 {
+    if constexpr (kFrom < kTo)
+        if (cdiv(p.N / 8, NT) > kFrom) return launch_vec<T, NT, kFrom + 1, kTo>(p, s);
     constexpr int kRows = NT == 32 ? 8 : 1;
-    const dim3 grid(cdiv(p.T, kRows)), block(NT == 32 ? 256 : NT);
-    const int each = cdiv(p.N / 8, NT);
-    if constexpr (kFrom <= 1)
-        if (each == 1) return launch_pdl(norm_vec_kernel<T, NT, 1>, grid, block, 0, s, p);
-    if constexpr (kFrom <= 2)
-        if (each == 2) return launch_pdl(norm_vec_kernel<T, NT, 2>, grid, block, 0, s, p);
-    if (each == 3) return launch_pdl(norm_vec_kernel<T, NT, 3>, grid, block, 0, s, p);
-    return launch_pdl(norm_vec_kernel<T, NT, 4>, grid, block, 0, s, p);
+    return launch_pdl(norm_vec_kernel<T, NT, kFrom>, dim3(cdiv(p.T, kRows)), dim3(NT == 32 ? 256 : NT), 0, s, p);
 }
 
 template <typename T>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s)
 {
     if (vec_rows(p)) {
-        // the fewest threads that hold a row in kVecMax pieces each
-        if (p.N <= 32 * 8 * kVecMax) return launch_vec<T, 32, 1>(p, s);
-        if (p.N <= 128 * 8 * kVecMax) return launch_vec<T, 128, 2>(p, s);
-        if (p.N <= 256 * 8 * kVecMax) return launch_vec<T, 256, 3>(p, s);
-        if (p.N <= 512 * 8 * kVecMax) return launch_vec<T, 512, 3>(p, s);
-        return launch_vec<T, 1024, 3>(p, s);
+        // a warp while a row fits one; wider ones two pieces a thread, or three where two would idle many threads
+        if (p.N <= 1024) return launch_vec<T, 32, 1, 4>(p, s);
+        if (p.N <= 2048) return launch_vec<T, 128, 2, 2>(p, s);
+        if (p.N <= 6144) return launch_vec<T, 256, 2, 3>(p, s);
+        if (p.N <= 12288) return launch_vec<T, 512, 2, 3>(p, s);
+        return launch_vec<T, 1024, 2, 4>(p, s);
     }
     static std::atomic<uint64_t> admitted{0};
     const cudaError_t e = admit_smem(norm_any_kernel<T>, kNormMaxN * sizeof(float), admitted);

@@ -13,7 +13,7 @@
 //   kind::f16 widening: byte ^ 0x80 put under the exponent of 1024 is 1024 + (w + 128) in fp16, less 1152 is w.
 //
 // Warps: 0 copies (TMA ring of 128-wide steps of K), 1 issues MMAs (first CTA of a pair), 2-9 widen (a quarter of the
-// lanes and half of the step each, into one of two slots), 10-13 take finished sums out (one of two accumulators).
+// lanes and half of the step each, into a slot of tensor memory), 10-13 take finished sums out (one of two accumulators).
 // Tiles that would leave SMs idle are split along K over the pairs of a cluster, which add up their sums through
 // distributed shared memory in a fixed order.
 // The kernel is launched without programmatic dependence: with it, calls that fill every SM with pairs, made back to back
@@ -42,21 +42,25 @@ constexpr int kMostStages = 10;
 constexpr int kMostSplit = 4;                         // pairs of a cluster
 constexpr int kThreads = 14 * 32;
 constexpr int kWideners = 8, kFirstWidener = 2, kFirstOut = 10;
-constexpr uint32_t kTmemCols = 512;                   // accumulators at 0 and 192, widened weights at 384 and 448
-constexpr uint32_t kWCol = 2 * kMostRows, kWCols = kStep / 2;
+// Two accumulators of a column a row first, then slots for the widened weights of 64 of K: as many as there is room for, an
+// even number. A slot is filled again some 1350 cycles after its MMAs were issued (their completion, the store, two
+// barriers between the CTAs), so slots in plenty keep the MMAs going: with two of 128 of K the head of 128 rows took 130 us.
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSlotCols = 32, kMostSlots = 8;
 constexpr unsigned long long kDrainNs = 4000000000ull;   // own copies and MMAs land long before
 
 // Barriers, from the ring's end on
-enum Bar { kFull = 0, kDone = kMostStages, kReady = 2 * kMostStages, kSumFull = kReady + 2, kSumEmpty = kSumFull + 2,
-           kFin = kSumEmpty + 2, kBars = kFin + 1 };
+enum Bar { kFull = 0, kDone = kMostStages, kReady = 2 * kMostStages, kFree = kReady + kMostSlots,
+           kSumFull = kFree + kMostSlots, kSumEmpty = kSumFull + 2, kFin = kSumEmpty + 2, kBars = kFin + 1 };
 constexpr uint32_t kMiscBytes = kBars * 8 + 8 + 4 * kMostRows * 8;
 constexpr uint32_t kSmem = kRingBytes + 1024 + kMiscBytes;
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-static_assert(kWCol + 2 * kWCols <= kTmemCols, "tensor memory");
+static_assert(2 * kMostRows + 4 * kSlotCols <= kTmemCols && kBars % 2 == 1, "tensor memory; words after the barriers");
 
 struct LinearPlan {
     int rows;        // of x a tile, a multiple of 32
     int stages;
+    int slots;       // of widened weights
     int split;       // pairs along K
     int band;        // tiles of rows that share a pass over the channels
     int x_pitch;     // halves
@@ -305,8 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kFull + i), 1);
             mbar_init(bar(kDone + i), 1);
         }
+        for (int i = 0; i < kMostSlots; ++i) {
+            mbar_init(bar(kReady + i), kWideners);   // four warps of each CTA
+            mbar_init(bar(kFree + i), 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kReady + i), 2 * kWideners);
             mbar_init(bar(kSumFull + i), 1);
             mbar_init(bar(kSumEmpty + i), 2 * 4);
         }
@@ -331,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int k_lo = (int)((long long)all * (rank >> 1) / g.split), k_hi = (int)((long long)all * ((rank >> 1) + 1) / g.split);
     const uint32_t box = (uint32_t)g.rows / 2 * 128;       // bytes of 64 channels of K of this CTA's rows of x
     const uint32_t stage_bytes = kWBytes + 2 * box;
+    const uint32_t w_slots = tmem + 2 * g.rows;
 
     if (warp == 0) {
         // ---------------- copies
@@ -371,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---------------- MMAs, by the first CTA of a pair
         if (half == 0) {
-            int st = 0, it = 0, n = 0;
+            int st = 0, it = 0, slot = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (long long i = tile0; i < count && ok; i += hop, ++it) {
                 const Tile t = tiles.at(i);
@@ -379,17 +388,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it >= 2 && !wait.warp(bar(kSumEmpty + b), ((it >> 1) - 1) & 1u)) break;
                 tc5::fence_after();
                 const uint32_t idesc = (1u << 4) | ((uint32_t)(t.cols >> 3) << 17) | ((2u * kChannels >> 4) << 24);
-                const uint32_t d = tmem + b * kMostRows;
-                for (int k = k_lo; k < k_hi; ++k, ++n) {
-                    const int a = n & 1;
-                    if (!wait.warp(bar(kReady + a), (n >> 1) & 1u)) {
-                        ok = false;
-                        break;
+                const uint32_t d = tmem + b * g.rows;
+                for (int k = k_lo; k < k_hi && ok; ++k) {
+                    const uint32_t x = ring + st * stage_bytes + kWBytes;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        if (!wait.warp(bar(kReady + slot), phase)) {
+                            ok = false;
+                            break;
+                        }
+                        tc5::fence_after();
+                        pair_mma4(d, w_slots + slot * kSlotCols, tc5::desc_sw128(x + part * box), idesc, (k - k_lo) | part);
+                        pair_commit(bar(kFree + slot), both);
+                        if (++slot == g.slots) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    tc5::fence_after();
-                    const uint32_t x = ring + st * stage_bytes + kWBytes, w = tmem + kWCol + a * kWCols;
-                    pair_mma4(d, w, tc5::desc_sw128(x), idesc, k != k_lo);
-                    pair_mma4(d, w + 32, tc5::desc_sw128(x + box), idesc, 1u);
+                    if (!ok) break;
                     pair_commit(bar(kDone + st), both);
                     if (++st == g.stages) st = 0;
                 }
@@ -403,13 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- widening: lane 32 (warp % 4) + lane, half `part` of the step
         const int part = (warp - kFirstWidener) >> 2;
         const uint32_t row = (uint32_t)(warp & 3) * 32 + lane;
-        const uint32_t slot = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kWCol + part * 32;
+        const uint32_t lanes = w_slots + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ready = at_rank(bar(kReady), first);
-        int st = 0, n = 0, back = 0;                       // back: the stage of two steps ago
-        uint32_t phase = 0, back_phase = 0;
-        bool ok = true;
+        int st = 0, slot = part;                           // part 0 fills the even slots, part 1 the odd ones
+        uint32_t phase = 0, refill = 1;                    // refill: of the slot's release, none the first time round
+        bool ok = true, used = false;
         for (long long i = tile0; i < count && ok; i += hop) {
-            for (int k = k_lo; k < k_hi; ++k, ++n) {
+            for (int k = k_lo; k < k_hi; ++k) {
                 if (!wait.warp(bar(kFull + st), phase)) {
                     ok = false;
                     break;
@@ -425,24 +441,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4(q.z, o[4], o[5]);
                     widen4(q.w, o[6], o[7]);
                 }
-                if (n >= 2) {
-                    // the MMAs of two steps ago have read this slot
-                    if (!wait.warp(bar(kDone + back), back_phase)) {
+                if (used) {
+                    // the MMAs that read this slot last are done
+                    if (!wait.warp(bar(kFree + slot), refill)) {
                         ok = false;
                         break;
                     }
                     tc5::fence_after();
-                    if (++back == g.stages) {
-                        back = 0;
-                        back_phase ^= 1u;
-                    }
                 }
-                tc5::st16(slot + (n & 1) * kWCols, v[0]);
-                tc5::st16(slot + (n & 1) * kWCols + 16, v[1]);
+                tc5::st16(lanes + slot * kSlotCols, v[0]);
+                tc5::st16(lanes + slot * kSlotCols + 16, v[1]);
                 tc5::wait_st();
                 tc5::fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(ready + 8u * (n & 1));
+                if (lane == 0) arrive_at(ready + 8u * slot);
+                if ((slot += 2) >= g.slots) {
+                    slot = part;
+                    refill ^= 1u;
+                    used = true;
+                }
                 if (++st == g.stages) {
                     st = 0;
                     phase ^= 1u;
@@ -471,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc5::fence_after();
             for (int c0 = 0; c0 < t.cols; c0 += 32) {
                 uint32_t v[32];
-                tc5::ld32(sums + b * kMostRows + c0, v);
+                tc5::ld32(sums + b * g.rows + c0, v);
                 if (g.split > 1) {
                     // the ring is free: every copy has landed and every MMA is done
 #pragma unroll
@@ -597,6 +614,8 @@ cudaError_t launch_tc(const LinearParams& p, void* ws, cudaStream_t s)
     g.rows = p.T >= kMostRows ? kMostRows : (int)align_up((size_t)p.T, 32);
     g.stages = (int)(kRingBytes / (kWBytes + (uint32_t)g.rows * 128));
     if (g.stages > kMostStages) g.stages = kMostStages;
+    g.slots = ((int)kTmemCols - 2 * g.rows) / kSlotCols & ~1;
+    if (g.slots > kMostSlots) g.slots = kMostSlots;
     // a band's rows of x stay in the L2 while the weights pass
     const long long row_bytes = (long long)g.rows * g.x_pitch * 2;
     g.band = (int)(row_bytes > (32ll << 20) ? 1 : row_bytes < (32ll << 10) ? 1024 : (32ll << 20) / row_bytes);

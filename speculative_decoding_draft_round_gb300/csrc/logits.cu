@@ -177,6 +177,40 @@ __device__ __forceinline__ void store_logits(const Logits8<T>& x, T* row, int v0
     }
 }
 
+// -infinity where the bit is 0
+template <typename T>
+__device__ __forceinline__ void hide(Logits8<T>& x, unsigned allowed);
+template <>
+__device__ __forceinline__ void hide<float>(Logits8<float>& x, unsigned allowed)
+{
+#pragma unroll
+    for (int e = 0; e < kAdjEach; ++e)
+        if (!((allowed >> e) & 1u)) x.u[e] = 0xFF800000u;
+}
+template <>
+__device__ __forceinline__ void hide<__nv_bfloat16>(Logits8<__nv_bfloat16>& x, unsigned allowed)
+{
+#pragma unroll
+    for (int i = 0; i < kAdjEach / 2; ++i) {
+        const uint32_t keep = ((allowed >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((allowed >> (2 * i)) & 2u ? 0xFFFF0000u : 0u);
+        x.u[i] = (x.u[i] & keep) | (0xFF80FF80u & ~keep);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ T narrowed(float x);
+template <>
+__device__ __forceinline__ float narrowed<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrowed<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// An id that something bears on: the times it has been put out before the rows, bit 30 if it is known, its biases
+struct Touched {
+    int id;
+    int known;
+    float bias;
+};
+
 // grid (stretches, requests)
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
@@ -185,9 +219,10 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
     __shared__ int s_mask[kAdjMaxS];
     __shared__ int s_bias_id[kAdjThreads];
     __shared__ float s_bias[kAdjThreads];
-    __shared__ int s_base[kAdjThreads / 32 + 1];
+    __shared__ Touched s_list[kAdjStretch];
+    __shared__ int s_touched;
     pdl_enter();
-    const int r = blockIdx.y, tid = threadIdx.x, v0 = blockIdx.x * kAdjStretch;
+    const int r = blockIdx.y, tid = threadIdx.x;
     const bool first = blockIdx.x == 0;
     int keep = p.keep ? p.keep[r] : p.S - 1;
     if (keep < 0 || keep >= p.S) {
@@ -224,10 +259,35 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
     const float rep = factor(p.repetition, 1.f, true), pres = factor(p.presence, 0.f, false),
                 freq = factor(p.frequency, 0.f, false);
     const bool penal = rep != 1.f || pres != 0.f || freq != 0.f;
+    int b0 = 0, b1 = 0;
+    if (p.bias_offsets) {
+        b0 = p.bias_offsets[r];
+        b1 = p.bias_offsets[r + 1];
+        if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
+            if (first && tid == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+            b0 = b1 = 0;
+        }
+    }
+    // the entries of the biases, 256 at a time; all there is for most requests
+    auto fetch = [&](int b) {
+        const int i = b + tid;
+        if (i >= b1) return;
+        const int v = p.bias_token[i];
+        if (first && (v < 0 || v >= p.V)) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
+        s_bias_id[tid] = v < 0 || v >= p.V ? -1 : v;
+        s_bias[tid] = p.bias_value[i];
+    };
+    fetch(b0);
+    __syncthreads();
+    const bool in_place = p.out == p.logits;
+    const size_t base = (size_t)r * p.S * p.V;
+    const T* src = static_cast<const T*>(p.logits) + base;
+    T* dst = static_cast<T*>(p.out) + base;
+    for (int v0 = blockIdx.x * kAdjStretch; v0 < p.V; v0 += gridDim.x * kAdjStretch) {
     // what this thread's ids have been, and what they are given
     int count[kAdjEach];
     float bias[kAdjEach] = {};
-    unsigned prompt = 0u, known = 0u, biased = 0u;       // bits by id
+    unsigned known = 0u, biased = 0u;                    // bits by id
 #pragma unroll
     for (int e = 0; e < kAdjEach; ++e) count[e] = 0;
     if (p.seen && penal) {
@@ -241,7 +301,6 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
                 for (int e = 0; e < kAdjEach; ++e) {
                     const uint32_t c = (w[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
                     count[e] = c & 0x7FFF;
-                    prompt |= (c >> 15) << e;
                     known |= (c != 0u ? 1u : 0u) << e;
                 }
             }
@@ -251,69 +310,56 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
                 const int v = id_of<T, kVec>(v0, e);
                 const uint32_t c = v < p.V ? (uint16_t)__ldg(row + v) : 0u;
                 count[e] = c & 0x7FFF;
-                prompt |= (c >> 15) << e;
                 known |= (c != 0u ? 1u : 0u) << e;
             }
         }
     }
-    if (p.bias_offsets) {
-        const int b0 = p.bias_offsets[r], b1 = p.bias_offsets[r + 1];
-        if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
-            if (first && tid == 0) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
-        } else {
-            // this stretch's entries, 256 looked at a time, in their order
-            for (int b = b0; b < b1; b += kAdjThreads) {
-                const int i = b + tid;
-                const int v = i < b1 ? p.bias_token[i] : -1;
-                if (first && i < b1 && (v < 0 || v >= p.V)) raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
-                const bool here = i < b1 && (unsigned)(v - v0) < (unsigned)kAdjStretch && v < p.V && v >= 0;
-                const unsigned vote = __ballot_sync(0xffffffffu, here);
-                __syncthreads();
-                if ((tid & 31) == 0) s_base[tid >> 5] = __popc(vote);
-                __syncthreads();
-                int at = __popc(vote & ((1u << (tid & 31)) - 1u)), total = 0;
+    for (int b = b0; b < b1; b += kAdjThreads) {
+        if (b1 - b0 > kAdjThreads) {   // more than one load of them: again for each stretch
+            __syncthreads();
+            fetch(b);
+            __syncthreads();
+        }
+        const int n = min(b1 - b, kAdjThreads);
+        for (int k = 0; k < n; ++k) {
+            const int d = s_bias_id[k] - v0;
+            if ((unsigned)d >= (unsigned)kAdjStretch || s_bias_id[k] < 0) continue;
+            const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
+            if (owner == tid) {
+                const float x = s_bias[k];
 #pragma unroll
-                for (int w = 0; w < kAdjThreads / 32; ++w) {
-                    if (w < (tid >> 5)) at += s_base[w];
-                    total += s_base[w];
-                }
-                if (here) {
-                    s_bias_id[at] = v - v0;
-                    s_bias[at] = p.bias_value[i];
-                }
-                __syncthreads();
-                for (int k = 0; k < total; ++k) {
-                    const int d = s_bias_id[k];
-                    const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
-                    if (owner == tid) {
-                        const float x = s_bias[k];
-#pragma unroll
-                        for (int e = 0; e < kAdjEach; ++e)
-                            if (e == slot) bias[e] += x;
-                        biased |= 1u << slot;
-                    }
-                }
+                for (int e = 0; e < kAdjEach; ++e)
+                    if (e == slot) bias[e] += x;
+                biased |= 1u << slot;
             }
         }
     }
+    // the ids that something bears on, into a list: few, and in no thread's way while the rows pass
+    if (tid == 0) s_touched = 0;
     __syncthreads();
+    unsigned touch = known | biased;
+    if (penal)
+        for (int j = 1; j < rows; ++j) {
+            const int d = s_token[j] - v0;
+            if (s_token[j] < 0 || (unsigned)d >= (unsigned)kAdjStretch) continue;
+            if ((kVec ? d / kAdjEach : d % kAdjThreads) == tid) touch |= 1u << (kVec ? d % kAdjEach : d / kAdjThreads);
+        }
+    if (touch) {
+        int at = atomicAdd(&s_touched, __popc(touch));
+#pragma unroll
+        for (int e = 0; e < kAdjEach; ++e)
+            if ((touch >> e) & 1u)
+                s_list[at++] = Touched{id_of<T, kVec>(v0, e), count[e] | (int)((known >> e) & 1u) << 30, bias[e]};
+    }
+    // the rows as they are, less what masks hide
     const bool inside = kVec ? v0 + tid * kAdjEach < p.V : v0 + tid < p.V;
-    if (!inside) return;
-    const bool in_place = p.out == p.logits;
-    const size_t base = (size_t)r * p.S * p.V;
-    const T* src = static_cast<const T*>(p.logits) + base;
-    T* dst = static_cast<T*>(p.out) + base;
-    for (int j0 = 0; j0 < rows; j0 += kAdjRows) {
+    for (int j0 = 0; inside && j0 < rows; j0 += kAdjRows) {
         Logits8<T> x[kAdjRows];
-        unsigned allowed[kAdjRows], near[kAdjRows];
-        unsigned touch = known | biased;
+        unsigned allowed[kAdjRows];
 #pragma unroll
         for (int u = 0; u < kAdjRows; ++u) {
-            const int j = j0 + u;
+            const int j = j0 + u, m = j < rows ? s_mask[j] : -1;
             allowed[u] = 0xFFu;
-            near[u] = 0u;
-            if (j >= rows) continue;
-            const int m = s_mask[j];
             if (m >= 0) {
                 const uint32_t* bits = p.mask + m * p.mask_rs;
                 if constexpr (kVec) {
@@ -327,54 +373,46 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
                     }
                 }
             }
-            const int d = s_token[j] - v0;
-            if (penal && s_token[j] >= 0 && (unsigned)d < (unsigned)kAdjStretch) {
-                const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
-                if (owner == tid) near[u] = 1u << slot;
-            }
-            touch |= near[u];
-            if (allowed[u] != 0u && (!in_place || touch != 0u || allowed[u] != 0xFFu))
+            if (j < rows && allowed[u] != 0u && (!in_place || allowed[u] != 0xFFu))
                 load_logits<T, kVec>(x[u], src + (size_t)j * p.V, v0, p.V);
         }
-        touch = known | biased;
 #pragma unroll
         for (int u = 0; u < kAdjRows; ++u) {
-            const int j = j0 + u;
-            if (j >= rows) continue;
-            if (near[u]) {
-                known |= near[u];
-                touch |= near[u];
-#pragma unroll
-                for (int e = 0; e < kAdjEach; ++e) count[e] += (near[u] >> e) & 1u;
-            }
-            if (touch == 0u && allowed[u] == 0xFFu) {
-                if (!in_place) store_logits<T, kVec>(x[u], dst + (size_t)j * p.V, v0, p.V);
-                continue;
-            }
-#pragma unroll
-            for (int e = 0; e < kAdjEach; ++e) {
-                if (!((allowed[u] >> e) & 1u)) {
-                    set_logit<T>(x[u], e, -INFINITY);
-                } else if ((touch >> e) & 1u) {
-                    float z = logit<T>(x[u], e);
-                    if ((known >> e) & 1u) {
-                        z = z > 0.f ? __fdiv_rn(z, rep) : z * rep;
-                        z = fmaf(-freq, (float)count[e], z);
-                        if (count[e] > 0) z -= pres;
-                    }
-                    if ((biased >> e) & 1u) z += bias[e];
-                    set_logit<T>(x[u], e, z);
-                }
-            }
-            store_logits<T, kVec>(x[u], dst + (size_t)j * p.V, v0, p.V);
+            if (j0 + u >= rows) continue;
+            if (allowed[u] != 0xFFu) hide<T>(x[u], allowed[u]);
+            if (!in_place || allowed[u] != 0xFFu) store_logits<T, kVec>(x[u], dst + (size_t)(j0 + u) * p.V, v0, p.V);
         }
+    }
+    // and the list, a thread an id and row, over what was stored
+    __syncthreads();
+    const int pairs = s_touched * rows;
+    for (int i = tid; i < pairs; i += kAdjThreads) {
+        const int j = i % rows;
+        const Touched w = s_list[i / rows];
+        const int m = s_mask[j];
+        if (m >= 0 && !((__ldg(p.mask + m * p.mask_rs + w.id / 32) >> (w.id % 32)) & 1u)) continue;
+        int n = w.known & 0x3FFFFFFF;
+        if (penal)
+            for (int k = 1; k <= j; ++k) n += s_token[k] == w.id;
+        const size_t at = (size_t)j * p.V + w.id;
+        float z = to_f32<T>(src[at]);
+        if (w.known >> 30 || n > 0) {
+            z = z > 0.f ? __fdiv_rn(z, rep) : z * rep;
+            z = fmaf(-freq, (float)n, z);
+            if (n > 0) z -= pres;
+        }
+        dst[at] = narrowed<T>(z + w.bias);
+    }
+    __syncthreads();
     }
 }
 
 template <typename T>
 cudaError_t launch_adjust(const AdjustParams& p, cudaStream_t s)
 {
-    const dim3 grid(cdiv(p.V, kAdjStretch), p.R);
+    // CTAs of a request take its stretches in turn; some 24 an SM keep the requests' unequal rows level
+    const int stretches = cdiv(p.V, kAdjStretch), most = cdiv(24 * num_sms(), p.R);
+    const dim3 grid(stretches < most ? stretches : most, p.R);
     const uintptr_t where = reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(p.out);
     // rows of whole 16-byte pieces
     if (p.V % 8 == 0 && where % 16 == 0) return launch_pdl(adjust_kernel<T, true>, grid, dim3(kAdjThreads), 0, s, p);
