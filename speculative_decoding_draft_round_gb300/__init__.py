@@ -1048,9 +1048,11 @@ class RoundRunner:
     """Runs sample_block -> schedule -> verify for one workload with persistent
     argument structs, outputs and workspaces (the launch sequence a serving
     loop would replay every round). path selects the sampler's contraction path; the verifier
-    has no resident loop and takes the per-step tensor-core kernels for PATH_RESIDENT."""
+    has no resident loop and takes the per-step tensor-core kernels for PATH_RESIDENT.
+    adjust: adjust_logits' keywords (penalties, biases, masks) for the target's logits, which run_verify then adjusts in
+    place before it verifies them; where they hold a table of seen tokens it adds what was accepted to it."""
 
-    def __init__(self, rnd, *, path=PATH_AUTO, surv_capacity=None, device=None):
+    def __init__(self, rnd, *, path=PATH_AUTO, surv_capacity=None, device=None, adjust=None):
         self.rnd = rnd
         self.path = path
         dev = device or rnd.U.device
@@ -1068,6 +1070,15 @@ class RoundRunner:
                                          bias_first=rnd.bias_first,
                                          path=PATH_TENSOR_CORE if path == PATH_RESIDENT else path)
         self.vws = torch.zeros(workspace_bytes("verify", self.va), dtype=torch.uint8, device=dev)
+        self.ja = self.na = None
+        if adjust is not None:
+            self.adjust = dict(adjust)      # the arguments hold addresses only
+            self.ja = adjust_logits_args(rnd.target, tokens=self.sout["tokens"], keep=self.cout["keep"],
+                                         out={"out": rnd.target}, **adjust)[0]
+            if adjust.get("seen") is not None:
+                self.na = seen_add_args(adjust["seen"], self.sout["tokens"], V=rnd.target.shape[2],
+                                        n=self.vout["accepted"], extra=self.vout["next_token"])
+            self.jws = torch.zeros(256, dtype=torch.uint8, device=dev)
 
     def set_round(self, rnd_index: int):
         self.sa.round = int(rnd_index)
@@ -1092,10 +1103,15 @@ class RoundRunner:
         _call("dspark_schedule", C.byref(self.ca), _ptr(self.cws), self.cws.numel(), s)
 
     def run_verify(self, stream=None):
-        _call("dspark_verify", C.byref(self.va), _ptr(self.vws), self.vws.numel(), _stream(stream))
+        s = _stream(stream)
+        if self.ja is not None:
+            _call("dspark_adjust_logits", C.byref(self.ja), _ptr(self.jws), self.jws.numel(), s)
+        _call("dspark_verify", C.byref(self.va), _ptr(self.vws), self.vws.numel(), s)
+        if self.na is not None:
+            _call("dspark_seen_add", C.byref(self.na), _ptr(self.jws), self.jws.numel(), s)
 
     def check(self, stream=None) -> int:
-        codes = [check(w, stream) for w in (self.sws, self.cws, self.vws)]
+        codes = [check(w, stream) for w in (self.sws, self.cws, self.vws) + ((self.jws,) if self.ja is not None else ())]
         return next((c for c in codes if c), 0)
 
     def results(self) -> dict:

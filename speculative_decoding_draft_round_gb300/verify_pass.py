@@ -20,8 +20,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (_launch, _on, assemble, assemble_args, cache_append, cache_append_args, cache_attend_args, cache_pool, check,
-               lib, qk_norm_rope, qk_norm_rope_args, rope_frequencies, workspace_bytes)
+from . import (_launch, _on, add_norm_quant, assemble, assemble_args, cache_append, cache_append_args, cache_attend_args,
+               cache_pool, check, lib, linear_i8, qk_norm_rope, qk_norm_rope_args, rope_frequencies, workspace_bytes)
 
 
 class VerifyPass:
@@ -137,17 +137,39 @@ class VerifyPass:
 
 
 class ToyTarget:
-    """A small random target model around VerifyPass: embedding, layers of attention with a residual, logits."""
+    """A small random target model around VerifyPass: embedding, layers of attention with a residual, logits. With
+    eight_bit the weights are held in 8 bits and every layer norms and quantises its rows (add_norm_quant, linear_i8)."""
 
-    def __init__(self, vp, V, width, *, seed=0):
+    def __init__(self, vp, V, width, *, seed=0, eight_bit=False):
         g = torch.Generator(device=vp.qkv.device).manual_seed(seed)
         dt, dev = vp.qkv.dtype, vp.qkv.device
         draw = lambda n, m: (torch.randn((n, m), device=dev, generator=g) / n ** 0.5).to(dt)
-        self.vp = vp
+        self.vp, self.eight_bit = vp, eight_bit
         self.embed = (draw(V, width).float() * V ** 0.5).to(dt)
         self.w_qkv = [draw(width, vp.qkv.shape[1]) for _ in range(vp.layers)]
         self.w_out = [draw(vp.Hq * vp.D, width) for _ in range(vp.layers)]
         self.w_logits = draw(width, V)
+        if eight_bit:
+            self.w_qkv, self.w_out = [self._codes(w) for w in self.w_qkv], [self._codes(w) for w in self.w_out]
+            self.w_logits = self._codes(self.w_logits)
+
+    @staticmethod
+    def _codes(w):
+        """A weight [in][out] as codes [out][in] with a scale for each channel."""
+        q = add_norm_quant(w.t().contiguous(), norm=False)
+        return q["codes"], q["scale"]
+
+    def _eight_bit(self, x, layer, n_rows=None):
+        """x [T][width] through all layers; layer(l, codes, scale) is layer l's attention of the rows. Returns the codes
+        and scales of the last norm."""
+        residual = None
+        for l in range(self.vp.layers):
+            q = add_norm_quant(x, residual=residual, n_rows=n_rows)
+            residual = x if residual is None else q["sum"]
+            a = add_norm_quant(layer(l, q["codes"], q["scale"]).flatten(1), norm=False, n_rows=n_rows)
+            x = linear_i8(a["codes"], a["scale"], *self.w_out[l], dtype=x.dtype, n_rows=n_rows)["out"]
+        q = add_norm_quant(x, residual=residual, n_rows=n_rows)
+        return q["codes"], q["scale"]
 
     def prompt(self, tokens, lengths):
         """tokens: the prompts one after the other on the device, lengths: a list of R."""
@@ -159,8 +181,12 @@ class ToyTarget:
         position = torch.arange(len(request), dtype=torch.int32) - offsets[request.long()]
         request, position, offsets, n = (x.to(dev) for x in (request, position, offsets, n))
         x = self.embed[tokens.long()]
-        for l in range(vp.layers):
-            x = x + vp.prompt(l, x @ self.w_qkv[l], request, position, offsets, max(lengths)).flatten(1) @ self.w_out[l]
+        at = (request, position, offsets, max(lengths))
+        if self.eight_bit:
+            self._eight_bit(x, lambda l, c, s: vp.prompt(l, linear_i8(c, s, *self.w_qkv[l], dtype=x.dtype)["out"], *at))
+        else:
+            for l in range(vp.layers):
+                x = x + vp.prompt(l, x @ self.w_qkv[l], *at).flatten(1) @ self.w_out[l]
         vp.advance_by(n)
 
     def logits(self, out):
@@ -168,6 +194,17 @@ class ToyTarget:
         logits after request r's token j (rows past its last admitted token: anything)."""
         vp, b = self.vp, self.vp.batch
         x = self.embed[b["flat_tokens"].clamp(min=0).long()]
+        if self.eight_bit:
+            rows = b["offsets"][-1:]
+
+            def layer(l, codes, scale):
+                linear_i8(codes, scale, *self.w_qkv[l], n_rows=rows, out={"out": vp.qkv})
+                return vp.layer(l)
+
+            # straight to their places; padding has negative ones
+            place = b["flat_request"] * (vp.gamma_max + 1) + b["flat_position"]
+            linear_i8(*self._eight_bit(x, layer, rows), *self.w_logits, out_row=place, n_rows=rows, out={"out": out})
+            return
         for l in range(vp.layers):
             torch.mm(x, self.w_qkv[l], out=vp.qkv)
             x = x + vp.layer(l).flatten(1) @ self.w_out[l]
@@ -175,18 +212,26 @@ class ToyTarget:
         out.copy_((x @ self.w_logits)[at.clamp(max=vp.T - 1).flatten()].view(out.shape))
 
 
-def main():
-    """Rounds of drafting, a verify pass through a random four-layer target, and acceptance."""
-    from . import RoundRunner
+def main(eight_bit=False):
+    """Rounds of drafting, a verify pass through a random four-layer target, and acceptance. eight_bit (--eight-bit): its
+    weights in 8 bits, and a penalty on what its requests have seen."""
+    from . import RoundRunner, seen_add, seen_table
     from .workloads import make_round
 
     R, G, V, rounds = 32, 7, 4096, 6
     rnd = make_round("verify_pass", R, G, V, 256, 512, "bf16", seed=1, device="cuda", u_std=1.0)
-    runner = RoundRunner(rnd)
     vp = VerifyPass(R, G, 4, 16, 4, 128, capacity=1024)
-    target = ToyTarget(vp, V, 512)
+    target = ToyTarget(vp, V, 512, eight_bit=eight_bit)
     lengths = [100 + 17 * r for r in range(R)]
-    target.prompt(torch.randint(0, V, (sum(lengths),), device="cuda"), lengths)
+    prompts = torch.randint(0, V, (sum(lengths),), device="cuda")
+    target.prompt(prompts, lengths)
+    adjust = None
+    if eight_bit:
+        seen = seen_table(R, V)
+        words = torch.nn.utils.rnn.pad_sequence(prompts.to(torch.int32).split(lengths), batch_first=True)
+        seen_add(seen, words, V=V, n=torch.tensor(lengths, dtype=torch.int32, device="cuda"), prompt=True)
+        adjust = dict(seen=seen, repetition=torch.full((R,), 1.2, device="cuda"))
+    runner = RoundRunner(rnd, adjust=adjust)
     for i in range(rounds):
         runner.set_round(i)
         runner.run_draft()
@@ -202,4 +247,6 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    import sys
+
+    main(eight_bit="--eight-bit" in sys.argv)
