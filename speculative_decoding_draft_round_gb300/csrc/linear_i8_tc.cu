@@ -42,20 +42,18 @@ constexpr int kMostStages = 10;
 constexpr int kMostSplit = 4;                         // pairs of a cluster
 constexpr int kThreads = 14 * 32;
 constexpr int kWideners = 8, kFirstWidener = 2, kFirstOut = 10;
-// Two accumulators of a column a row first, then slots for the widened weights of 64 of K: as many as there is room for, an
-// even number. A slot is filled again some 1350 cycles after its MMAs were issued (their completion, the store, two
-// barriers between the CTAs), so slots in plenty keep the MMAs going: with two of 128 of K the head of 128 rows took 130 us.
-constexpr uint32_t kTmemCols = 512;
-constexpr int kSlotCols = 32, kMostSlots = 8;
+// Two accumulators of a column a row first, then slots for a step's widened weights: two, or four where there is room.
+constexpr uint32_t kTmemCols = 512, kSlotCols = kStep / 2;
+constexpr int kMostSlots = 4;
 constexpr unsigned long long kDrainNs = 4000000000ull;   // own copies and MMAs land long before
 
 // Barriers, from the ring's end on
-enum Bar { kFull = 0, kDone = kMostStages, kReady = 2 * kMostStages, kFree = kReady + kMostSlots,
-           kSumFull = kFree + kMostSlots, kSumEmpty = kSumFull + 2, kFin = kSumEmpty + 2, kBars = kFin + 1 };
+enum Bar { kFull = 0, kDone = kMostStages, kReady = 2 * kMostStages, kSumFull = kReady + kMostSlots, kSumEmpty = kSumFull + 2,
+           kFin = kSumEmpty + 2, kBars = kFin + 1 };
 constexpr uint32_t kMiscBytes = kBars * 8 + 8 + 4 * kMostRows * 8;
 constexpr uint32_t kSmem = kRingBytes + 1024 + kMiscBytes;
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-static_assert(2 * kMostRows + 4 * kSlotCols <= kTmemCols && kBars % 2 == 1, "tensor memory; words after the barriers");
+static_assert(2 * kMostRows + 2 * kSlotCols <= kTmemCols && 2 * 128 + 4 * kSlotCols <= kTmemCols, "tensor memory");
 
 struct LinearPlan {
     int rows;        // of x a tile, a multiple of 32
@@ -159,11 +157,14 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+constexpr unsigned long long kShortNs = 1000000;
+
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                        unsigned long long limit_ns)
 {
+    // a try may suspend the warp for a time of its own, so under a short limit tries do not suspend
     const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!(limit_ns < kShortNs ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
@@ -180,7 +181,9 @@ struct Waits {
     unsigned long long limit_ns;
     __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const
     {
-        return mbar_test_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit_ns);
+        // one try that may suspend the warp before the timer is looked at, which takes longer than most waits
+        return mbar_test_wait(bar, parity) || (limit_ns >= kShortNs && mbar_try_wait(bar, parity)) ||
+               wait_slow(bar, parity, abort, status, limit_ns);
     }
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const
     {
@@ -309,10 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kFull + i), 1);
             mbar_init(bar(kDone + i), 1);
         }
-        for (int i = 0; i < kMostSlots; ++i) {
-            mbar_init(bar(kReady + i), kWideners);   // four warps of each CTA
-            mbar_init(bar(kFree + i), 1);
-        }
+        for (int i = 0; i < kMostSlots; ++i) mbar_init(bar(kReady + i), 2 * kWideners);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSumFull + i), 1);
             mbar_init(bar(kSumEmpty + i), 2 * 4);
@@ -368,12 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (*s_abort) {   // copies still in flight land before the CTA leaves
-                for (int back = issued; back > 0; --back) {
-                    const int s = (st - back + g.stages) % g.stages;
-                    // the phase that the stage's last copy ends
-                    drain(bar(kFull + s), s < st ? phase ^ 1u : phase);
-                }
+            // copies still in flight land before the CTA leaves (also where only a later wait of another warp runs out)
+            for (int back = issued; back > 0; --back) {
+                const int s = (st - back + g.stages) % g.stages;
+                // the phase that the stage's last copy ends
+                drain(bar(kFull + s), s < st ? phase ^ 1u : phase);
             }
         }
     } else if (warp == 1) {
@@ -389,25 +388,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc5::fence_after();
                 const uint32_t idesc = (1u << 4) | ((uint32_t)(t.cols >> 3) << 17) | ((2u * kChannels >> 4) << 24);
                 const uint32_t d = tmem + b * g.rows;
-                for (int k = k_lo; k < k_hi && ok; ++k) {
-                    const uint32_t x = ring + st * stage_bytes + kWBytes;
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        if (!wait.warp(bar(kReady + slot), phase)) {
-                            ok = false;
-                            break;
-                        }
-                        tc5::fence_after();
-                        pair_mma4(d, w_slots + slot * kSlotCols, tc5::desc_sw128(x + part * box), idesc, (k - k_lo) | part);
-                        pair_commit(bar(kFree + slot), both);
-                        if (++slot == g.slots) {
-                            slot = 0;
-                            phase ^= 1u;
-                        }
+                for (int k = k_lo; k < k_hi; ++k) {
+                    if (!wait.warp(bar(kReady + slot), phase)) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
+                    tc5::fence_after();
+                    const uint32_t x = ring + st * stage_bytes + kWBytes, w = w_slots + slot * kSlotCols;
+                    pair_mma4(d, w, tc5::desc_sw128(x), idesc, k != k_lo);
+                    pair_mma4(d, w + 32, tc5::desc_sw128(x + box), idesc, 1u);
                     pair_commit(bar(kDone + st), both);
                     if (++st == g.stages) st = 0;
+                    if (++slot == g.slots) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
                 if (ok) pair_commit(bar(kSumFull + b), both);
             }
@@ -419,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- widening: lane 32 (warp % 4) + lane, half `part` of the step
         const int part = (warp - kFirstWidener) >> 2;
         const uint32_t row = (uint32_t)(warp & 3) * 32 + lane;
-        const uint32_t lanes = w_slots + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t lanes = w_slots + ((uint32_t)((warp & 3) * 32) << 16) + part * 32;
         const uint32_t ready = at_rank(bar(kReady), first);
-        int st = 0, slot = part;                           // part 0 fills the even slots, part 1 the odd ones
-        uint32_t phase = 0, refill = 1;                    // refill: of the slot's release, none the first time round
-        bool ok = true, used = false;
+        int st = 0, n = 0, slot = 0, back = 0;             // back: the stage of the step that had the slot before
+        uint32_t phase = 0, back_phase = 0;
+        bool ok = true;
         for (long long i = tile0; i < count && ok; i += hop) {
-            for (int k = k_lo; k < k_hi; ++k) {
+            for (int k = k_lo; k < k_hi; ++k, ++n) {
                 if (!wait.warp(bar(kFull + st), phase)) {
                     ok = false;
                     break;
@@ -441,13 +436,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4(q.z, o[4], o[5]);
                     widen4(q.w, o[6], o[7]);
                 }
-                if (used) {
-                    // the MMAs that read this slot last are done
-                    if (!wait.warp(bar(kFree + slot), refill)) {
+                if (n >= g.slots) {
+                    // that step's MMAs have read the slot
+                    if (!wait.warp(bar(kDone + back), back_phase)) {
                         ok = false;
                         break;
                     }
                     tc5::fence_after();
+                    if (++back == g.stages) {
+                        back = 0;
+                        back_phase ^= 1u;
+                    }
                 }
                 tc5::st16(lanes + slot * kSlotCols, v[0]);
                 tc5::st16(lanes + slot * kSlotCols + 16, v[1]);
@@ -455,11 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc5::fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_at(ready + 8u * slot);
-                if ((slot += 2) >= g.slots) {
-                    slot = part;
-                    refill ^= 1u;
-                    used = true;
-                }
+                if (++slot == g.slots) slot = 0;
                 if (++st == g.stages) {
                     st = 0;
                     phase ^= 1u;
@@ -614,8 +609,7 @@ cudaError_t launch_tc(const LinearParams& p, void* ws, cudaStream_t s)
     g.rows = p.T >= kMostRows ? kMostRows : (int)align_up((size_t)p.T, 32);
     g.stages = (int)(kRingBytes / (kWBytes + (uint32_t)g.rows * 128));
     if (g.stages > kMostStages) g.stages = kMostStages;
-    g.slots = ((int)kTmemCols - 2 * g.rows) / kSlotCols & ~1;
-    if (g.slots > kMostSlots) g.slots = kMostSlots;
+    g.slots = g.rows > 128 ? 2 : kMostSlots;
     // a band's rows of x stay in the L2 while the weights pass
     const long long row_bytes = (long long)g.rows * g.x_pitch * 2;
     g.band = (int)(row_bytes > (32ll << 20) ? 1 : row_bytes < (32ll << 10) ? 1024 : (32ll << 20) / row_bytes);

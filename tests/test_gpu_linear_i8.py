@@ -184,3 +184,32 @@ def test_empty_and_refused():
     with pytest.raises(ds.DsparkError) as e:
         ds.linear_i8(x, xs, w, ws, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
     assert e.value.code == 3
+
+
+@pytest.mark.parametrize("T,K,N", [(20, 2048, 300), (300, 1024, 40000)])
+def test_a_wait_that_runs_out_is_recorded(T, K, N):
+    """Under a limit of 1 ns the call ends with the status, and the next one without it is right."""
+    x, xs, w, ws, _ = _case(T, K, N)
+    args = _dev(x, xs, w, ws)
+    want = ds.linear_i8(*args, path=ds.PATH_CUDA_CORE, dtype=torch.float32)["out"]
+    ds.set_wait_limit(1)
+    try:
+        got = ds.linear_i8(*args, path=ds.PATH_TENSOR_CORE, dtype=torch.float32)
+        assert ds.check(got["workspace"]) == ds.ERR_TIMEOUT
+    finally:
+        ds.set_wait_limit(0)
+    for _ in range(3):
+        got = ds.linear_i8(*args, path=ds.PATH_TENSOR_CORE, dtype=torch.float32)
+        assert ds.check(got["workspace"]) == 0 and torch.equal(got["out"], want)
+
+
+def test_calls_that_fill_every_sm_back_to_back():
+    """Tiles by the hundred, several to a pair, in calls that nothing waits between."""
+    x, xs, w, ws, _ = _case(700, 640, 8000)
+    args = _dev(x, xs, w, ws)
+    a, out = ds.linear_i8_args(*args, dtype=torch.float32)
+    work = torch.zeros(ds.workspace_bytes("linear_i8", a), dtype=torch.uint8, device=DEV)
+    want = ds.linear_i8(*args, path=ds.PATH_CUDA_CORE, dtype=torch.float32)["out"]
+    for _ in range(300):
+        ds.linear_i8(*args, out=out, workspace=work)
+    assert ds.check(work) == 0 and torch.equal(out["out"], want)
