@@ -1,10 +1,11 @@
 // logits.cu -- penalties for tokens seen, biases and grammar masks on rows of logits (dspark_adjust_logits), and the
 // table of what each request has seen (dspark_seen_add).
 //
-// A request's rows share its row of the table and its biases: a CTA takes a stretch of the vocabulary of one request,
-// keeps both for its ids in registers, and runs through the rows, counting a drafted token when it has passed its row.
-// The bytes bound it: a row is read and written once; in place, only 16-byte pieces that change are written, pieces that
-// nothing bears on are not read, and pieces that a mask hides whole are written without being read.
+// A request's rows share its row of the table and its biases: a CTA takes stretches of the vocabulary of one request, lists
+// the ids of a stretch that something bears on, runs the rows past as they are, and goes through the list afterwards, a
+// thread an id and row. (Adjusted in the threads that load them, those ids held up whole warps: 128 x 17 x 151936 in bf16
+// took 236 us, 176 now, of 109 at the copy's rate; 28 warps an SM wait for loads.) In place, only 16-byte pieces that a
+// mask changes and listed ids are written, and pieces that a mask hides whole are written without being read.
 #include <float.h>
 
 #include "common.cuh"
@@ -46,7 +47,8 @@ __device__ __forceinline__ void mark_one(int16_t* at)
     atomicOr(reinterpret_cast<unsigned*>(a & ~uintptr_t(3)), a & 2 ? 0x80000000u : 0x8000u);
 }
 
-// grid (stretches of the vocabulary, requests). A fresh row is written whole, each CTA the stretch whose tokens it has
+// grid (stretches of the vocabulary, requests). 128 fresh rows of 151936 with prompts of up to 4096 tokens take 20 us: the
+// 39 MB are 6, the rest is each stretch's pass over the tokens. A fresh row is written whole, each CTA the stretch whose tokens it has
 // counted in shared memory; otherwise the CTAs of a request share its tokens, and each goes into the row by an atomic.
 __global__ void __launch_bounds__(kSeenThreads) seen_add_kernel(SeenParams p)
 {
