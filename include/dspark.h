@@ -578,8 +578,8 @@ dspark_status dspark_linear_i8(const dspark_linear_i8_args* args, void* workspac
  * number of times it has been put out (32767 at most). For every request r, rows of zeros first where fresh[r] != 0, the
  * tokens tokens[r][0 .. n[r] - 1] and extra[r] are added: to the counts, or with prompt = 1 by setting bit 15. After
  * dspark_verify: tokens with n = accepted and extra = next_token. A token outside 0 .. V-1 or n[r] outside 0 .. W is
- * recorded (DSPARK_ERR_DEVICE_INPUT) and skipped, or clamped. Words from V to seen_stride are zeroed with a fresh row and
- * otherwise left as they are.
+ * recorded (DSPARK_ERR_DEVICE_INPUT) and skipped, or clamped. A row has V words rounded up to a multiple of 8; those past V are
+ * zeroed with a fresh row and otherwise left as they are, and what lies between the rows is not touched.
  */
 typedef struct {
     uint32_t struct_size;

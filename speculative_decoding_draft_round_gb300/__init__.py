@@ -963,6 +963,9 @@ def seen_add_args(seen, tokens, *, V, n=None, extra=None, fresh=None, prompt=Fal
     sp, s_rs = _rows2(seen, "seen", torch.int16, seen.shape)
     if not 0 < V <= seen.shape[1]:
         raise ValueError("V is %d, seen has %d words a request" % (V, seen.shape[1]))
+    if -(-V // 8) * 8 > seen.shape[1]:
+        raise DsparkError("dspark_seen_add", 1, "%d tokens need their number rounded up to 8 in words a request, seen has %d"
+                          % (V, seen.shape[1]))
     W, tp, t_rs = 0, None, 0
     if tokens is not None:
         W = tokens.shape[1] if tokens.dim() == 2 else 0

@@ -19,6 +19,8 @@ namespace {
 
 constexpr int kSeenThreads = 256;
 constexpr int kSeenStretch = 8192;       // ids whose new counts a CTA holds: 32 KB
+constexpr int kSeenMarks = 32768;        // ids whose marks it holds, a bit each: 4 KB (with stretches of 8192 for both the
+                                         // prompts below took 20 us, each stretch's pass over the tokens most of it)
 
 __device__ __forceinline__ int seen_tokens(const SeenParams& p, int r, bool report)
 {
@@ -72,27 +74,30 @@ __global__ void __launch_bounds__(kSeenThreads) seen_add_kernel(SeenParams p)
         }
         return;
     }
-    const int v0 = blockIdx.x * kSeenStretch;
-    for (int i = tid; i < kSeenStretch; i += kSeenThreads) s_new[i] = 0;
+    const int stretch = p.prompt ? kSeenMarks : kSeenStretch, v0 = blockIdx.x * stretch;
+    for (int i = tid; i < (p.prompt ? kSeenMarks / 32 : kSeenStretch); i += kSeenThreads) s_new[i] = 0;
     __syncthreads();
 #pragma unroll 4
     for (int i = tid; i < all; i += kSeenThreads) {
-        const int v = token(i);
-        if ((unsigned)(v - v0) < (unsigned)kSeenStretch && v < p.V) {
-            if (p.prompt) s_new[v - v0] = 1;
-            else atomicAdd(&s_new[v - v0], 1);
+        const int v = token(i), d = v - v0;
+        if ((unsigned)d < (unsigned)stretch && v < p.V) {
+            if (p.prompt) atomicOr(&s_new[d >> 5], 1 << (d & 31));
+            else atomicAdd(&s_new[d], 1);
         } else if (blockIdx.x == 0 && (unsigned)v >= (unsigned)p.V) {
             raise_status(p.status, DSPARK_ERR_DEVICE_INPUT);
         }
     }
     __syncthreads();
-    const int words = (int)min((long long)kSeenStretch, (long long)p.seen_rs - v0);
+    const int words = min(stretch, ((p.V + 7) & ~7) - v0);   // a row's own words: what lies behind them is another's
     for (int i = tid * 8; i < words; i += kSeenThreads * 8) {
         uint32_t w[4];
+        const uint32_t marks = p.prompt ? (uint32_t)s_new[i >> 5] >> (i & 31) : 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int a = s_new[i + 2 * j], b = s_new[i + 2 * j + 1];
-            w[j] = p.prompt ? (a ? 0x8000u : 0u) | (b ? 0x80000000u : 0u) : (uint32_t)min(a, 32767) | (uint32_t)min(b, 32767) << 16;
+            if (p.prompt)
+                w[j] = ((marks >> (2 * j)) & 1u) << 15 | ((marks >> (2 * j + 1)) & 1u) << 31;
+            else
+                w[j] = (uint32_t)min(s_new[i + 2 * j], 32767) | (uint32_t)min(s_new[i + 2 * j + 1], 32767) << 16;
         }
         *reinterpret_cast<uint4*>(row + v0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -286,126 +291,126 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
     const T* src = static_cast<const T*>(p.logits) + base;
     T* dst = static_cast<T*>(p.out) + base;
     for (int v0 = blockIdx.x * kAdjStretch; v0 < p.V; v0 += gridDim.x * kAdjStretch) {
-    // what this thread's ids have been, and what they are given
-    int count[kAdjEach];
-    float bias[kAdjEach] = {};
-    unsigned known = 0u, biased = 0u;                    // bits by id
+        // what this thread's ids have been, and what they are given
+        int count[kAdjEach];
+        float bias[kAdjEach] = {};
+        unsigned known = 0u, biased = 0u;                    // bits by id
 #pragma unroll
-    for (int e = 0; e < kAdjEach; ++e) count[e] = 0;
-    if (p.seen && penal) {
-        const int16_t* row = p.seen + r * p.seen_rs;
-        if constexpr (kVec) {
-            const int v = v0 + tid * kAdjEach;
-            if (v < p.V) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + v));
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        for (int e = 0; e < kAdjEach; ++e) count[e] = 0;
+        if (p.seen && penal) {
+            const int16_t* row = p.seen + r * p.seen_rs;
+            if constexpr (kVec) {
+                const int v = v0 + tid * kAdjEach;
+                if (v < p.V) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + v));
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < kAdjEach; ++e) {
+                        const uint32_t c = (w[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
+                        count[e] = c & 0x7FFF;
+                        known |= (c != 0u ? 1u : 0u) << e;
+                    }
+                }
+            } else {
 #pragma unroll
                 for (int e = 0; e < kAdjEach; ++e) {
-                    const uint32_t c = (w[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
+                    const int v = id_of<T, kVec>(v0, e);
+                    const uint32_t c = v < p.V ? (uint16_t)__ldg(row + v) : 0u;
                     count[e] = c & 0x7FFF;
                     known |= (c != 0u ? 1u : 0u) << e;
                 }
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kAdjEach; ++e) {
-                const int v = id_of<T, kVec>(v0, e);
-                const uint32_t c = v < p.V ? (uint16_t)__ldg(row + v) : 0u;
-                count[e] = c & 0x7FFF;
-                known |= (c != 0u ? 1u : 0u) << e;
+        }
+        for (int b = b0; b < b1; b += kAdjThreads) {
+            if (b1 - b0 > kAdjThreads) {   // more than one load of them: again for each stretch
+                __syncthreads();
+                fetch(b);
+                __syncthreads();
             }
-        }
-    }
-    for (int b = b0; b < b1; b += kAdjThreads) {
-        if (b1 - b0 > kAdjThreads) {   // more than one load of them: again for each stretch
-            __syncthreads();
-            fetch(b);
-            __syncthreads();
-        }
-        const int n = min(b1 - b, kAdjThreads);
-        for (int k = 0; k < n; ++k) {
-            const int d = s_bias_id[k] - v0;
-            if ((unsigned)d >= (unsigned)kAdjStretch || s_bias_id[k] < 0) continue;
-            const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
-            if (owner == tid) {
-                const float x = s_bias[k];
+            const int n = min(b1 - b, kAdjThreads);
+            for (int k = 0; k < n; ++k) {
+                const int d = s_bias_id[k] - v0;
+                if ((unsigned)d >= (unsigned)kAdjStretch || s_bias_id[k] < 0) continue;
+                const int owner = kVec ? d / kAdjEach : d % kAdjThreads, slot = kVec ? d % kAdjEach : d / kAdjThreads;
+                if (owner == tid) {
+                    const float x = s_bias[k];
 #pragma unroll
-                for (int e = 0; e < kAdjEach; ++e)
-                    if (e == slot) bias[e] += x;
-                biased |= 1u << slot;
-            }
-        }
-    }
-    // the ids that something bears on, into a list: few, and in no thread's way while the rows pass
-    if (tid == 0) s_touched = 0;
-    __syncthreads();
-    unsigned touch = known | biased;
-    if (penal)
-        for (int j = 1; j < rows; ++j) {
-            const int d = s_token[j] - v0;
-            if (s_token[j] < 0 || (unsigned)d >= (unsigned)kAdjStretch) continue;
-            if ((kVec ? d / kAdjEach : d % kAdjThreads) == tid) touch |= 1u << (kVec ? d % kAdjEach : d / kAdjThreads);
-        }
-    if (touch) {
-        int at = atomicAdd(&s_touched, __popc(touch));
-#pragma unroll
-        for (int e = 0; e < kAdjEach; ++e)
-            if ((touch >> e) & 1u)
-                s_list[at++] = Touched{id_of<T, kVec>(v0, e), count[e] | (int)((known >> e) & 1u) << 30, bias[e]};
-    }
-    // the rows as they are, less what masks hide
-    const bool inside = kVec ? v0 + tid * kAdjEach < p.V : v0 + tid < p.V;
-    for (int j0 = 0; inside && j0 < rows; j0 += kAdjRows) {
-        Logits8<T> x[kAdjRows];
-        unsigned allowed[kAdjRows];
-#pragma unroll
-        for (int u = 0; u < kAdjRows; ++u) {
-            const int j = j0 + u, m = j < rows ? s_mask[j] : -1;
-            allowed[u] = 0xFFu;
-            if (m >= 0) {
-                const uint32_t* bits = p.mask + m * p.mask_rs;
-                if constexpr (kVec) {
-                    allowed[u] = __ldg(reinterpret_cast<const uint8_t*>(bits) + (v0 + tid * kAdjEach) / 8);
-                } else {
-                    allowed[u] = 0u;
-#pragma unroll
-                    for (int e = 0; e < kAdjEach; ++e) {
-                        const int v = id_of<T, kVec>(v0, e);
-                        if (v < p.V) allowed[u] |= ((__ldg(bits + v / 32) >> (v % 32)) & 1u) << e;
-                    }
+                    for (int e = 0; e < kAdjEach; ++e)
+                        if (e == slot) bias[e] += x;
+                    biased |= 1u << slot;
                 }
             }
-            if (j < rows && allowed[u] != 0u && (!in_place || allowed[u] != 0xFFu))
-                load_logits<T, kVec>(x[u], src + (size_t)j * p.V, v0, p.V);
         }
-#pragma unroll
-        for (int u = 0; u < kAdjRows; ++u) {
-            if (j0 + u >= rows) continue;
-            if (allowed[u] != 0xFFu) hide<T>(x[u], allowed[u]);
-            if (!in_place || allowed[u] != 0xFFu) store_logits<T, kVec>(x[u], dst + (size_t)(j0 + u) * p.V, v0, p.V);
-        }
-    }
-    // and the list, a thread an id and row, over what was stored
-    __syncthreads();
-    const int pairs = s_touched * rows;
-    for (int i = tid; i < pairs; i += kAdjThreads) {
-        const int j = i % rows;
-        const Touched w = s_list[i / rows];
-        const int m = s_mask[j];
-        if (m >= 0 && !((__ldg(p.mask + m * p.mask_rs + w.id / 32) >> (w.id % 32)) & 1u)) continue;
-        int n = w.known & 0x3FFFFFFF;
+        // the ids that something bears on, into a list: few, and in no thread's way while the rows pass
+        if (tid == 0) s_touched = 0;
+        __syncthreads();
+        unsigned touch = known | biased;
         if (penal)
-            for (int k = 1; k <= j; ++k) n += s_token[k] == w.id;
-        const size_t at = (size_t)j * p.V + w.id;
-        float z = to_f32<T>(src[at]);
-        if (w.known >> 30 || n > 0) {
-            z = z > 0.f ? __fdiv_rn(z, rep) : z * rep;
-            z = fmaf(-freq, (float)n, z);
-            if (n > 0) z -= pres;
+            for (int j = 1; j < rows; ++j) {
+                const int d = s_token[j] - v0;
+                if (s_token[j] < 0 || (unsigned)d >= (unsigned)kAdjStretch) continue;
+                if ((kVec ? d / kAdjEach : d % kAdjThreads) == tid) touch |= 1u << (kVec ? d % kAdjEach : d / kAdjThreads);
+            }
+        if (touch) {
+            int at = atomicAdd(&s_touched, __popc(touch));
+#pragma unroll
+            for (int e = 0; e < kAdjEach; ++e)
+                if ((touch >> e) & 1u)
+                    s_list[at++] = Touched{id_of<T, kVec>(v0, e), count[e] | (int)((known >> e) & 1u) << 30, bias[e]};
         }
-        dst[at] = narrowed<T>(z + w.bias);
-    }
-    __syncthreads();
+        // the rows as they are, less what masks hide
+        const bool inside = kVec ? v0 + tid * kAdjEach < p.V : v0 + tid < p.V;
+        for (int j0 = 0; inside && j0 < rows; j0 += kAdjRows) {
+            Logits8<T> x[kAdjRows];
+            unsigned allowed[kAdjRows];
+#pragma unroll
+            for (int u = 0; u < kAdjRows; ++u) {
+                const int j = j0 + u, m = j < rows ? s_mask[j] : -1;
+                allowed[u] = 0xFFu;
+                if (m >= 0) {
+                    const uint32_t* bits = p.mask + m * p.mask_rs;
+                    if constexpr (kVec) {
+                        allowed[u] = __ldg(reinterpret_cast<const uint8_t*>(bits) + (v0 + tid * kAdjEach) / 8);
+                    } else {
+                        allowed[u] = 0u;
+#pragma unroll
+                        for (int e = 0; e < kAdjEach; ++e) {
+                            const int v = id_of<T, kVec>(v0, e);
+                            if (v < p.V) allowed[u] |= ((__ldg(bits + v / 32) >> (v % 32)) & 1u) << e;
+                        }
+                    }
+                }
+                if (j < rows && allowed[u] != 0u && (!in_place || allowed[u] != 0xFFu))
+                    load_logits<T, kVec>(x[u], src + (size_t)j * p.V, v0, p.V);
+            }
+#pragma unroll
+            for (int u = 0; u < kAdjRows; ++u) {
+                if (j0 + u >= rows) continue;
+                if (allowed[u] != 0xFFu) hide<T>(x[u], allowed[u]);
+                if (!in_place || allowed[u] != 0xFFu) store_logits<T, kVec>(x[u], dst + (size_t)(j0 + u) * p.V, v0, p.V);
+            }
+        }
+        // and the list, a thread an id and row, over what was stored
+        __syncthreads();
+        const int pairs = s_touched * rows;
+        for (int i = tid; i < pairs; i += kAdjThreads) {
+            const int j = i % rows;
+            const Touched w = s_list[i / rows];
+            const int m = s_mask[j];
+            if (m >= 0 && !((__ldg(p.mask + m * p.mask_rs + w.id / 32) >> (w.id % 32)) & 1u)) continue;
+            int n = w.known & 0x3FFFFFFF;
+            if (penal)
+                for (int k = 1; k <= j; ++k) n += s_token[k] == w.id;
+            const size_t at = (size_t)j * p.V + w.id;
+            float z = to_f32<T>(src[at]);
+            if (w.known >> 30 || n > 0) {
+                z = z > 0.f ? __fdiv_rn(z, rep) : z * rep;
+                z = fmaf(-freq, (float)n, z);
+                if (n > 0) z -= pres;
+            }
+            dst[at] = narrowed<T>(z + w.bias);
+        }
+        __syncthreads();
     }
 }
 
@@ -425,7 +430,7 @@ cudaError_t launch_adjust(const AdjustParams& p, cudaStream_t s)
 
 cudaError_t launch_seen_add(const SeenParams& p, cudaStream_t s)
 {
-    const dim3 grid(cdiv(p.seen_rs, kSeenStretch), p.R);
+    const dim3 grid(cdiv(p.V, p.prompt ? kSeenMarks : kSeenStretch), p.R);
     const cudaError_t e = launch_pdl(seen_add_kernel, grid, dim3(kSeenThreads), 0, s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

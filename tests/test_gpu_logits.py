@@ -251,3 +251,16 @@ def test_many_biases_of_one_token_add_up_in_order():
     for t, v in zip(token, value):
         want[t] = np.float32(want[t] + v)
     assert np.array_equal(out, want)
+
+
+def test_fresh_rows_end_with_their_words():
+    """Clearing the rows of a view leaves what lies between them, before the first and behind the last as it was."""
+    wide = torch.full((5, 96), 7, dtype=torch.int16, device=DEV)
+    view = wide[1:4, 40:80]
+    ds.seen_add(view, _i32([[3], [32], [0]]), V=33, fresh=torch.ones(3, dtype=torch.uint8, device=DEV))
+    want = np.full((5, 96), 7, np.int16)
+    want[1:4, 40:80] = 0
+    want[[1, 2, 3], [43, 72, 40]] = 1
+    assert np.array_equal(wide.cpu().numpy(), want)
+    with pytest.raises(ds.DsparkError):
+        ds.seen_add(wide[:, 40:76], None, V=33)
