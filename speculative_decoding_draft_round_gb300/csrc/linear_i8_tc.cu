@@ -18,8 +18,8 @@
 // distributed shared memory in a fixed order.
 // Measured, layout included: 6007 x 8192 x 8192 rows x K x channels 459 to 497 us (the product alone 435, 1850 TFLOP/s of
 // 1926 that the library's bf16 product reaches), 2176 x 4096 x 6144 93 us of 57 (3.8 tiles a pair), 128 x 4096 x 151936
-// 133 to 141 us of 98 (a step's 256 lines of 128 bytes keep the copy engine some 900 cycles, at any number of slots and
-// widening warps), 16 x 4096 x 6144 16.5 us (two launches).
+// 133 to 141 us of 98 (a step takes 900 cycles from copy to release, at any number of slots and widening warps, with x
+// shared between pairs or not; MMAs are 512 of them), 16 x 4096 x 6144 16.5 us (two launches).
 // The kernel is launched without programmatic dependence: with it, calls that fill every SM with pairs, made back to back
 // by the thousand, came to a stop (none did in 4000 without).
 // Every wait is bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT, the CTAs stop issuing, let

@@ -19,8 +19,8 @@ namespace {
 
 constexpr int kSeenThreads = 256;
 constexpr int kSeenStretch = 8192;       // ids whose new counts a CTA holds: 32 KB
-constexpr int kSeenMarks = 32768;        // ids whose marks it holds, a bit each: 4 KB (with stretches of 8192 for both the
-                                         // prompts below took 20 us, each stretch's pass over the tokens most of it)
+constexpr int kSeenMarks = 32768;        // ids whose marks it holds, a bit each: 4 KB (with stretches of 8192 the
+                                         // prompts below took 20 us, each one's pass over the tokens most of it)
 
 __device__ __forceinline__ int seen_tokens(const SeenParams& p, int r, bool report)
 {
@@ -49,8 +49,8 @@ __device__ __forceinline__ void mark_one(int16_t* at)
     atomicOr(reinterpret_cast<unsigned*>(a & ~uintptr_t(3)), a & 2 ? 0x80000000u : 0x8000u);
 }
 
-// grid (stretches of the vocabulary, requests). 128 fresh rows of 151936 with prompts of up to 4096 tokens take 20 us: the
-// 39 MB are 6, the rest is each stretch's pass over the tokens. A fresh row is written whole, each CTA the stretch whose tokens it has
+// grid (stretches of the vocabulary, requests). 128 fresh rows of 151936 with prompts of up to 4096 tokens take 8 us, the 39 MB
+// 6 of them. A fresh row is written whole, each CTA the stretch whose tokens it has
 // counted in shared memory; otherwise the CTAs of a request share its tokens, and each goes into the row by an atomic.
 __global__ void __launch_bounds__(kSeenThreads) seen_add_kernel(SeenParams p)
 {
