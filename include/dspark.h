@@ -269,6 +269,10 @@ dspark_status dspark_schedule(const dspark_schedule_args* args, void* workspace,
  *   target row j (lowest index on ties); the first mismatch is replaced by that arg-max
  *   (resampled 1), and when every admitted token matches, the arg-max of row keep[r] is the
  *   bonus token (resampled 0). No random numbers are drawn.
+ * target_ready = 1 lets row 0 of the target be read while the kernel before this call still runs. It is for calls that
+ *   directly follow dspark_schedule on their stream, the target having been written before dspark_sample_block; a
+ *   target written later (by the head's product or dspark_adjust_logits) needs 0. struct_size may be that of the struct
+ *   without target_ready and reserved, which are 0 then.
  */
 typedef struct {
     uint32_t struct_size;
@@ -296,6 +300,8 @@ typedef struct {
     int32_t* next_token;         /* out [R] */
     uint8_t* resampled;          /* out [R] */
     const float* a_rows;         /* [R][gamma_max][r] bias operands from dspark_sample_block, or NULL */
+    int32_t target_ready;        /* 1: target was written before the kernel this call follows began (below) */
+    int32_t reserved;            /* 0 */
 } dspark_verify_args;
 
 dspark_status dspark_verify_workspace_size(const dspark_verify_args* args, size_t* bytes);

@@ -83,6 +83,7 @@ class VerifyArgs(C.Structure):
         ("draft_lse", _vp), ("draft_logit", _vp), ("keep", _vp), ("temperature", _vp),
         ("seed", C.c_uint64), ("round", C.c_uint64),
         ("accepted", _vp), ("next_token", _vp), ("resampled", _vp), ("a_rows", _vp),
+        ("target_ready", C.c_int32), ("reserved", C.c_int32),
     ]
 
 
@@ -1089,7 +1090,12 @@ class RoundRunner:
 
     def run(self, stream=None):
         self.run_draft(stream)
-        self.run_verify(stream)
+        # the target was there before the draft, and nothing stands between: its first rows are read under the scheduler
+        self.va.target_ready = int(self.ja is None)
+        try:
+            self.run_verify(stream)
+        finally:
+            self.va.target_ready = 0
 
     def run_draft(self, stream=None, step_ready=None):
         """The sampler and the scheduler: keep is known (on the device) when these have run.

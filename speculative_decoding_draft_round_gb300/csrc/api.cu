@@ -164,7 +164,11 @@ struct VerifyLayout {
 
 dspark_status check_verify(const dspark_verify_args* a)
 {
-    if (!a || a->struct_size != sizeof(dspark_verify_args)) return DSPARK_ERR_INVALID_ARGUMENT;
+    // struct_size without target_ready and reserved: 0
+    if (!a || (a->struct_size != sizeof(dspark_verify_args) && a->struct_size != offsetof(dspark_verify_args, target_ready)))
+        return DSPARK_ERR_INVALID_ARGUMENT;
+    if (a->struct_size == sizeof(dspark_verify_args) && ((a->target_ready | 1) != 1 || a->reserved != 0))
+        return DSPARK_ERR_INVALID_ARGUMENT;
     if (a->R < 1 || a->gamma_max < 1 || a->gamma_max > DSPARK_MAX_GAMMA) return DSPARK_ERR_INVALID_ARGUMENT;
     if (a->V < 1 || a->V > (1 << 24) || a->r < 1 || a->r > 1024) return DSPARK_ERR_INVALID_ARGUMENT;
     if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARGUMENT;
@@ -687,6 +691,7 @@ dspark_status dspark_verify(const dspark_verify_args* a, void* ws, size_t ws_byt
     p.tokens = a->tokens;
     p.draft_lse = a->draft_lse;
     p.a_rows = a->a_rows;
+    p.target_ready = a->struct_size == sizeof(dspark_verify_args) ? a->target_ready : 0;
     p.draft_logit = a->draft_logit;
     p.keep = a->keep;
     p.temperature = a->temperature;

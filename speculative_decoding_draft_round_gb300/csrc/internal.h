@@ -62,7 +62,7 @@ struct DraftStep {
 // Verification (dspark_verify).
 struct VerifyParams {
     int R, G, V, r, nblk;
-    int dtype, bias_first;
+    int dtype, bias_first, target_ready;
     const int32_t* gamma;
     const void* target;
     const void* U;

@@ -60,7 +60,8 @@ __device__ __forceinline__ void row_load8(const T* row, int V, int b0, int lane,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int v = (b0 + bb) * kNoiseBlock + j * 32 + qq * 8;
-        raw[j] = v < V ? __ldg(reinterpret_cast<const uint4*>(row + v)) : make_uint4(0, 0, 0, 0);
+        // a plain load: the rows may be written by a kernel that still runs when this one starts
+        raw[j] = v < V ? *reinterpret_cast<const uint4*>(row + v) : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -161,11 +162,6 @@ __device__ __forceinline__ float2 row_block_argmax(const T* row, int V, int b, i
     return make_float2(best.v, (float)best.i);   // indices below 2^24 are exact in fp32
 }
 
-// grid (vocabulary chunks, R): the CTA walks target rows 0..keep[r] of its request. Row 0 is
-// verified whatever keep is (rows 0..keep), and its statistics read only inputs: they are formed
-// before the dependency wait, while the scheduler runs, and stored after it (the workspace may
-// still be read by the kernel before this one); rows 1..keep follow once keep exists.
-//
 // a NaN or +inf logit leaves a NaN sum or an infinite maximum (-inf is a zero weight)
 __device__ __forceinline__ void check_row_stats(const VerifyParams& p, int b0, int lane, float2 st, bool& nonfinite)
 {
@@ -226,14 +222,23 @@ __device__ __forceinline__ void store_row_stats(const VerifyParams& p, int q, in
 }
 
 // A persistent grid walks items (request q, target row i, chunk c of 64 blocks), every warp taking
-// 8 blocks of the chunk. Row 0 is verified whatever keep is and reads only inputs: each CTA forms
-// up to kRowPre row-0 items before the dependency wait, while the scheduler runs, and stores them
-// after it (the workspace may still be read by the kernel before this one). Then the items of
-// rows 1..keep[q], numbered through the prefix sum of keep over the requests, are dealt to the
+// 8 blocks of the chunk. Row 0 is verified whatever keep is. Where the caller states that the target
+// was written before the kernel this one follows began (target_ready: that kernel is the scheduler),
+// each CTA forms up to kRowPre row-0 items before the dependency wait, while the scheduler runs, and
+// stores them after it (the workspace may still be read by the kernel before this one). Otherwise
+// that kernel may be the one that writes the target (its head, dspark_adjust_logits): nothing of it
+// is read before the wait, its row 0 is only asked of the L2, where what is written later lands too.
+// (A round of 128 requests, 16 drafts, V 151936: 0.518 ms with it, 0.525 without.)
+// Then the items of rows 1..keep[q], numbered through the prefix sum of keep over the requests, are dealt to the
 // CTAs in turn, so that a request with many admitted tokens spreads over the whole GPU instead of
 // walking its rows one after the other. In the bf16 vector path each warp issues the next item's
 // loads before it reduces the current one.
 constexpr int kRowPre = 16;
+// `bytes` (a multiple of 16) from a 16-byte boundary on into the L2
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
+}
 constexpr int kRowCtasPerSm = 4;   // 256 threads at 64 registers: four CTAs fill an SM's registers
 __device__ __forceinline__ int cdiv_dev(int a, int b) { return (a + b - 1) / b; }
 constexpr int kRowChunk = kRowWarps * kRowBlocksPerWarp;   // blocks per item
@@ -282,6 +287,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) verify_rows_kernel(VerifyParam
     const bool vec = (p.V % 8 == 0) && ((reinterpret_cast<uintptr_t>(p.target) & 15u) == 0);
     const int nch = cdiv_dev(p.nblk, kRowChunk);
     const int n0 = p.R * nch;   // row-0 items
+    const int pre = p.target_ready ? kRowPre : 0;   // of them, a CTA forms this many before the wait
     const int wb = warp * kRowBlocksPerWarp;
     bool nonfinite = false;
     uint4 rc[4], rn[4];
@@ -291,11 +297,18 @@ __global__ void __launch_bounds__(kRowWarps * 32) verify_rows_kernel(VerifyParam
     }
     __syncthreads();
 
-    // before the wait: row 0 of items blockIdx.x + k * gridDim.x, k < kRowPre (a warp whose 8
+    if (pre == 0 && vec && threadIdx.x < kRowPre) {
+        const int it = blockIdx.x + (int)threadIdx.x * gridDim.x, v = it % nch * kRowChunk * kNoiseBlock;
+        if (it < n0)
+            prefetch_l2(static_cast<const T*>(p.target) + (size_t)(it / nch) * (p.G + 1) * p.V + v,
+                        (uint32_t)(min(p.V - v, kRowChunk * kNoiseBlock) * sizeof(T)));
+    }
+
+    // before the wait: row 0 of items blockIdx.x + k * gridDim.x, k < pre (a warp whose 8
     // blocks lie past the vocabulary skips its part)
     const auto pre_item = [&](int k) {
         const int it = blockIdx.x + k * gridDim.x;
-        if (k >= kRowPre || it >= n0) return RowItem{-1, 0, 0};
+        if (k >= pre || it >= n0) return RowItem{-1, 0, 0};
         return RowItem{it / nch, 0, (it % nch) * kRowChunk + wb};
     };
     {
@@ -319,12 +332,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) verify_rows_kernel(VerifyParam
         }
     }
     if (threadIdx.x == 0)
-        for (int k = 0; k < kRowPre; ++k)
+        for (int k = 0; k < pre; ++k)
             if (blockIdx.x + k * gridDim.x >= n0) s_pre_q[k] = -1;
     __syncthreads();
     pdl_enter();   // keep comes from the scheduler
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_rej = 0;   // verify_decide counts from zero
-    for (int k = 0; k < kRowPre && s_pre_q[k] >= 0; ++k) {
+    for (int k = 0; k < pre && s_pre_q[k] >= 0; ++k) {
         const int b0 = ((blockIdx.x + k * gridDim.x) % nch) * kRowChunk + wb;
         if (b0 < p.nblk) {
             const size_t row = (size_t)s_pre_q[k] * (p.G + 1);   // row 0 of the request
@@ -352,12 +365,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) verify_rows_kernel(VerifyParam
     }
     if (threadIdx.x == kRowWarps * 32 - 1) s_pref[p.R] = base;
     __syncthreads();
-    const int n_left0 = max(0, n0 - kRowPre * (int)gridDim.x);   // row-0 items not formed before the wait
+    const int n_left0 = max(0, n0 - pre * (int)gridDim.x);   // row-0 items not formed before the wait
     const int n_items = n_left0 + s_pref[p.R] * nch;
     const auto post_item = [&](int it) {
         if (it >= n_items) return RowItem{-1, 0, 0};
         if (it < n_left0) {
-            const int j = kRowPre * gridDim.x + it;
+            const int j = pre * gridDim.x + it;
             return RowItem{j / nch, 0, (j % nch) * kRowChunk + wb};
         }
         const int rr = (it - n_left0) / nch;
