@@ -218,7 +218,8 @@ struct Touched {
     float bias;
 };
 
-// grid (stretches, requests)
+// grid (stretches, requests). Plain loads all over: the kernel before this one may write the table (dspark_seen_add), the
+// masks or the logits while this one's first CTAs already stand, which loads through the read-only path do not allow for.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
 {
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
             if constexpr (kVec) {
                 const int v = v0 + tid * kAdjEach;
                 if (v < p.V) {
-                    const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + v));
+                    const uint4 q = *reinterpret_cast<const uint4*>(row + v);
                     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int e = 0; e < kAdjEach; ++e) {
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
 #pragma unroll
                 for (int e = 0; e < kAdjEach; ++e) {
                     const int v = id_of<T, kVec>(v0, e);
-                    const uint32_t c = v < p.V ? (uint16_t)__ldg(row + v) : 0u;
+                    const uint32_t c = v < p.V ? (uint16_t)row[v] : 0u;
                     count[e] = c & 0x7FFF;
                     known |= (c != 0u ? 1u : 0u) << e;
                 }
@@ -370,13 +371,13 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
                 if (m >= 0) {
                     const uint32_t* bits = p.mask + m * p.mask_rs;
                     if constexpr (kVec) {
-                        allowed[u] = __ldg(reinterpret_cast<const uint8_t*>(bits) + (v0 + tid * kAdjEach) / 8);
+                        allowed[u] = reinterpret_cast<const uint8_t*>(bits)[(v0 + tid * kAdjEach) / 8];
                     } else {
                         allowed[u] = 0u;
 #pragma unroll
                         for (int e = 0; e < kAdjEach; ++e) {
                             const int v = id_of<T, kVec>(v0, e);
-                            if (v < p.V) allowed[u] |= ((__ldg(bits + v / 32) >> (v % 32)) & 1u) << e;
+                            if (v < p.V) allowed[u] |= ((bits[v / 32] >> (v % 32)) & 1u) << e;
                         }
                     }
                 }
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(AdjustParams p)
             const int j = i % rows;
             const Touched w = s_list[i / rows];
             const int m = s_mask[j];
-            if (m >= 0 && !((__ldg(p.mask + m * p.mask_rs + w.id / 32) >> (w.id % 32)) & 1u)) continue;
+            if (m >= 0 && !((p.mask[m * p.mask_rs + w.id / 32] >> (w.id % 32)) & 1u)) continue;
             int n = w.known & 0x3FFFFFFF;
             if (penal)
                 for (int k = 1; k <= j; ++k) n += s_token[k] == w.id;
