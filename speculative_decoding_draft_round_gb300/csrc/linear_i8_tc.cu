@@ -20,10 +20,13 @@
 // 1926 that the library's bf16 product reaches), 2176 x 4096 x 6144 93 us of 57 (3.8 tiles a pair), 128 x 4096 x 151936
 // 133 to 141 us of 98 (a step takes 900 cycles from copy to release, at any number of slots and widening warps, with x
 // shared between pairs or not; MMAs are 512 of them), 16 x 4096 x 6144 16.5 us (two launches).
-// The kernel is launched without programmatic dependence: with it, calls that fill every SM with pairs, made back to back
-// by the thousand, came to a stop (none did in 4000 without).
-// Every wait is bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT, the CTAs stop issuing, let
-// copies and MMAs land, free their tensor memory and return.
+// The kernel is launched without programmatic dependence. A first form that had it, that asked for tensor memory before
+// it knew that the other CTA of the pair had begun, and whose second CTA did not wait for the last arrivals, came to a
+// stop in calls made back to back; which of the three it was is not known. Now a pair asks for tensor memory when both
+// CTAs stand, and leaves when every arrival at its barriers has been made.
+// Waits at barriers in shared memory are bounded by the global timer; one that runs out records DSPARK_ERR_TIMEOUT, the
+// CTAs stop issuing, let copies and MMAs land, free their tensor memory and return. Not bounded are the waits inside
+// tcgen05.alloc and the barriers of a cluster, where a pair's CTAs wait for each other only.
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
@@ -160,6 +163,10 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// The same in two halves, without an order of anything written
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 constexpr unsigned long long kShortNs = 1000000;
 
@@ -308,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* s_scale = reinterpret_cast<float*>(s_tmem + 2);             // [4][kMostRows] of a tile's rows, each warp its own
     int* s_place = reinterpret_cast<int*>(s_scale + 4 * kMostRows);    // where they go
 
+    cluster_arrive();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank(), half = rank & 1u, first = rank & ~1u;
     const uint16_t both = (uint16_t)(3u << first);
@@ -326,6 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    __syncwarp();
+    cluster_wait();                      // the pair's other CTA stands: the allocation is one of both
     if (warp == 1) pair_alloc(s_tmem);
     tc5::fence_before();
     __syncthreads();
@@ -412,8 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             pair_commit(bar(kFin), both);
         }
-        // every MMA issued is done, and its arrivals here have been made, before the CTAs leave (also after an abort)
-        drain(bar(kFin), 0u);
     } else if (warp < kFirstOut) {
         // ---------------- widening: lane 32 (warp % 4) + lane, half `part` of the step
         const int part = (warp - kFirstWidener) >> 2;
@@ -465,6 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        // the last steps' releases too have arrived before the CTA leaves
+        for (int left = min(n, g.slots); left > 0 && ok; --left) {
+            ok = wait.warp(bar(kDone + back), back_phase);
+            if (++back == g.stages) {
+                back = 0;
+                back_phase ^= 1u;
+            }
+        }
     } else {
         // ---------------- sums out
         const int q = warp & 3;
@@ -508,6 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
+    if (warp == 1) {
+        // every MMA issued is done, and its arrivals here have been made, before the CTAs leave (also after an abort)
+        drain(bar(kFin), 0u);
+        __syncwarp();
+    }
     cluster_sync();
     if (g.split > 1 && tile0 < count) {
         // the pairs' sums: each adds up its share of the rows, in the order of the pairs
