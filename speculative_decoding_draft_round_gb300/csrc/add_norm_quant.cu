@@ -123,7 +123,7 @@ __device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b >
 // What the product s * g leaves beyond its fp32 rounding, where that is the row's largest
 __device__ __forceinline__ int remainder_at(float s, float g, uint32_t m, int lo)
 {
-    const float h = s * g, rest = fmaf(s, g, -h);
+    const float h = __fmul_rn(s, g), rest = __fmaf_rn(s, g, -h);
     return (__float_as_uint(h) & 0x7FFFFFFFu) == m ? max(lo, ordered(h < 0.f ? -rest : rest)) : lo;
 }
 
@@ -225,11 +225,15 @@ struct RowScales {
 // The code of a quotient f near a half, k + 1/2: the sign of 254 |p| - (2 k + 1) max|p|, whose heads are near enough to
 // leave each other exactly and whose remainders are exact. 64 bits only where that is next to nothing: on this chip a
 // division in 64 bits by a warp takes as long as its whole row (2176 rows of 4096 29 us with one for every such code).
+// Each rounding is spelt out: a product that the compiler fused with the difference would be exact there, and its
+// remainder counted twice.
 __device__ __noinline__ int settled(float s, float g, float f, const RowScales& r)
 {
-    const float h = s * g, rest = fmaf(s, g, -h), k = floorf(fabsf(f)), o = 2.f * k + 1.f;
-    const float a = 254.f * fabsf(h), b = o * r.m;
-    const float d = (a - b) + ((fmaf(254.f, fabsf(h), -a) - fmaf(o, r.m, -b)) + (254.f * (h < 0.f ? -rest : rest) - o * r.lo));
+    const float h = __fmul_rn(s, g), rest = __fmaf_rn(s, g, -h), k = floorf(fabsf(f)), o = 2.f * k + 1.f;
+    const float a = __fmul_rn(254.f, fabsf(h)), b = __fmul_rn(o, r.m);
+    const float heads = __fsub_rn(__fmaf_rn(254.f, fabsf(h), -a), __fmaf_rn(o, r.m, -b));
+    const float rests = __fsub_rn(__fmul_rn(254.f, h < 0.f ? -rest : rest), __fmul_rn(o, r.lo));
+    const float d = __fadd_rn(__fsub_rn(a, b), __fadd_rn(heads, rests));
     if (fabsf(d) <= 0x1.0p-34f * r.m) return code_in_64(s, g, (double)r.m + (double)r.lo);
     const int q = (int)k + (d > 0.f ? 1 : 0);
     return f < 0.f ? -q : q;

@@ -1,0 +1,63 @@
+"""add_norm_quant's codes next to a half against whole numbers of any length."""
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import speculative_decoding_draft_round_gb300 as ds
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _codes(s, g):
+    """The nearest whole number to 127 p / max|p| of a row, ties to even, in exact arithmetic."""
+    p = [Fraction(float(a)) * Fraction(float(b)) for a, b in zip(s, g)]
+    top = max(abs(x) for x in p)
+    return np.array([round(127 * x / top) for x in p])       # Fraction rounds ties to even
+
+
+def _quantised(s, g, bf16=False, norm=True):
+    x = torch.as_tensor(np.ascontiguousarray(s), device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    got = ds.add_norm_quant(x.bfloat16() if bf16 else x, gain=None if g is None else torch.as_tensor(g, device=DEV),
+                            norm=norm, eps=0.0, workspace=ws)
+    assert ds.check(ws) == 0
+    return got["codes"].cpu().numpy().astype(np.int64), got["scale"].cpu().numpy()
+
+
+@pytest.mark.parametrize("N", [256, 2048, 77])
+@pytest.mark.parametrize("gained", [False, True])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -60, 2.0 ** -110, 2.0 ** 100])
+def test_the_nearest_values_on_both_sides_of_a_half(N, gained, size):
+    """Quotients as near to k + 1/2 as fp32 elements allow, and an ulp beside that. (Sizes out of fp32's range for the
+    squares go through 64 bits.)"""
+    rng = np.random.default_rng(N)
+    T = 12
+    g = (1 + rng.random(N)).astype(np.float32) if gained else np.ones(N, np.float32)
+    s = np.empty((T, N), np.float32)
+    s[:, 0] = ((2 + rng.random(T)) * size).astype(np.float32)
+    top = s[:, 0].astype(np.float64) * float(g[0])
+    k = rng.integers(0, 126, (T, N - 1))
+    near = ((k + 0.5) / 127 * top[:, None] / g[1:]).astype(np.float32)
+    near = np.where(rng.random(near.shape) < .3, np.nextafter(near, np.float32(np.inf)), near)
+    s[:, 1:] = near * rng.choice([-1, 1], near.shape)
+    codes, _ = _quantised(s, g if gained else None)
+    for t in range(T):
+        assert np.array_equal(codes[t], _codes(s[t], g))
+
+
+@pytest.mark.parametrize("N", [64, 2048, 77])
+def test_rows_in_bf16_next_to_a_half(N):
+    """Elements of 8 bits, gains of 24: the gain brings the quotient next to the half."""
+    rng = np.random.default_rng(N)
+    for _ in range(6):
+        s = (1 + rng.integers(0, 128, N) / 128).astype(np.float32)
+        g = np.empty(N, np.float32)
+        g[0] = 2 + rng.random()
+        top = float(s[0]) * float(g[0])
+        g[1:] = (rng.integers(0, 120, N - 1) + 0.5) / 127 * top / s[1:]
+        codes, _ = _quantised(s[None], g, bf16=True)
+        assert np.array_equal(codes[0], _codes(s, g))
