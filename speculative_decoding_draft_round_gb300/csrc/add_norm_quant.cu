@@ -202,9 +202,14 @@ __device__ __forceinline__ double larger(double top, double h)
     return h <= top ? top : h < (double)INFINITY ? h : (double)INFINITY;
 }
 
+// 127 p has up to 55 bits and the division rounds, so the quotient tells k only; whether the code is k or k + 1 tells the
+// sign of 254 |p| - (2 k + 1) top = (256 |p| - (2 k + 1) top) - 2 |p|. Next to k + 1/2 the bracket is near 2 |p| and, as |p|
+// and top have 48 bits and top / |p| is at most 254, a whole number of at most 50 bits: the fused multiply-add is exact.
 __device__ __noinline__ int code_in_64(float s, float g, double top)
 {
-    return (int)rint(product(s, g) * 127.0 / top);
+    const double p = fabs(product(s, g)), k = floor(p * 127.0 / top), d = __fma_rn(-(2.0 * k + 1.0), top, 256.0 * p) - 2.0 * p;
+    const int q = (int)k, n = q + (d > 0.0 || (d == 0.0 && (q & 1)) ? 1 : 0);   // a tie goes to the even one
+    return product(s, g) < 0.0 ? -n : n;
 }
 
 // Whether a row's fp32 statistics can be used: what is formed from them neither overflows nor loses bits below the
@@ -234,8 +239,10 @@ __device__ __noinline__ int settled(float s, float g, float f, const RowScales& 
     const float heads = __fsub_rn(__fmaf_rn(254.f, fabsf(h), -a), __fmaf_rn(o, r.m, -b));
     const float rests = __fsub_rn(__fmul_rn(254.f, h < 0.f ? -rest : rest), __fmul_rn(o, r.lo));
     const float d = __fadd_rn(__fsub_rn(a, b), __fadd_rn(heads, rests));
-    if (fabsf(d) <= 0x1.0p-34f * r.m) return code_in_64(s, g, (double)r.m + (double)r.lo);
-    const int q = (int)k + (d > 0.f ? 1 : 0);
+    // heads alone (no gain): d has the sign of the difference itself, and is 0 for a tie, which goes to the even code
+    const bool exact = rest == 0.f && r.lo == 0.f;
+    if (fabsf(d) <= 0x1.0p-34f * r.m && !exact) return code_in_64(s, g, (double)r.m + (double)r.lo);
+    const int q = (int)k + (d > 0.f || (d == 0.f && ((int)k & 1)) ? 1 : 0);
     return f < 0.f ? -q : q;
 }
 
@@ -250,10 +257,18 @@ __device__ __forceinline__ void finish(const NormParams& p, const RowStats& st, 
     k.lo = 0.f;
 }
 
+// CTAs an SM that the registers have to leave room for: the branches in 64 bits, which hardly any row takes, would cost
+// one otherwise (32749 rows of 5120 in bf16 309 us instead of 236).
+template <typename T, int NT, int V>
+constexpr int kCtas = NT == 32    ? (V == 1 ? 4 : V < 4 ? 3 : 2)
+                      : NT == 128 ? 7
+                      : NT == 256 ? 3
+                      : NT == 512 && V == 2 && sizeof(T) == 2 ? 2 : 1;
+
 // N a multiple of 8, rows and outputs on 16-byte (codes on 8-byte) boundaries: V pieces of 8 elements a thread, kept in
 // registers. NT = 32: a row is a warp, eight to a CTA.
 template <typename T, int NT, int V>
-__global__ void __launch_bounds__(NT == 32 ? 256 : NT) norm_vec_kernel(NormParams p)
+__global__ void __launch_bounds__(NT == 32 ? 256 : NT, kCtas<T, NT, V>) norm_vec_kernel(NormParams p)
 {
     constexpr int kRows = NT == 32 ? 8 : 1, kWarps = NT / 32;
     __shared__ float s_sums[kWarps];

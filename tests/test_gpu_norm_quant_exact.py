@@ -61,3 +61,24 @@ def test_rows_in_bf16_next_to_a_half(N):
         g[1:] = (rng.integers(0, 120, N - 1) + 0.5) / 127 * top / s[1:]
         codes, _ = _quantised(s[None], g, bf16=True)
         assert np.array_equal(codes[0], _codes(s, g))
+
+
+# s, g, the largest element and its gain, all of 24 bits: 127 s g / 128 and the product of the others are whole numbers and
+# 1/128 apart, so that the quotient is next to 1/2 by less than 64 bits of floating point hold
+NEAR = [(15652751, 9918353, 12350715, 12471879), (16756431, 9875153, 12658865, 12969533),
+        (11865523, 14839045, 12684132, 13772914), (14687705, 13442327, 13376829, 14644312),
+        (15280753, 11557615, 11426133, 15335836), (13947433, 14094233, 13558418, 14385351)]
+
+
+@pytest.mark.parametrize("N", [64, 2048, 33])
+@pytest.mark.parametrize("size", [2.0 ** -24, 2.0 ** -90])
+def test_quotients_that_64_bits_do_not_tell_from_a_half(N, size):
+    for a, b, c, d in NEAR:
+        s, g = np.zeros(N, np.float32), np.ones(N, np.float32)
+        s[:4] = [c * size, a / 256 * size, -a / 256 * size, c * size / 3]
+        g[:4] = [d * 2.0 ** -24, b * 2.0 ** -24, b * 2.0 ** -24, 1.0]
+        want = _codes(s, g)
+        assert abs(want[1]) == int(127 * a * b > 128 * c * d)
+        for sign in (1, -1):
+            codes, _ = _quantised((sign * s)[None], g)
+            assert np.array_equal(codes[0], sign * want)
