@@ -251,7 +251,8 @@ __device__ __forceinline__ void finish(const NormParams& p, const RowStats& st, 
 {
     const float m = __uint_as_float(st.m);
     k.inv = p.norm ? 1.f / sqrtf(st.sum / (float)p.N + p.eps) : 1.f;
-    k.scale = m * k.inv / 127.f;
+    const float top = m * k.inv;
+    k.scale = top <= FLT_MAX ? top / 127.f : m * (k.inv / 127.f);   // the largest |y| may be past fp32's end and this not
     k.per = 127.f / m;
     k.m = m;
     k.lo = 0.f;

@@ -1,4 +1,4 @@
-"""add_norm_quant's codes next to a half against whole numbers of any length."""
+"""add_norm_quant's codes next to a half and its scales next to fp32's end, against whole numbers of any length."""
 from fractions import Fraction
 
 import numpy as np
@@ -82,3 +82,19 @@ def test_quotients_that_64_bits_do_not_tell_from_a_half(N, size):
         for sign in (1, -1):
             codes, _ = _quantised((sign * s)[None], g)
             assert np.array_equal(codes[0], sign * want)
+
+
+@pytest.mark.parametrize("N", [1024, 8192, 999])
+def test_scales_whose_largest_value_leaves_fp32(N):
+    """The largest |y| is past fp32's end and its 127th part is not."""
+    s, g = np.zeros((2, N), np.float32), np.ones(N, np.float32)
+    s[0, 3], s[1, 3], s[1, 5] = 1e-9, -1e-9, 3e-10
+    g[3] = 3e38
+    codes, scale = _quantised(s, g)
+    for t in range(2):
+        assert np.array_equal(codes[t], _codes(s[t], g))
+        p = s[t].astype(np.float64) * g
+        want = np.abs(p).max() / np.sqrt((s[t].astype(np.float64) ** 2).mean()) / 127
+        assert want > 2.0 ** 128 / 127 and want < 2.0 ** 128
+        # the sum's and the other steps' roundings: fewer than 2^7 of 2^-24
+        assert abs(scale[t] - want) <= 2.0 ** -17 * want
