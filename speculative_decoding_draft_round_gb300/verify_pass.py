@@ -18,10 +18,13 @@ query looks past its own position. ToyTarget and main() below run rounds of a sm
 """
 from __future__ import annotations
 
+import ctypes as C
+
 import torch
 
-from . import (_launch, _on, add_norm_quant, assemble, assemble_args, cache_append, cache_append_args, cache_attend_args,
-               cache_pool, check, lib, linear_i8, qk_norm_rope, qk_norm_rope_args, rope_frequencies, workspace_bytes)
+from . import (PATH_AUTO, LinearI8Args, _dtype_code, _launch, _on, add_norm_quant, assemble, assemble_args, cache_append,
+               cache_append_args, cache_attend_args, cache_pool, check, lib, linear_i8, qk_norm_rope, qk_norm_rope_args,
+               rope_frequencies, workspace_bytes)
 
 
 class VerifyPass:
@@ -138,7 +141,8 @@ class VerifyPass:
 
 class ToyTarget:
     """A small random target model around VerifyPass: embedding, layers of attention with a residual, logits. With
-    eight_bit the weights are held in 8 bits and every layer norms and quantises its rows (add_norm_quant, linear_i8)."""
+    eight_bit the weights are held in 8 bits and every layer norms and quantises its rows (add_norm_quant, linear_i8); these
+    calls share a workspace, so that all passes go on one stream, and check() reads what they have recorded."""
 
     def __init__(self, vp, V, width, *, seed=0, eight_bit=False):
         g = torch.Generator(device=vp.qkv.device).manual_seed(seed)
@@ -149,26 +153,51 @@ class ToyTarget:
         self.w_qkv = [draw(width, vp.qkv.shape[1]) for _ in range(vp.layers)]
         self.w_out = [draw(vp.Hq * vp.D, width) for _ in range(vp.layers)]
         self.w_logits = draw(width, V)
+        # the last one is in use; wider ones follow for longer prompts, and captured passes keep theirs
+        self.works = [torch.zeros(256, dtype=torch.uint8, device=dev)]
         if eight_bit:
             self.w_qkv, self.w_out = [self._codes(w) for w in self.w_qkv], [self._codes(w) for w in self.w_out]
             self.w_logits = self._codes(self.w_logits)
+            self._room(vp.T)
 
-    @staticmethod
-    def _codes(w):
+    def _codes(self, w):
         """A weight [in][out] as codes [out][in] with a scale for each channel."""
-        q = add_norm_quant(w.t().contiguous(), norm=False)
+        q = self._norm(w.t().contiguous(), norm=False)
         return q["codes"], q["scale"]
+
+    def _room(self, T):
+        """Workspace for the widest product of T rows."""
+        need = 0
+        for w, scale in (*self.w_qkv, *self.w_out, self.w_logits):
+            p, (N, K) = w.data_ptr(), w.shape
+            need = max(need, workspace_bytes("linear_i8", LinearI8Args(
+                C.sizeof(LinearI8Args), T, K, N, _dtype_code(self.vp.qkv), PATH_AUTO, T, 0, p, p, p, scale.data_ptr(), None,
+                None, None, p, K, w.stride(0), N)))
+        if need > self.works[-1].numel():
+            work = torch.empty(need, dtype=torch.uint8, device=w.device)
+            work[:256].zero_()
+            self.works.append(work)
+
+    def check(self, stream=None) -> int:
+        """The first status that the norms and 8-bit products have recorded since the last check."""
+        return next((c for c in [check(w, stream) for w in self.works] if c), 0)
+
+    def _norm(self, x, **kw):
+        return add_norm_quant(x, workspace=self.works[-1], **kw)
+
+    def _product(self, codes, scale, w, **kw):
+        return linear_i8(codes, scale, *w, workspace=self.works[-1], **kw)["out"]
 
     def _eight_bit(self, x, layer, n_rows=None):
         """x [T][width] through all layers; layer(l, codes, scale) is layer l's attention of the rows. Returns the codes
         and scales of the last norm."""
         residual = None
         for l in range(self.vp.layers):
-            q = add_norm_quant(x, residual=residual, n_rows=n_rows)
+            q = self._norm(x, residual=residual, n_rows=n_rows)
             residual = x if residual is None else q["sum"]
-            a = add_norm_quant(layer(l, q["codes"], q["scale"]).flatten(1), norm=False, n_rows=n_rows)
-            x = linear_i8(a["codes"], a["scale"], *self.w_out[l], dtype=x.dtype, n_rows=n_rows)["out"]
-        q = add_norm_quant(x, residual=residual, n_rows=n_rows)
+            a = self._norm(layer(l, q["codes"], q["scale"]).flatten(1), norm=False, n_rows=n_rows)
+            x = self._product(a["codes"], a["scale"], self.w_out[l], dtype=x.dtype, n_rows=n_rows)
+        q = self._norm(x, residual=residual, n_rows=n_rows)
         return q["codes"], q["scale"]
 
     def prompt(self, tokens, lengths):
@@ -183,7 +212,8 @@ class ToyTarget:
         x = self.embed[tokens.long()]
         at = (request, position, offsets, max(lengths))
         if self.eight_bit:
-            self._eight_bit(x, lambda l, c, s: vp.prompt(l, linear_i8(c, s, *self.w_qkv[l], dtype=x.dtype)["out"], *at))
+            self._room(len(x))
+            self._eight_bit(x, lambda l, c, s: vp.prompt(l, self._product(c, s, self.w_qkv[l], dtype=x.dtype), *at))
         else:
             for l in range(vp.layers):
                 x = x + vp.prompt(l, x @ self.w_qkv[l], *at).flatten(1) @ self.w_out[l]
@@ -198,12 +228,12 @@ class ToyTarget:
             rows = b["offsets"][-1:]
 
             def layer(l, codes, scale):
-                linear_i8(codes, scale, *self.w_qkv[l], n_rows=rows, out={"out": vp.qkv})
+                self._product(codes, scale, self.w_qkv[l], n_rows=rows, out={"out": vp.qkv})
                 return vp.layer(l)
 
             # straight to their places; padding has negative ones
             place = b["flat_request"] * (vp.gamma_max + 1) + b["flat_position"]
-            linear_i8(*self._eight_bit(x, layer, rows), *self.w_logits, out_row=place, n_rows=rows, out={"out": out})
+            self._product(*self._eight_bit(x, layer, rows), self.w_logits, out_row=place, n_rows=rows, out={"out": out})
             return
         for l in range(vp.layers):
             torch.mm(x, self.w_qkv[l], out=vp.qkv)
@@ -229,7 +259,8 @@ def main(eight_bit=False):
     if eight_bit:
         seen = seen_table(R, V)
         words = torch.nn.utils.rnn.pad_sequence(prompts.to(torch.int32).split(lengths), batch_first=True)
-        seen_add(seen, words, V=V, n=torch.tensor(lengths, dtype=torch.int32, device="cuda"), prompt=True)
+        added = seen_add(seen, words, V=V, n=torch.tensor(lengths, dtype=torch.int32, device="cuda"), prompt=True)
+        assert check(added["workspace"]) == 0
         adjust = dict(seen=seen, repetition=torch.full((R,), 1.2, device="cuda"))
     runner = RoundRunner(rnd, adjust=adjust)
     for i in range(rounds):
@@ -241,7 +272,7 @@ def main(eight_bit=False):
         out = runner.results()
         vp.advance(out["accepted"])
         rnd.anchor.copy_(out["next_token"])
-        assert runner.check() == 0 and vp.check() == 0
+        assert runner.check() == 0 and vp.check() == 0 and target.check() == 0
         print("round %d: %d tokens admitted, %d accepted, longest context %d" % (
             i, int(out["keep"].sum()), int(out["accepted"].sum()), int(vp.ctx_len.max())))
 
