@@ -617,6 +617,8 @@ dspark_status dspark_seen_add(const dspark_seen_add_args* args, void* workspace,
  * Biases: entries bias_offsets[r] .. bias_offsets[r+1]-1 of bias_token and bias_value; entries of one token add up in
  * their order. Mask rows: mask_row[r][j] < 0 allows all. Bit v % 32 of word v / 32 allows token v. What a mask hides is
  * never looked at; other infinities and NaN pass through. Rows j > keep[r] are not read, and stay as they were in out.
+ * A mask that leaves nothing makes its row -infinity throughout: dspark_verify then puts out token 0 for it (and records
+ * DSPARK_ERR_DEVICE_INPUT where the request samples).
  * out may be logits (in place: what does not change is not written) but must not overlap it otherwise.
  * Recorded (DSPARK_ERR_DEVICE_INPUT): a repetition that is not above zero and finite (1 is taken), a penalty that is
  * not finite (0 is taken), keep outside 0 .. S-1 (clamped), bias offsets that decrease or pass n_bias (no biases), a

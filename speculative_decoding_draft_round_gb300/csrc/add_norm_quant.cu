@@ -9,9 +9,10 @@
 // from the exact products s * gain (48 bits) and the exact largest of them (fp32 head and remainder). Rows whose
 // products or squares leave fp32's range, and those with a NaN or an infinity, are done in 64 bits altogether.
 //
-// The bytes bound it: a row is read once into registers and every output leaves from there. Measured: 32749 rows of 5120 in
-// bf16 with a residual (1341 MB) 236 us, 198 at the copy's rate; with codes 2176 rows of 4096 about 20 us of 9, where
-// instructions (some 40 an element) and the two barriers a row count. A warp a row up to 1024 wide; above, two or three
+// The bytes bound it: a row is read once into registers (above 12288 wide part of it goes through local memory) and every
+// output leaves from there. Measured, in bf16 with a residual: 32749 rows of 5120 to values (1341 MB) 235 us, 201 at the
+// copy's rate; to codes 2176 rows of 4096 16 us in a row (inputs in the L2), 9 at the copy's rate, where instructions (some
+// 40 an element) and the two barriers a row count, and 16 rows 3 us. A warp a row up to 1024 wide; above, two or three
 // pieces of 8 a thread (four took 26 us for those 2176 rows: fewer warps wait for the barriers).
 #include <float.h>
 

@@ -16,10 +16,12 @@
 // lanes and half of the step each, into a slot of tensor memory), 10-13 take finished sums out (one of two accumulators).
 // Tiles that would leave SMs idle are split along K over the pairs of a cluster, which add up their sums through
 // distributed shared memory in a fixed order.
-// Measured, layout included: 6007 x 8192 x 8192 rows x K x channels 459 to 497 us (the product alone 435, 1850 TFLOP/s of
-// 1926 that the library's bf16 product reaches), 2176 x 4096 x 6144 93 us of 57 (3.8 tiles a pair), 128 x 4096 x 151936
-// 133 to 141 us of 98 (a step takes 900 cycles from copy to release, at any number of slots and widening warps, with x
-// shared between pairs or not; MMAs are 512 of them), 16 x 4096 x 6144 16.5 us (two launches).
+// Measured, layout included, rows x K x channels, calls from Python in a row (replayed from a graph): 6007 x 8192 x 8192
+// 482 to 497 us (474) of 416 at the library's bf16 rate, 2176 x 4096 x 6144 92 to 94 us (91) of 57, 128 x 4096 x 151936
+// 139 us (130) of 99, 16 x 4096 x 6144 16.5 to 17.5 us (14.5, two launches). A tile's way out costs much: four full tiles a
+// pair (1536 x K x 9728) take 70 us at K = 1024, 78 at 2048, 91 at 4096, 142 at 8192. For few rows a step takes 900 cycles
+// from copy to release where its MMAs are 512, at any number of slots and widening warps, with x shared between pairs or
+// not; which limit that is has not been found.
 // The kernel is launched without programmatic dependence. A first form that had it, that asked for tensor memory before
 // it knew that the other CTA of the pair had begun, and whose second CTA did not wait for the last arrivals, came to a
 // stop in calls made back to back; which of the three it was is not known. Now a pair asks for tensor memory when both

@@ -4,7 +4,8 @@
 // A request's rows share its row of the table and its biases: a CTA takes stretches of the vocabulary of one request, lists
 // the ids of a stretch that something bears on, runs the rows past as they are, and goes through the list afterwards, a
 // thread an id and row. (Adjusted in the threads that load them, those ids held up whole warps: 128 x 17 x 151936 in bf16
-// took 236 us, 176 now, of 109 at the copy's rate; 28 warps an SM wait for loads.) In place, only 16-byte pieces that a
+// took 236 us, 167 to 177 now, of 111 at the copy's rate; 28 warps an SM wait for loads. In place it takes 157 us: the time is
+// less the rows' than that of the CTAs with long lists, for text's ids crowd at the vocabulary's low end.) In place, only 16-byte pieces that a
 // mask changes and listed ids are written, and pieces that a mask hides whole are written without being read.
 #include <float.h>
 

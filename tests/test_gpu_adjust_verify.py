@@ -115,3 +115,27 @@ def test_rounds_that_adjust_are_the_same_in_a_row():
 
     for a, b in zip(rounds(True), rounds(False)):
         assert all(np.array_equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("V", [600, 5003])
+def test_masks_that_leave_nothing(V):
+    """Token 0 comes out, recorded where the request samples; the other requests are not touched by it."""
+    R, G = 8, 3
+    for greedy in (False, True):
+        got = []
+        for empty in (False, True):
+            rnd = wl.make_round("nothing_left", R, G, V, 32, 48, "bf16", seed=4, device=DEV, u_std=1.0)
+            rnd.temperature.fill_(0.0 if greedy else 1.0)
+            mask = torch.zeros((2, -(-V // 32)), dtype=torch.int32, device=DEV)
+            mask[1] = -1
+            state = torch.ones((R, G + 1), dtype=torch.int32, device=DEV)
+            if empty:
+                state[0], state[3, 1:] = 0, 0
+            runner = ds.RoundRunner(rnd, adjust=dict(mask=mask, mask_row=state))
+            runner.run()
+            assert runner.check() == (ds.ERR_DEVICE_INPUT if empty and not greedy else 0)
+            got.append([runner.results()[k].cpu().numpy().copy() for k in ("accepted", "next_token")])
+        (_, plain), (accepted, masked) = got
+        assert accepted[0] == 0 and masked[0] == 0
+        others = [1, 2, 4, 5, 6, 7]
+        assert np.array_equal(plain[others], masked[others]) and 0 <= masked[3] < V
