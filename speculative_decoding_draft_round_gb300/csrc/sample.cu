@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kNoiseBlock) draft_stats_simt_kernel(DraftStep
         float x = -INFINITY;
         if (v < p.V) x = (ld(U, ((size_t)q * p.G + p.k) * p.V + v) + acc[j]) * req[j].scale;
         const float m = block_max<kNoiseBlock>(x, red);
-        const float e = v < p.V ? exp2f(x - m) : 0.f;
+        const float e = x == -INFINITY ? 0.f : exp2f(x - m);   // also where the whole block has no weight
         const float s = block_sum<kNoiseBlock>(e, red);
         if (t == 0) {
             // a NaN or +inf logit leaves a NaN sum or an infinite maximum (-inf is a zero weight)

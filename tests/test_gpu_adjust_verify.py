@@ -139,3 +139,33 @@ def test_masks_that_leave_nothing(V):
         assert accepted[0] == 0 and masked[0] == 0
         others = [1, 2, 4, 5, 6, 7]
         assert np.array_equal(plain[others], masked[others]) and 0 <= masked[3] < V
+
+
+@pytest.mark.parametrize("path", [ds.PATH_AUTO, ds.PATH_CUDA_CORE, ds.PATH_RESIDENT])
+def test_a_draft_right_behind_the_adjustment_of_its_logits(path):
+    """The backbone's logits adjusted in place and drafted from at once, and with the adjustment's end awaited."""
+    R, G, V = 64, 4, 65536
+    rnd = wl.make_round("adjust_draft", R, G, V, 256, 96, "bf16", seed=6, device=DEV, u_std=1.0)
+    given = rnd.U.clone()
+    allowed = np.zeros((1, V), bool)
+    allowed[0, V - 200:V - 50] = True
+    mask = torch.as_tensor(ref.pack_bits(allowed), device=DEV)
+    state = torch.zeros((R, G), dtype=torch.int32, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    runner = ds.RoundRunner(rnd, path=path)
+    got = []
+    for apart in (True, False):
+        for i in range(3):
+            runner.set_round(i)
+            rnd.U.copy_(given)
+            torch.cuda.synchronize()
+            ds.adjust_logits(rnd.U, mask=mask, mask_row=state, out={"out": rnd.U}, workspace=ws)
+            if apart:
+                torch.cuda.synchronize()
+            runner.run_draft()
+            torch.cuda.synchronize()
+            got.append({k: runner.sout[k].cpu().numpy().copy() for k in ("tokens", "draft_lse", "draft_logit", "surv")})
+    assert runner.check() == 0 and ds.check(ws) == 0
+    for a, b in zip(got[:3], got[3:]):
+        assert all(np.array_equal(a[k], b[k]) for k in a)
+        assert np.all((b["tokens"] >= V - 200) & (b["tokens"] < V - 50))
